@@ -16,8 +16,9 @@ from ._build import LIB, build  # noqa: F401
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_BOUNDS, \
     MOE_ERR_NOMEM = range(8)
-MOE_F32, MOE_BF16 = 0, 1
-MOE_W_BF16, MOE_W_Q4G64 = 0, 1
+MOE_F32, MOE_BF16, MOE_MX8 = 0, 1, 2
+MOE_W_BF16, MOE_W_Q4G64, MOE_W_MX8 = 0, 1, 2
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_GEMM = 0, 1, 2
 MOE_ROUTER_AUTO, MOE_ROUTER_SIMT, MOE_ROUTER_TENSOR = 0, 1, 2
 (MOE_K_ROUTER, MOE_K_SELECT, MOE_K_GROUP, MOE_K_GEMV_GATE_UP, MOE_K_GEMV_DOWN, MOE_K_GEMM_GATE_UP, MOE_K_GEMM_DOWN,
@@ -36,6 +37,10 @@ class moe_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("d", "n_experts", "inter", "shared_inter", "top_k", "max_tokens",
                                             "x_dtype", "has_router_bias", "has_shared", "bias_select_only",
                                             "shared_gate", "weight_format")]
+
+
+class moe_ffn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("d", "inter", "max_tokens", "activation", "weight_format", "training")]
 
 
 _lib = None
@@ -73,6 +78,23 @@ def lib() -> ctypes.CDLL:
         L.moe_decode_noalloc.restype = I
         L.moe_last_routing.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(I), ctypes.POINTER(I), P]
         L.moe_last_routing.restype = I
+        L.moe_add_norm.argtypes = [P, I, P, I, P, I, I, I, F, P, P, I, P, P]
+        L.moe_add_norm_backward.argtypes = [P, P, P, P, I, I, I, I, F, P, P, P, P]
+        L.moe_quantize_mx.argtypes = [P, I, I, I, P, P, P]
+        L.moe_ffn_init.argtypes = [ctypes.POINTER(moe_ffn_config), ctypes.POINTER(P)]
+        L.moe_ffn_forward.argtypes = [P, P, P, I, P, P, P, P, P, P, P]
+        L.moe_ffn_backward.argtypes = [P, P, P, I, P, P, P, P, P, P, P]
+        L.moe_ffn_status.argtypes = [P]
+        for f in ("moe_add_norm", "moe_add_norm_backward", "moe_quantize_mx", "moe_ffn_init", "moe_ffn_forward",
+                  "moe_ffn_backward", "moe_ffn_status"):
+            getattr(L, f).restype = I
+        L.moe_add_norm_workspace.argtypes = [I]
+        L.moe_mx_scale_bytes.argtypes = [I, I]
+        L.moe_ffn_launch_count.argtypes = [P]
+        for f in ("moe_add_norm_workspace", "moe_mx_scale_bytes", "moe_ffn_launch_count"):
+            getattr(L, f).restype = ctypes.c_longlong
+        L.moe_ffn_destroy.argtypes = [P]
+        L.moe_ffn_destroy.restype = None
         L.moe_status.argtypes = [P]
         L.moe_strerror.argtypes = [I]
         L.moe_strerror.restype = ctypes.c_char_p
@@ -81,7 +103,6 @@ def lib() -> ctypes.CDLL:
         for f in ("moe_init", "moe_route", "moe_forward", "moe_set_path", "moe_set_router", "moe_set_spin_limit",
                   "moe_status"):
             getattr(L, f).restype = I
-        del F
         _lib = L
     return _lib
 
@@ -310,6 +331,239 @@ class MoeLayer:
     def close(self):
         if self.ctx:
             moe_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- feed-forward block and its norm
+def _dtype_code(t, name):
+    import torch
+
+    known = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    if t.dtype not in known:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return known[t.dtype]
+
+
+def _need_shape(t, name, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def moe_mx_scale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the scales of an mx8 matrix (MOE_MX8, see moe.h)."""
+    return lib().moe_mx_scale_bytes(rows, cols)
+
+
+def _mx_pair(pair, name, rows, cols):
+    """(codes, scales) of an mx8 matrix, checked."""
+    import torch
+
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+        raise ValueError(f"{name} must be a pair (codes, scales)")
+    codes, scales = pair
+    _need_cuda(codes, f"{name} codes")
+    _need_cuda(scales, f"{name} scales")
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"{name} codes must be float8_e4m3fn or uint8, got {codes.dtype}")
+    if scales.element_size() != 1:
+        raise ValueError(f"{name} scales must be bytes, got {scales.dtype}")
+    _need_shape(codes, f"{name} codes", (rows, cols))
+    if scales.numel() != moe_mx_scale_bytes(rows, cols):
+        raise ValueError(f"{name} scales must be {moe_mx_scale_bytes(rows, cols)} bytes, got {scales.numel()}")
+    return codes, scales
+
+
+def _mx_empty(rows, cols, device):
+    import torch
+
+    return (torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(moe_mx_scale_bytes(rows, cols), dtype=torch.uint8, device=device))
+
+
+def moe_quantize_mx(v, codes=None, scales=None, stream=None):
+    """Round a float32 or bfloat16 matrix to mx8: (codes, scales); see moe.h."""
+    _need_cuda(v, "v")
+    rows, cols = v.shape
+    dt = _dtype_code(v, "v")
+    if codes is None or scales is None:
+        codes, scales = _mx_empty(rows, cols, v.device)
+    _mx_pair((codes, scales), "output", rows, cols)
+    _check(lib().moe_quantize_mx(_ptr(v), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(stream)),
+           "moe_quantize_mx")
+    return codes, scales
+
+
+def moe_add_norm(x, residual, weight, eps, s_out, y, y_scales=None, stream=None) -> None:
+    """See moe.h.  ``y`` is float32, bfloat16, or float8_e4m3fn codes with ``y_scales``."""
+    import torch
+
+    T, d = x.shape
+    for name, t in (("x", x), ("residual", residual), ("weight", weight), ("s_out", s_out), ("y", y),
+                    ("y_scales", y_scales)):
+        _need_cuda(t, name)
+    for name, t in (("residual", residual), ("s_out", s_out), ("y", y)):
+        _need_shape(t, name, (T, d))
+    _need_shape(weight, "weight", (d,))
+    if residual is not None and s_out is not None and residual.dtype != s_out.dtype:
+        raise ValueError(f"s_out must be {residual.dtype}, got {s_out.dtype}")
+    stream_t = residual if residual is not None else s_out
+    s_dtype = MOE_F32 if stream_t is None else _dtype_code(stream_t, "residual")
+    if y.dtype == torch.float8_e4m3fn:
+        y_dtype = MOE_MX8
+        if y_scales is not None and d % 32 == 0:
+            _mx_pair((y, y_scales), "y", T, d)
+    else:
+        y_dtype = _dtype_code(y, "y")
+    _check(lib().moe_add_norm(_ptr(x), _dtype_code(x, "x"), _ptr(residual), s_dtype, _ptr(weight),
+                              _dtype_code(weight, "weight"), T, d, eps, _ptr(s_out), _ptr(y), y_dtype, _ptr(y_scales),
+                              _stream(stream)), "moe_add_norm")
+
+
+def moe_add_norm_backward(s, weight, dy, ds, eps, dx, dweight, workspace, stream=None) -> None:
+    T, d = s.shape
+    for name, t in (("s", s), ("dy", dy), ("ds", ds), ("dx", dx)):
+        _need_cuda(t, name, s.dtype)
+        _need_shape(t, name, (T, d))
+    for name, t in (("weight", weight), ("dweight", dweight)):
+        _need_cuda(t, name, weight.dtype)
+        _need_shape(t, name, (d,))
+    _need_cuda(workspace, "workspace")
+    if workspace is not None and workspace.numel() * workspace.element_size() < lib().moe_add_norm_workspace(d):
+        raise ValueError("workspace is smaller than moe_add_norm_workspace(d) bytes")
+    _check(lib().moe_add_norm_backward(_ptr(s), _ptr(weight), _ptr(dy), _ptr(ds), _dtype_code(s, "s"),
+                                       _dtype_code(weight, "weight"), T, d, eps, _ptr(dx), _ptr(dweight),
+                                       _ptr(workspace), _stream(stream)), "moe_add_norm_backward")
+
+
+class AddNorm:
+    """The norm of rows of width ``d`` with the residual's addition; keeps the
+    workspace of the backward pass (two backward calls on one object must not
+    overlap in time)."""
+
+    def __init__(self, d, eps=1e-6):
+        self.d = d
+        self.eps = float(eps)
+        self._workspace = None
+
+    def forward(self, x, residual, weight, y_dtype=MOE_BF16, s_out=None, stream=None):
+        """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
+        in the residual's dtype (x's without a residual)."""
+        import torch
+
+        if y_dtype not in (MOE_F32, MOE_BF16, MOE_MX8):
+            raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
+        _need_shape(x, "x", (x.shape[0], self.d))
+        if s_out is None:
+            s_out = torch.empty_like(x if residual is None else residual)
+        if y_dtype == MOE_MX8:
+            y, scales = _mx_empty(x.shape[0], self.d, x.device)
+        else:
+            y = torch.empty(x.shape, dtype=torch.float32 if y_dtype == MOE_F32 else torch.bfloat16, device=x.device)
+            scales = None
+        moe_add_norm(x, residual, weight, self.eps, s_out, y, scales, stream)
+        return ((y, scales) if y_dtype == MOE_MX8 else y), s_out
+
+    def backward(self, s, weight, dy, ds=None, stream=None):
+        """(dx, dweight); dx is the gradient of x and of the residual alike."""
+        import torch
+
+        _need_shape(s, "s", (s.shape[0], self.d))
+        if self._workspace is None or self._workspace.device != s.device:
+            self._workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
+        dx, dweight = torch.empty_like(s), torch.empty_like(weight)
+        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, self._workspace, stream)
+        return dx, dweight
+
+
+def moe_ffn_init(d, inter, max_tokens, activation=MOE_ACT_SILU, weight_format=MOE_W_BF16,
+                 training=False) -> ctypes.c_void_p:
+    cfg = moe_ffn_config(d, inter, max_tokens, activation, weight_format, int(training))
+    h = ctypes.c_void_p()
+    _check(lib().moe_ffn_init(ctypes.byref(cfg), ctypes.byref(h)), "moe_ffn_init")
+    return h
+
+
+def moe_ffn_destroy(ctx) -> None:
+    lib().moe_ffn_destroy(ctx)
+
+
+def moe_ffn_status(ctx) -> int:
+    return lib().moe_ffn_status(ctx)
+
+
+def moe_ffn_launch_count(ctx) -> int:
+    return lib().moe_ffn_launch_count(ctx)
+
+
+class GatedFfn:
+    """Owns one context of the dense gated feed-forward block (moe_ffn_*, see moe.h);
+    with MOE_W_MX8 x and the weights are pairs (codes, scales)."""
+
+    def __init__(self, d, inter, max_tokens, *, activation=MOE_ACT_SILU, weight_format=MOE_W_BF16, training=False):
+        self.ctx = None
+        self.d, self.inter, self.mx = d, inter, weight_format == MOE_W_MX8
+        self.ctx = moe_ffn_init(d, inter, max_tokens, activation, weight_format, training)
+
+    def _operand(self, t, name, rows, cols):
+        import torch
+
+        if self.mx:
+            return _mx_pair(t, name, rows, cols)
+        _need_cuda(t, name, torch.bfloat16)
+        _need_shape(t, name, (rows, cols))
+        return t, None
+
+    def forward(self, x, gate_up, down, y=None, pre=None, save=False, stream=None):
+        """y, or (y, pre) with ``save`` (pre: the pre-activations that ``backward`` needs)."""
+        import torch
+
+        rows = x[0] if isinstance(x, (tuple, list)) else x
+        T = rows.shape[0]
+        x, xs = self._operand(x, "x", T, self.d)
+        gu, gus = self._operand(gate_up, "gate_up", 2 * self.inter, self.d)
+        dn, dns = self._operand(down, "down", self.d, self.inter)
+        if y is None:
+            y = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+        if pre is None and save:
+            pre = torch.empty(T, 2 * self.inter, dtype=torch.bfloat16, device=x.device)
+        for name, t, cols in (("y", y, self.d), ("pre", pre, 2 * self.inter)):
+            _need_cuda(t, name, torch.bfloat16)
+            _need_shape(t, name, (T, cols))
+        _check(lib().moe_ffn_forward(self.ctx, _ptr(x), _ptr(xs), T, _ptr(gu), _ptr(gus), _ptr(dn), _ptr(dns), _ptr(y),
+                                     _ptr(pre), _stream(stream)), "moe_ffn_forward")
+        return (y, pre) if pre is not None else y
+
+    def backward(self, x, pre, gate_up, down, dy, dx=None, dgate_up=None, ddown=None, stream=None):
+        """(dx, dgate_up, ddown); pass ``False`` for one of them to leave it out (None comes back)."""
+        import torch
+
+        T = x.shape[0]
+        given = dict(x=(x, (T, self.d)), pre=(pre, (T, 2 * self.inter)), gate_up=(gate_up, (2 * self.inter, self.d)),
+                     down=(down, (self.d, self.inter)), dy=(dy, (T, self.d)))
+        outs = []
+        for name, t, like in (("dx", dx, x), ("dgate_up", dgate_up, gate_up), ("ddown", ddown, down)):
+            t = None if t is False else torch.empty_like(like) if t is None else t
+            outs.append(t)
+            given[name] = (t, tuple(like.shape))
+        for name, (t, shape) in given.items():
+            _need_cuda(t, name, torch.bfloat16)
+            _need_shape(t, name, shape)
+        _check(lib().moe_ffn_backward(self.ctx, _ptr(x), _ptr(pre), T, _ptr(gate_up), _ptr(down), _ptr(dy),
+                                      *(_ptr(t) for t in outs), _stream(stream)), "moe_ffn_backward")
+        return tuple(outs)
+
+    def status(self) -> int:
+        return moe_ffn_status(self.ctx)
+
+    def close(self):
+        if self.ctx:
+            moe_ffn_destroy(self.ctx)
             self.ctx = None
 
     def __del__(self):

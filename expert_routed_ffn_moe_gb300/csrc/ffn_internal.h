@@ -1,0 +1,135 @@
+// Internal declarations of the dense gated feed-forward block and the norm in
+// front of it: shapes, the context's workspace and the kernel launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+#include "moe_common.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------- mx8
+// Scale bytes of a [rows, cols] mx8 matrix: tiles of 128 rows x 4 groups of 32
+// columns, 512 bytes each, in the order in which tcgen05.cp moves them into
+// tensor memory (row r of the tile at byte (r % 32) * 16 + (r / 32) * 4).
+__host__ __device__ inline size_t mx_tile_cols(size_t cols) { return (cols + 127) / 128; }
+__host__ __device__ inline size_t mx_scale_bytes(size_t rows, size_t cols) {
+  return (rows + 127) / 128 * mx_tile_cols(cols) * 512;
+}
+// Byte of the first of the four groups 4 w .. 4 w + 3 of row r.
+__host__ __device__ inline size_t mx_scale_word(size_t r, size_t w, size_t tile_cols) {
+  return (r / 128 * tile_cols + w) * 512 + r % 32 * 16 + r / 32 % 4 * 4;
+}
+
+// The scale byte of a group whose largest magnitude is amax: e + 127 with e the
+// least integer >= -127 such that amax <= 448 * 2^e.  amax = 1.m * 2^p: e is
+// p - 8 where 1.m <= 1.75 (448 = 1.75 * 2^8), else p - 7.  Infinity and NaN give
+// 255, the scale that is not a number.
+MOE_DEV uint32_t mx_scale_byte(float amax) {
+  const uint32_t b = __float_as_uint(amax) & 0x7fffffffu;
+  if (b >= 0x7f800000u) return 255u;
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(e, 0);
+}
+// 2^-e, what the values are multiplied by before they are rounded to e4m3.
+// Exact for every byte 0..246 that a finite amax can have (2^127 .. 2^-119); byte 255 gives NaN.
+MOE_DEV float mx_inverse_scale(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - byte) << 23);
+}
+MOE_DEV float mx_scale(uint32_t byte) {  // 2^e; 2^-127 is subnormal
+  return byte == 255u ? __uint_as_float(0x7fffffffu) : (byte ? __uint_as_float(byte << 23) : __uint_as_float(0x400000u));
+}
+// |v| for a running maximum that keeps NaN (fmaxf drops it): as an integer the
+// magnitude bits of a NaN lie above those of infinity.
+MOE_DEV uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Two values to e4m3, to the nearest even (the scales keep them within 448).
+MOE_DEV uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+MOE_DEV uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
+
+// ---------------------------------------------------------------- activations
+// silu(g) = g sigmoid(g); gelu in its tanh form, 0.5 g (1 + tanh z) =
+// g sigmoid(2 z): both from the fast exponential and division of sigmoid
+// (~2^-21 relative).
+// The logistic function, 0 below e^-80 (so that a huge negative g gives 0 and
+// not g e^-80; NaN stays NaN through the product with g).
+MOE_DEV float logistic(float z) { return z < -80.0f ? 0.0f : sigmoid(z); }
+MOE_DEV float act_value(float g, int act) {
+  if (act == MOE_ACT_SILU) return g * logistic(g);
+  return g * logistic(1.5957691216057308f * (g + 0.044715f * g * g * g));
+}
+// act(g) and its derivative
+MOE_DEV void act_and_grad(float g, int act, float& a, float& da) {
+  if (act == MOE_ACT_SILU) {
+    const float p = logistic(g);
+    a = g * p;
+    da = p + a * (1.0f - p);
+  } else {
+    const float g2 = g * g;
+    const float p = logistic(1.5957691216057308f * (g + 0.044715f * g * g2));
+    a = g * p;
+    // beyond |g| = 10 p is 0 or 1 to fp32 and the second term vanishes; the bound keeps an overflowing g^2 out
+    da = p + a * (1.0f - p) * (1.5957691216057308f * (1.0f + 0.134145f * fminf(g2, 100.0f)));
+  }
+}
+
+struct FfnShape {
+  int T, d, I, act;
+};
+
+// ffn_norm.cu
+constexpr int kMaxNormWidth = 16384;
+constexpr int kNormPartials = 608;  // rows of partial weight gradients (4 blocks for each of 152 SMs)
+struct NormArgs {
+  const void *x, *res, *w;
+  void *s, *y;
+  uint8_t* scales;
+  int T, d;
+  int x_dtype, s_dtype, w_dtype, y_dtype;
+  float eps;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+struct NormGradArgs {
+  const void *s, *w, *dy, *ds;
+  void *dx, *dw;
+  float* partial;  // [kNormPartials, d]
+  int T, d;
+  int dtype, w_dtype;
+  float eps;
+};
+cudaError_t launch_norm_backward(const NormGradArgs& a, cudaStream_t st);
+cudaError_t launch_mx_quantize(const void* v, int dtype, int rows, int cols, uint8_t* codes, uint8_t* scales,
+                               cudaStream_t st);
+
+// Operands and outputs of one call on device memory (NULL where absent).
+struct FfnForwardArgs {
+  const void *x, *gate_up, *down;
+  const uint8_t *xs, *gate_up_s, *down_s;  // mx8 scales
+  void* y;
+  void* pre;
+};
+struct FfnBackwardArgs {
+  const uint16_t *x, *pre, *gate_up, *down, *dy;
+  uint16_t *dx, *dgate_up, *ddown;
+};
+struct FfnScratch {
+  uint16_t* h;       // [max_tokens, I] bf16 act(gate) * up
+  uint8_t* hq;       // the same as mx8 codes
+  uint8_t* hs;       // and scales
+  uint16_t* dpre;    // [max_tokens, 2 I] bf16 gradients of the pre-activations (training)
+  unsigned* status;  // device status word
+};
+
+// ffn_simple.cu
+cudaError_t launch_simple_forward(const FfnShape& s, bool mx, const FfnForwardArgs& a, const FfnScratch& sc,
+                                  cudaStream_t st);
+cudaError_t launch_simple_backward(const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc, cudaStream_t st);
+
+}  // namespace moe

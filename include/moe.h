@@ -59,6 +59,18 @@ extern "C" {
 /* dtype of x (and of y, which has the same dtype) */
 #define MOE_F32 0
 #define MOE_BF16 1
+/* 8-bit rows with scales (the feed-forward block and the norm only): a matrix
+ * of [rows, cols] values, cols a multiple of 32, is stored as its e4m3 codes
+ * [rows, cols] and one scale 2^e per group of 32 neighbouring columns, e the
+ * least integer >= -127 with max|v| <= 448 * 2^e; a code is v / 2^e rounded to
+ * the nearest e4m3 value, ties to even.  A scale is stored as the byte e + 127;
+ * a group that holds an infinity or a NaN has the byte 255 (not a number).  The
+ * scale bytes lie in tiles of 128 rows x 4 groups, 512 bytes each, row tile by
+ * row tile: the byte of (row, group) is at
+ *   ((row / 128) * ((cols + 127) / 128) + group / 4) * 512
+ *     + (row % 32) * 16 + (row / 32 % 4) * 4 + group % 4,
+ * and the bytes of rows and groups past the matrix are 0. */
+#define MOE_MX8 2
 
 /* storage format of the expert weights (moe_config.weight_format) */
 #define MOE_W_BF16 0           /* bf16 matrices, as described at moe_forward */
@@ -76,6 +88,11 @@ extern "C" {
                                   [2I] rows of d weights followed by its down [d] rows of I weights.
                                   Needs inter % 256 == 0 (and, on the grouped-GEMM path, d and inter
                                   each 256 or a multiple of 512). */
+#define MOE_W_MX8 2            /* MOE_MX8 matrices (moe_ffn_config.weight_format only) */
+
+/* activation of the feed-forward block's gate (moe_ffn_config.activation) */
+#define MOE_ACT_SILU 0         /* g / (1 + exp(-g)) */
+#define MOE_ACT_GELU 1         /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
 
 /* execution path for the expert FFNs (moe_set_path) */
 #define MOE_PATH_AUTO 0        /* T <= 4: GEMV over the selected experts; otherwise grouped GEMM */
@@ -288,6 +305,99 @@ int moe_decode_noalloc(const void* x, int T, int x_dtype, int d, int n_experts, 
  * moe_forward call has run on it yet; MOE_ERR_ALIGN for unaligned outputs. */
 int moe_last_routing(moe_ctx* ctx, int32_t* idx, float* w, int32_t* counts, int32_t* offsets, int32_t* perm,
                      int32_t* slot, int* T_out, int* k_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The dense gated feed-forward block and the norm in front of it: what stands
+ * beside the routed layer in a model whose first layers are not routed, in
+ * training as well as in serving.  Same conventions as above.
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm with the residual's addition, for every row t:
+ *   s = x + residual (s = x with residual NULL),
+ *   y = s * rsqrt(mean(s^2) + eps) * weight,
+ * in fp32, y from the sum before it is rounded into s_out.  x [T, d] (x_dtype),
+ * residual and s_out [T, d] (s_dtype; either may be NULL), weight [d]
+ * (w_dtype), y [T, d] (y_dtype: MOE_F32, MOE_BF16, or MOE_MX8 with its scales
+ * in y_scales, which is NULL for the others).  s_out may be residual itself,
+ * and y may be x where their dtypes are the same and d is a multiple of 8;
+ * no other output may overlap an input.  d is any width up to 16384 (a multiple
+ * of 32 for MOE_MX8), MOE_ERR_UNSUPPORTED beyond; MOE_ERR_ARG for a dtype not
+ * listed or eps < 0.  No workspace, no context. */
+int moe_add_norm(const void* x, int x_dtype, const void* residual, int s_dtype, const void* weight, int w_dtype, int T,
+                 int d, float eps, void* s_out, void* y, int y_dtype, void* y_scales, void* stream);
+
+/* Bytes of the workspace of moe_add_norm_backward for rows of width d. */
+long long moe_add_norm_workspace(int d);
+
+/* Gradients of moe_add_norm from the s it stored: with n = s * rsqrt(mean(s^2)
+ * + eps) and g = dy * weight,
+ *   dx = rsqrt(mean(s^2) + eps) * (g - n * mean(g * n)) + ds,
+ *   dweight = sum over the rows of dy * n.
+ * s, dy, ds [T, d] and dx [T, d] have `dtype`; ds is the gradient that reaches s
+ * by the residual path (NULL: none), and dx is the gradient of x and of the
+ * residual alike.  weight and dweight [d] have w_dtype.  dx or dweight may be
+ * NULL to skip it; dx may be dy or ds.  workspace: moe_add_norm_workspace(d)
+ * bytes, needed for dweight; calls that overlap in time need one each.  The
+ * result does not depend on timing.  T == 0 sets dweight to 0. */
+int moe_add_norm_backward(const void* s, const void* weight, const void* dy, const void* ds, int dtype, int w_dtype,
+                          int T, int d, float eps, void* dx, void* dweight, void* workspace, void* stream);
+
+/* Bytes of the scales of a MOE_MX8 matrix of [rows, cols]. */
+long long moe_mx_scale_bytes(int rows, int cols);
+
+/* Round v [rows, cols] (dtype MOE_F32 or MOE_BF16) to MOE_MX8: codes [rows,
+ * cols] and scales, e.g. for the weights of a block with MOE_W_MX8.  cols is a
+ * multiple of 32 (MOE_ERR_UNSUPPORTED otherwise). */
+int moe_quantize_mx(const void* v, int dtype, int rows, int cols, void* codes, void* scales, void* stream);
+
+typedef struct moe_ffn_config {
+  int d;               /* width of x and y; a multiple of 8 (of 32 with MOE_W_MX8) */
+  int inter;           /* inner size I; the same */
+  int max_tokens;      /* largest T a call will use (the workspace is sized for it) */
+  int activation;      /* MOE_ACT_* */
+  int weight_format;   /* MOE_W_BF16: x and the weights are bf16; MOE_W_MX8: they are MOE_MX8 */
+  int training;        /* 1: calls of moe_ffn_backward are allowed (MOE_W_BF16 only); 0: forward only */
+} moe_ffn_config;
+
+typedef struct moe_ffn moe_ffn;
+
+/* Validate `cfg`, select the current CUDA device and allocate the workspace.
+ * On success *out owns it until moe_ffn_destroy.  Errors: MOE_ERR_ARG,
+ * MOE_ERR_UNSUPPORTED (sizes above, training with MOE_W_MX8, device is not
+ * sm_103), MOE_ERR_NOMEM, MOE_ERR_CUDA.  Synchronous. */
+int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out);
+
+/* pre = x gate_up^T, h = act(pre[:, :I]) * pre[:, I:], y = h down^T.
+ * x [T, d], gate_up [2I, d] (rows 0..I-1 gate, I..2I-1 up), down [d, I],
+ * y [T, d] bf16.  pre: [T, 2I] bf16, what moe_ffn_backward needs, or NULL
+ * (MOE_ERR_UNSUPPORTED with MOE_W_MX8).  The *_scales are those of MOE_MX8
+ * operands, NULL otherwise.  Sums are fp32; h is held in bf16, or, with
+ * MOE_W_MX8, in MOE_MX8, between the two products.  y and pre overlap no input.
+ * Asynchronous on `stream`, nothing allocated, no host synchronisation:
+ * captures into a CUDA graph. */
+int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, const void* gate_up,
+                    const void* gate_up_scales, const void* down, const void* down_scales, void* y, void* pre,
+                    void* stream);
+
+/* Gradients of moe_ffn_forward, all bf16: with [g | u] = pre, dh = dy down,
+ *   dpre = [dh * u * act'(g) | dh * act(g)],  dx = dpre gate_up,
+ *   dgate_up = dpre^T x,  ddown = dy^T (act(g) * u).
+ * x, pre and the weights are those of the forward call, dy [T, d].  Any of dx
+ * [T, d], dgate_up [2I, d], ddown [d, I] may be NULL to skip it.  Sums are fp32;
+ * dpre and act(g) * u are held in bf16 between the products.  T == 0 sets
+ * dgate_up and ddown to 0.  MOE_ERR_UNSUPPORTED without cfg.training. */
+int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const void* gate_up, const void* down,
+                     const void* dy, void* dx, void* dgate_up, void* ddown, void* stream);
+
+/* Number of kernels this context has launched (or captured) so far. */
+long long moe_ffn_launch_count(moe_ffn* ctx);
+
+/* As moe_status, for a moe_ffn context. */
+int moe_ffn_status(moe_ffn* ctx);
+
+/* Free the context and its workspace (synchronises the device first).  NULL is
+ * a no-op. */
+void moe_ffn_destroy(moe_ffn* ctx);
 
 /* Static description of a return code. */
 const char* moe_strerror(int code);
