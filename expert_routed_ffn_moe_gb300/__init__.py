@@ -84,8 +84,10 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_init.argtypes = [ctypes.POINTER(moe_ffn_config), ctypes.POINTER(P)]
         L.moe_ffn_forward.argtypes = [P, P, P, I, P, P, P, P, P, P, P]
         L.moe_ffn_backward.argtypes = [P, P, P, I, P, P, P, P, P, P, P]
+        L.moe_ffn_set_spin_limit.argtypes = [P, ctypes.c_longlong]
+        L.moe_ffn_inject_stall.argtypes = [P, I]
         L.moe_ffn_status.argtypes = [P]
-        for f in ("moe_add_norm", "moe_add_norm_backward", "moe_quantize_mx", "moe_ffn_init", "moe_ffn_forward",
+        for f in ("moe_ffn_set_spin_limit", "moe_ffn_inject_stall", "moe_add_norm", "moe_add_norm_backward", "moe_quantize_mx", "moe_ffn_init", "moe_ffn_forward",
                   "moe_ffn_backward", "moe_ffn_status"):
             getattr(L, f).restype = I
         L.moe_add_norm_workspace.argtypes = [I]
@@ -495,6 +497,14 @@ def moe_ffn_destroy(ctx) -> None:
 
 def moe_ffn_status(ctx) -> int:
     return lib().moe_ffn_status(ctx)
+
+
+def moe_ffn_set_spin_limit(ctx, limit_ns: int) -> None:
+    _check(lib().moe_ffn_set_spin_limit(ctx, limit_ns), "moe_ffn_set_spin_limit")
+
+
+def moe_ffn_inject_stall(ctx, on: bool) -> None:
+    _check(lib().moe_ffn_inject_stall(ctx, int(on)), "moe_ffn_inject_stall")
 
 
 def moe_ffn_launch_count(ctx) -> int:

@@ -13,10 +13,13 @@ struct moe_ffn {
   moe_ffn_config cfg;
   void* block = nullptr;  // the single device allocation holding the workspace
   FfnScratch sc{};
+  FfnEngine eng{};
   long long launches = 0;
 };
 
 namespace {
+
+constexpr long long kDefaultSpinNs = 1000000000LL;  // 1 s
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool stream_dtype(int t) { return t == MOE_F32 || t == MOE_BF16; }
@@ -102,6 +105,19 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
   }
   if (!(prop.major == 10 && prop.minor == 3)) return MOE_ERR_UNSUPPORTED;
 
+  FfnEngine eng{};
+  eng.pairs = prop.multiProcessorCount / 2;
+  eng.ctl.spin_limit = kDefaultSpinNs;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (prepare_ffn_gemm(&eng.pairs) != cudaSuccess || eng.pairs < 1 ||
+      cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || !fn) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  eng.encode = reinterpret_cast<EncodeTiledFn>(fn);
+
   const size_t T = c.max_tokens, I = c.inter;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -136,7 +152,21 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
   ctx->sc.hq = reinterpret_cast<uint8_t*>(b + o_hq);
   ctx->sc.hs = reinterpret_cast<uint8_t*>(b + o_hs);
   ctx->sc.dpre = reinterpret_cast<uint16_t*>(b + o_dpre);
+  eng.ctl.status = ctx->sc.status;
+  ctx->eng = eng;
   *out = ctx;
+  return MOE_OK;
+}
+
+int moe_ffn_set_spin_limit(moe_ffn* ctx, long long limit) {
+  if (!ctx || limit < 0) return MOE_ERR_ARG;
+  ctx->eng.ctl.spin_limit = limit == 0 ? kDefaultSpinNs : limit;
+  return MOE_OK;
+}
+
+int moe_ffn_inject_stall(moe_ffn* ctx, int on) {
+  if (!ctx || (on != 0 && on != 1)) return MOE_ERR_ARG;
+  ctx->eng.ctl.stall = on;
   return MOE_OK;
 }
 
@@ -157,8 +187,12 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
   const FfnShape s{T, c.d, c.inter, c.activation};
   const FfnForwardArgs a{x,   gate_up, down, static_cast<const uint8_t*>(x_scales),
                          static_cast<const uint8_t*>(gate_up_scales), static_cast<const uint8_t*>(down_scales), y, pre};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   ctx->launches += 2;
-  return cuda_code(launch_simple_forward(s, mx, a, ctx->sc, static_cast<cudaStream_t>(stream)));
+  if (mx) return cuda_code(launch_simple_forward(s, mx, a, ctx->sc, st));
+  cudaError_t err = launch_ffn_gate_up(ctx->eng, s, x, gate_up, ctx->sc.h, static_cast<uint16_t*>(pre), st);
+  if (err == cudaSuccess) err = launch_ffn_down(ctx->eng, s, ctx->sc.h, down, y, st);
+  return cuda_code(err);
 }
 
 int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const void* gate_up, const void* down,
@@ -182,9 +216,22 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
   const FfnShape s{T, c.d, c.inter, c.activation};
   auto in = [](const void* p) { return static_cast<const uint16_t*>(p); };
   auto out = [](void* p) { return static_cast<uint16_t*>(p); };
-  const FfnBackwardArgs a{in(x), in(pre), in(gate_up), in(down), in(dy), out(dx), out(dgate_up), out(ddown)};
-  ctx->launches += 1 + (dx != nullptr) + (dgate_up != nullptr) + (ddown != nullptr);
-  return cuda_code(launch_simple_backward(s, a, ctx->sc, st));
+  const FfnScratch& sc = ctx->sc;
+  cudaError_t err = launch_ffn_grad_h(ctx->eng, s, in(dy), in(down), in(pre), sc.dpre, sc.h, st);
+  ++ctx->launches;
+  if (err == cudaSuccess && dx) {
+    err = launch_ffn_dx(ctx->eng, s, sc.dpre, in(gate_up), out(dx), st);
+    ++ctx->launches;
+  }
+  if (err == cudaSuccess && dgate_up) {
+    err = launch_ffn_weight_grad(ctx->eng, sc.dpre, 2 * s.I, in(x), s.d, T, out(dgate_up), st);
+    ++ctx->launches;
+  }
+  if (err == cudaSuccess && ddown) {
+    err = launch_ffn_weight_grad(ctx->eng, in(dy), s.d, sc.h, s.I, T, out(ddown), st);
+    ++ctx->launches;
+  }
+  return cuda_code(err);
 }
 
 long long moe_ffn_launch_count(moe_ffn* ctx) { return ctx ? ctx->launches : 0; }

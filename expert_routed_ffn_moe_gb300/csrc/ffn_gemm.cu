@@ -1,0 +1,573 @@
+// The gated feed-forward block's matrix products on the 5th-generation tensor
+// cores, for the forward and the backward pass.
+//
+//   gate_up   [g | u] = x gate_up^T; h = act(g) * u        (x, weights K-major)
+//   down      y = h down^T
+//   grad_h    dh = dy down; dpre = [dh u act'(g) | dh act(g)]; h = act(g) * u
+//   dx        dx = dpre gate_up
+//   dgate_up  dpre^T x
+//   ddown     dy^T h
+//
+// One persistent kernel.  A pair of CTAs on neighbouring SMs (a cluster of two)
+// computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA loads its
+// own 128 rows of A and half of B's 256 rows, so a 64-deep k block costs each
+// SM 32 KB of shared-memory fill for 256 cycles of MMA (a lone CTA's 128 x 256
+// tile takes 48 KB for the same work).  Per CTA 10 warps:
+//   warp 0     TMA producer (one thread) of a ring of k blocks, 128-byte swizzle;
+//   warp 1     allocates all 512 TMEM columns: two fp32 accumulators of 256
+//              columns; in the pair's first CTA one thread issues the MMAs;
+//   warps 2-9  epilogue: two warps for each quarter of the TMEM lanes, each
+//              taking one half of the columns, through a swizzled staging tile
+//              per warp and TMA stores (which clip ragged edges).
+// The epilogue of tile i overlaps the main loop of tile i + 1.  In the gate/up
+// product B's first half holds gate rows and the second half the up rows of the
+// same 128 neurons, so the activation finishes in the accumulator's columns.
+//
+// Operands may lie K-major (the reduction contiguous in memory) or MN-major:
+// dx, dgate_up and ddown read the forward pass's matrices where they lie, with
+// no transposed copies.  A ragged M, N or K reads zeros from TMA's bounds fill.
+//
+// Every wait is bounded; on expiry the kernel drains what it has in flight,
+// frees TMEM and returns (see the end of the kernel).
+#include "ffn_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBM = 128;                    // rows of A per CTA
+constexpr int kBN = 256;                    // accumulator columns
+constexpr int kBK = 64;                     // k block: 128 bytes of bf16
+constexpr int kOpBytes = 128 * kBK * 2;     // one operand's half tile: 16 KB
+constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kStoreBytes = 32 * 128;       // staging tile: 32 rows x 64 bf16
+constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
+
+enum { kEpiStore, kEpiGateUp, kEpiGrad };
+
+struct GemmParams {
+  CUtensorMap a, b;                // operands
+  CUtensorMap out;                 // bf16 result: y / dx / dW, or h
+  CUtensorMap out_g, out_u;        // the halves of pre (gate/up) or of dpre (grad)
+  const uint16_t* pre;             // grad: [M, 2N] pre-activations
+  int M, N, K;                     // N: columns of the result (gate/up: neurons)
+  int act;
+  int store_pre;
+  DevCtl ctl;
+};
+
+constexpr int stages_of(int epi) { return epi == kEpiStore ? 6 : 5; }
+constexpr int buffers_of(int epi) { return epi == kEpiStore ? 1 : 2; }  // staging tiles per epilogue warp
+
+struct __align__(8) Bars {
+  uint64_t full[6];    // used in the first CTA: both CTAs' copies of a k block have landed
+  uint64_t empty[6];   // the MMAs of a k block are done (committed to both CTAs)
+  uint64_t tfull[2];   // an accumulator is complete (both CTAs)
+  uint64_t tempty[2];  // used in the first CTA: both CTAs' epilogues have read an accumulator
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t peer_issued;  // first CTA, after an abort: k blocks that the other CTA has loaded
+  uint32_t peer_abort;
+};
+
+constexpr size_t smem_of(int epi) {
+  return 1024 + (size_t)stages_of(epi) * kStageBytes + (size_t)kEpiWarps * buffers_of(epi) * kStoreBytes + sizeof(Bars);
+}
+static_assert(smem_of(kEpiStore) <= 227 * 1024 && smem_of(kEpiGateUp) <= 227 * 1024, "shared memory of one CTA");
+
+MOE_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of `p` (this CTA's shared memory) in the pair's CTA `rank`.
+MOE_DEV uint32_t map_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+MOE_DEV void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// TMA load into this CTA whose bytes count on a barrier of the pair's first CTA.
+MOE_DEV void tma_load_pair(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+MOE_DEV void tma_store(const CUtensorMap* m, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+MOE_DEV void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEV void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// Shared-memory matrix descriptor of an MN-major bf16 operand, 128-byte swizzle:
+// each k is a 128-byte row of 64 elements along m (or n), 8 k rows make a
+// 1024-byte atom; the next 64 elements along m lie `64 k rows` further.
+MOE_DEV uint64_t desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>((kBK * 128) >> 4) << 16;  // leading: from 64 elements of m to the next 64
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;         // stride: from 8 k rows to the next 8
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+MOE_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once this thread's earlier MMAs have finished.
+MOE_DEV void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
+MOE_DEV void set_abort(Bars* b) { *reinterpret_cast<volatile int*>(&b->abort_flag) = 1; }
+
+// Tile t of the sweep: kGroupM m-tiles at a time, all n for each group.
+MOE_DEV void tile_of(int t, int mt, int nt, int& m, int& n) {
+  const int per = kGroupM * nt, g = t / per, r = t - g * per;
+  const int gm = min(kGroupM, mt - g * kGroupM);
+  m = g * kGroupM + r % gm;
+  n = r / gm;
+}
+
+// 16 bytes (8 bf16) into a swizzled staging tile: row `lane`, 16-byte column c.
+MOE_DEV void stage16(uint8_t* tile, int lane, int c, uint4 v) {
+  *reinterpret_cast<uint4*>(tile + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
+  constexpr int S = stages_of(EPI), NB = buffers_of(EPI);
+  constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;  // result columns per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = base + S * kStageBytes;
+  Bars* bar = reinterpret_cast<Bars*>(staging + kEpiWarps * NB * kStoreBytes);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mt = (p.M + 2 * kBM - 1) / (2 * kBM), nt = (p.N + TN - 1) / TN, tiles = mt * nt;
+  const int KB = (p.K + kBK - 1) / kBK;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->tfull[i], 1);
+      mbar_init(&bar->tempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(&bar->mma_done, 1);
+    bar->abort_flag = 0;
+    bar->peer_issued = bar->peer_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bar->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  int issued = 0;  // producer thread: k blocks loaded
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&p.a);
+      tma_prefetch_desc(&p.b);
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        int m, n;
+        tile_of(t, mt, nt, m, n);
+        const int arow = (2 * m + (int)rank) * kBM;
+        // B's half: gate rows in the first CTA, up rows in the second
+        const int brow = EPI == kEpiGateUp ? n * TN + (int)rank * p.N : n * TN + (int)rank * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          const int st = issued % S;
+          if (!mbar_wait(&bar->empty[st], ((issued / S) & 1) ^ 1, p.ctl) || aborted(bar)) {
+            set_abort(bar);
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kStageBytes);
+          const uint32_t fb = map_cta(&bar->full[st], 0);
+          uint8_t* a = base + st * kStageBytes;
+          uint8_t* b = a + kOpBytes;
+          const int k = kb * kBK;
+          if (A_MN) {
+            tma_load_pair(a, &p.a, arow, k, fb);
+            tma_load_pair(a + kOpBytes / 2, &p.a, arow + 64, k, fb);
+          } else {
+            tma_load_pair(a, &p.a, k, arow, fb);
+          }
+          if (B_MN) {
+            tma_load_pair(b, &p.b, brow, k, fb);
+            tma_load_pair(b + kOpBytes / 2, &p.b, brow + 64, k, fb);
+          } else {
+            tma_load_pair(b, &p.b, k, brow, fb);
+          }
+          ++issued;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      int it = 0, lt = 0;
+      bool ok = true;
+      if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
+        set_abort(bar);
+        ok = false;
+      }
+      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
+        const int acc = lt & 1;
+        if (!mbar_wait(&bar->tempty[acc], ((lt >> 1) & 1) ^ 1, p.ctl) || aborted(bar)) {
+          set_abort(bar);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * kBN;
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const int st = it % S;
+          if (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar)) {
+            set_abort(bar);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
+          const uint64_t da = A_MN ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
+          // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+          constexpr uint64_t sa = A_MN ? 128 : 2, sb = B_MN ? 128 : 2;
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, (kb | j) != 0);
+          commit_pair(&bar->empty[st]);
+        }
+        if (ok) commit_pair(&bar->tfull[acc]);
+      }
+      // the MMAs issued so far are done before TMEM is freed and shared memory left
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&bar->mma_done))
+                   : "memory");
+      mbar_wait(&bar->mma_done, 0, p.ctl);
+    }
+  } else {
+    const int ew = warp - 2, part = warp & 3, half = ew >> 2;
+    uint8_t* tile0 = staging + ew * NB * kStoreBytes;
+    const uint32_t lanes = (uint32_t)(part * 32) << 16;
+    int lt = 0, nbuf = 0;
+    // a staging tile that no store reads any more
+    auto next_tile = [&]() {
+      if (lane == 0) tma_store_wait_read<NB - 1>();
+      __syncwarp();
+      return tile0 + (NB > 1 ? (nbuf++ % NB) * kStoreBytes : 0);
+    };
+    auto put_tile = [&](const CUtensorMap* map, const uint8_t* tile, int x, int y) {
+      fence_proxy_async_shared_cta();
+      __syncwarp();
+      if (lane == 0) {
+        if (x < p.N && y < p.M) tma_store(map, x, y, tile);
+        tma_store_commit();  // also without a store, so that groups and staging tiles stay in step
+      }
+    };
+    for (int t = pair; t < tiles; t += pairs, ++lt) {
+      int m, n;
+      tile_of(t, mt, nt, m, n);
+      const int acc = lt & 1;
+      const int y = (2 * m + (int)rank) * kBM + part * 32;
+      if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
+        set_abort(bar);
+        break;
+      }
+      tc_fence_after();
+      __syncwarp();
+      const uint32_t src = tmem + lanes + acc * kBN;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[acc], 0));
+      };
+      if (EPI == kEpiStore) {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {  // two boxes of 64 columns
+          uint32_t r[2][32];
+          tmem_ld32_async(src + half * 128 + c * 64, r[0]);
+          tmem_ld32_async(src + half * 128 + c * 64 + 32, r[1]);
+          uint8_t* tile = next_tile();
+          tmem_ld_wait();
+          if (c == 1) release();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(r[q >> 2][(q & 3) * 8 + 2 * i]),
+                                 __uint_as_float(r[q >> 2][(q & 3) * 8 + 2 * i + 1]));
+            stage16(tile, lane, q, make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          put_tile(&p.out, tile, n * TN + half * 128 + c * 64, y);
+        }
+      } else if (EPI == kEpiGateUp) {
+        const int x = n * TN + half * 64;
+        auto stage_all = [&](const CUtensorMap* map, auto&& value) {
+          uint8_t* tile = next_tile();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t g[32], u[32];
+            tmem_ld32_async(src + half * 64 + c * 32, g);
+            tmem_ld32_async(src + 128 + half * 64 + c * 32, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int e = q * 8 + 2 * i;
+                w[i] = pack_bf16x2(value(__uint_as_float(g[e]), __uint_as_float(u[e])),
+                                   value(__uint_as_float(g[e + 1]), __uint_as_float(u[e + 1])));
+              }
+              stage16(tile, lane, c * 4 + q, make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          put_tile(map, tile, x, y);
+        };
+        if (p.store_pre) {
+          stage_all(&p.out_g, [](float g, float) { return g; });
+          stage_all(&p.out_u, [](float, float u) { return u; });
+        }
+        const int act = p.act;
+        stage_all(&p.out, [act](float g, float u) { return act_value(g, act) * u; });
+        release();
+      } else {
+        // gradients of 128 neurons: dh in the accumulator, g and u from memory
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int x = n * TN + half * 128 + c * 64;
+          const int row = y + lane;
+          uint32_t dg[32], du[32], hh[32];  // bf16 pairs
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t r[32];
+            tmem_ld32_async(src + half * 128 + c * 64 + q * 32, r);
+            uint4 g4[4], u4[4];
+            const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + x + q * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool in = row < p.M && x + q * 32 + i * 8 < p.N;
+              g4[i] = in ? *reinterpret_cast<const uint4*>(gp + i * 8) : make_uint4(0, 0, 0, 0);
+              u4[i] = in ? *reinterpret_cast<const uint4*>(gp + p.N + i * 8) : make_uint4(0, 0, 0, 0);
+            }
+            tmem_ld_wait();
+            if (c == 1 && q == 1) release();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint4 gv = g4[i >> 2], uv = u4[i >> 2];
+              const uint32_t gw = (i & 3) == 0 ? gv.x : (i & 3) == 1 ? gv.y : (i & 3) == 2 ? gv.z : gv.w;
+              const uint32_t uw = (i & 3) == 0 ? uv.x : (i & 3) == 1 ? uv.y : (i & 3) == 2 ? uv.z : uv.w;
+              float a0, d0, a1, d1;
+              act_and_grad(bf16_lo(gw), p.act, a0, d0);
+              act_and_grad(bf16_hi(gw), p.act, a1, d1);
+              const float h0 = __uint_as_float(r[2 * i]), h1 = __uint_as_float(r[2 * i + 1]);
+              const float u0 = bf16_lo(uw), u1 = bf16_hi(uw);
+              dg[q * 16 + i] = pack_bf16x2(h0 * u0 * d0, h1 * u1 * d1);
+              du[q * 16 + i] = pack_bf16x2(h0 * a0, h1 * a1);
+              hh[q * 16 + i] = pack_bf16x2(a0 * u0, a1 * u1);
+            }
+          }
+          auto put = [&](const CUtensorMap* map, const uint32_t(&v)[32]) {
+            uint8_t* tile = next_tile();
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              stage16(tile, lane, q, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+            put_tile(map, tile, x, y);
+          };
+          put(&p.out_g, dg);
+          put(&p.out_u, du);
+          put(&p.out, hh);
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait_read<0>();
+  }
+
+  __syncthreads();
+  // Leave together: the other CTA's shared memory is the target of remote
+  // arrivals and of the MMAs' reads.  On the normal path every copy has landed
+  // (an MMA waited for it).  After an abort copies may be in flight: the second
+  // CTA reports how many k blocks it has loaded, and the first waits for both
+  // CTAs' copies block by block -- a barrier that expects a half that was never
+  // issued is credited with it.
+  if (threadIdx.x == 0 && rank == 1) {
+    store_cluster(map_cta(&bar->peer_issued, 0), (uint32_t)issued);
+    store_cluster(map_cta(&bar->peer_abort, 0), (uint32_t)bar->abort_flag);
+  }
+  cluster_sync();
+  if (threadIdx.x == 0 && rank == 0 && (bar->abort_flag || bar->peer_abort)) {
+    DevCtl drain = p.ctl;
+    drain.spin_limit = 1000000000LL;
+    const int theirs = (int)bar->peer_issued, most = max(issued, theirs);
+    for (int j = max(0, most - S); j < most; ++j) {
+      uint64_t* fb = &bar->full[j % S];
+      if (j >= issued) mbar_expect_tx(fb, kStageBytes);  // only the other CTA's half was issued
+      if (j >= theirs)                                   // only this CTA's half was issued
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, 0)),
+                     "r"(kStageBytes)
+                     : "memory");
+      mbar_wait(fb, (j / S) & 1, drain);
+    }
+  }
+  cluster_sync();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------ host side
+// A 2-D bf16 map: `inner` contiguous elements per row, rows `pitch` elements apart.
+bool make_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+              uint32_t box_inner, uint32_t box_outer) {
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {pitch * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b, uint64_t b_rows, void* out,
+                cudaStream_t st) {
+  // a K-major operand is [rows, K], an MN-major one [K, rows]
+  bool ok = A_MN ? make_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK) : make_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
+  ok = ok && (B_MN ? make_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
+                   : make_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
+  ok = ok && make_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32);
+  if (!ok) return cudaErrorInvalidValue;
+  p.ctl = e.ctl;
+  constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
+  const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
+  ffn_gemm_kernel<EPI, A_MN, B_MN><<<2 * pairs, kThreads, smem_of(EPI), st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t prepare(int* pairs) {
+  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN>;
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_of(EPI);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  err = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+  if (err == cudaSuccess && n < *pairs) *pairs = n;
+  return err;
+}
+
+}  // namespace
+
+cudaError_t prepare_ffn_gemm(int* pairs) {
+  cudaError_t err = prepare<kEpiGateUp, false, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, false, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiGrad, false, true>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, false, true>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, true, true>(pairs);
+  return err;
+}
+
+cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void* x, const void* gate_up, uint16_t* h,
+                               uint16_t* pre, cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.I;
+  p.K = s.d;
+  p.act = s.act;
+  p.store_pre = pre != nullptr;
+  if (pre && (!make_map(e.encode, &p.out_g, pre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
+              !make_map(e.encode, &p.out_u, pre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32)))
+    return cudaErrorInvalidValue;
+  return run<kEpiGateUp, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
+}
+
+cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
+                            cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.d;
+  p.K = s.I;
+  return run<kEpiStore, false, false>(e, p, h, down, s.d, y, st);
+}
+
+cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint16_t* dy, const uint16_t* down,
+                              const uint16_t* pre, uint16_t* dpre, uint16_t* h, cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.I;
+  p.K = s.d;
+  p.act = s.act;
+  p.pre = pre;
+  if (!make_map(e.encode, &p.out_g, dpre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
+      !make_map(e.encode, &p.out_u, dpre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32))
+    return cudaErrorInvalidValue;
+  return run<kEpiGrad, false, true>(e, p, dy, down, s.I, h, st);
+}
+
+cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t* dpre, const uint16_t* gate_up,
+                          uint16_t* dx, cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.d;
+  p.K = 2 * s.I;
+  return run<kEpiStore, false, true>(e, p, dpre, gate_up, s.d, dx, st);
+}
+
+cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
+                                   uint16_t* dw, cudaStream_t st) {
+  GemmParams p{};
+  p.M = M;
+  p.N = N;
+  p.K = T;
+  return run<kEpiStore, true, true>(e, p, a, b, N, dw, st);
+}
+
+}  // namespace moe

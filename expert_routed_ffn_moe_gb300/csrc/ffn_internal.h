@@ -115,10 +115,6 @@ struct FfnForwardArgs {
   void* y;
   void* pre;
 };
-struct FfnBackwardArgs {
-  const uint16_t *x, *pre, *gate_up, *down, *dy;
-  uint16_t *dx, *dgate_up, *ddown;
-};
 struct FfnScratch {
   uint16_t* h;       // [max_tokens, I] bf16 act(gate) * up
   uint8_t* hq;       // the same as mx8 codes
@@ -127,9 +123,33 @@ struct FfnScratch {
   unsigned* status;  // device status word
 };
 
+// Signature of the driver's cuTensorMapEncodeTiled (fetched at run time, so the
+// library needs no link-time dependency on libcuda).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+struct FfnEngine {
+  EncodeTiledFn encode;
+  int pairs;  // CTA pairs that run at a time
+  DevCtl ctl;
+};
+
+// ffn_gemm.cu
+cudaError_t prepare_ffn_gemm(int* pairs);  // kernel attributes; lowers *pairs to what the device runs at a time
+cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void* x, const void* gate_up, uint16_t* h,
+                               uint16_t* pre, cudaStream_t st);
+cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
+                            cudaStream_t st);
+cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint16_t* dy, const uint16_t* down,
+                              const uint16_t* pre, uint16_t* dpre, uint16_t* h, cudaStream_t st);
+cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t* dpre, const uint16_t* gate_up,
+                          uint16_t* dx, cudaStream_t st);
+// dw [M, N] = a^T b, a [T, M], b [T, N]
+cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
+                                   uint16_t* dw, cudaStream_t st);
+
 // ffn_simple.cu
 cudaError_t launch_simple_forward(const FfnShape& s, bool mx, const FfnForwardArgs& a, const FfnScratch& sc,
                                   cudaStream_t st);
-cudaError_t launch_simple_backward(const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc, cudaStream_t st);
 
 }  // namespace moe

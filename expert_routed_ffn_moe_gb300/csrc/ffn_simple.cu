@@ -5,7 +5,7 @@
 namespace moe {
 namespace {
 
-enum { kEpiStore, kEpiGateUp, kEpiGrad };
+enum { kEpiStore, kEpiGateUp };
 
 // Element (row, k) of an operand: bf16 with strides, or mx8 rows.
 struct Operand {
@@ -32,16 +32,13 @@ struct Operand {
 };
 
 struct Epilogue {
-  uint16_t* out;           // kEpiStore: [M, N]; kEpiGateUp: h [M, N]; kEpiGrad: h [M, N]
+  uint16_t* out;           // kEpiStore: [M, N]; kEpiGateUp: h [M, N]
   uint16_t* pre;           // kEpiGateUp: [M, 2N] or NULL
   uint8_t *codes, *scales; // kEpiGateUp on mx8: h in mx8
-  const uint16_t* pre_in;  // kEpiGrad: [M, 2N]
-  uint16_t* dpre;          // kEpiGrad: [M, 2N]
   int act;
 };
 
 MOE_DEV uint16_t to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-MOE_DEV float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // C[m, n] = sum_k A(m, k) B(n, k); kEpiGateUp also with the rows N + n of B.
 template <int EPI>
@@ -87,13 +84,6 @@ __global__ void __launch_bounds__(256) simple_gemm(Operand A, Operand B, int M, 
           ep.pre[pg] = to_bf16(c[i][j]);
           ep.pre[pg + N] = to_bf16(u[i][j]);
         }
-      } else if (in) {
-        float a, da;
-        const float g = from_bf16(ep.pre_in[pg]), up = from_bf16(ep.pre_in[pg + N]);
-        act_and_grad(g, ep.act, a, da);
-        ep.dpre[pg] = to_bf16(c[i][j] * up * da);
-        ep.dpre[pg + N] = to_bf16(c[i][j] * a);
-        ep.out[at] = to_bf16(a * up);
       }
     }
   if (EPI == kEpiGateUp && ep.codes) {
@@ -140,33 +130,6 @@ cudaError_t launch_simple_forward(const FfnShape& s, bool mx, const FfnForwardAr
   e2.out = static_cast<uint16_t*>(a.y);
   return gemm<kEpiStore>(Operand{mx ? (const void*)sc.hq : sc.h, mx ? sc.hs : nullptr, s.I, 1, s.T, s.I},
                          Operand{a.down, a.down_s, s.I, 1, s.d, s.I}, s.T, s.d, s.I, e2, st);
-}
-
-cudaError_t launch_simple_backward(const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc, cudaStream_t st) {
-  Epilogue e1{};
-  e1.act = s.act;
-  e1.pre_in = a.pre;
-  e1.dpre = sc.dpre;
-  e1.out = sc.h;
-  cudaError_t err = gemm<kEpiGrad>(Operand{a.dy, nullptr, s.d, 1, s.T, s.d}, Operand{a.down, nullptr, 1, s.I, s.I, s.d},
-                                   s.T, s.I, s.d, e1, st);
-  Epilogue e{};
-  if (err == cudaSuccess && a.dx) {
-    e.out = a.dx;
-    err = gemm<kEpiStore>(Operand{sc.dpre, nullptr, 2 * s.I, 1, s.T, 2 * s.I},
-                          Operand{a.gate_up, nullptr, 1, s.d, s.d, 2 * s.I}, s.T, s.d, 2 * s.I, e, st);
-  }
-  if (err == cudaSuccess && a.dgate_up) {
-    e.out = a.dgate_up;
-    err = gemm<kEpiStore>(Operand{sc.dpre, nullptr, 1, 2 * s.I, 2 * s.I, s.T}, Operand{a.x, nullptr, 1, s.d, s.d, s.T},
-                          2 * s.I, s.d, s.T, e, st);
-  }
-  if (err == cudaSuccess && a.ddown) {
-    e.out = a.ddown;
-    err = gemm<kEpiStore>(Operand{a.dy, nullptr, 1, s.d, s.d, s.T}, Operand{sc.h, nullptr, 1, s.I, s.I, s.T}, s.d, s.I,
-                          s.T, e, st);
-  }
-  return err;
 }
 
 }  // namespace moe

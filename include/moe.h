@@ -392,6 +392,12 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
 /* Number of kernels this context has launched (or captured) so far. */
 long long moe_ffn_launch_count(moe_ffn* ctx);
 
+/* As moe_set_spin_limit and moe_inject_stall, for a moe_ffn context (the thread
+ * that issues a product's matrix instructions waits for what never happens; calls
+ * whose products run without tensor cores do not wait). */
+int moe_ffn_set_spin_limit(moe_ffn* ctx, long long limit);
+int moe_ffn_inject_stall(moe_ffn* ctx, int on);
+
 /* As moe_status, for a moe_ffn context. */
 int moe_ffn_status(moe_ffn* ctx);
 

@@ -336,6 +336,25 @@ def test_offsets_past_32_bits():
     near(dx[rows], *fc.backward(x[rows], pre[rows], gu, dn, dy[rows], False)["dx"], "dx")
 
 
+def test_wait_that_runs_out_is_reported_and_recovered():
+    g = gen(12)
+    T, d, I = 700, 256, 520
+    x, gu, dn = normal(g, T, d), normal(g, 2 * I, d, scale=0.06), normal(g, d, I, scale=0.04)
+    op = moe.GatedFfn(d, I, T, training=True)
+    want, pre = op.forward(x, gu, dn, save=True)
+    moe.moe_ffn_set_spin_limit(op.ctx, 20_000_000)
+    moe.moe_ffn_inject_stall(op.ctx, True)
+    op.forward(x, gu, dn)
+    assert op.status() == moe.MOE_ERR_TIMEOUT and op.status() == moe.MOE_OK
+    op.backward(x, pre, gu, dn, x)
+    assert op.status() == moe.MOE_ERR_TIMEOUT
+    moe.moe_ffn_inject_stall(op.ctx, False)
+    moe.moe_ffn_set_spin_limit(op.ctx, 0)
+    assert torch.equal(op.forward(x, gu, dn), want) and op.status() == moe.MOE_OK
+    with pytest.raises(moe.MoeError):
+        moe.moe_ffn_set_spin_limit(op.ctx, -1)
+
+
 def test_no_rows():
     d, I = 64, 48
     op, nm = moe.GatedFfn(d, I, 8, training=True), moe.AddNorm(d)
