@@ -129,6 +129,7 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
   const size_t o_h = take(mx ? 0 : T * I * 2);
   const size_t o_hq = take(mx ? T * I : 0);
   const size_t o_hs = take(mx ? mx_scale_bytes(T, I) : 0);
+  const size_t o_up_s = take(mx && I % 128 != 0 ? mx_scale_bytes(I, c.d) : 0);
   const size_t o_dpre = take(c.training ? T * 2 * I * 2 : 0);
   moe_ffn* ctx = new (std::nothrow) moe_ffn();
   if (!ctx) return MOE_ERR_NOMEM;
@@ -151,6 +152,7 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
   ctx->sc.h = reinterpret_cast<uint16_t*>(b + o_h);
   ctx->sc.hq = reinterpret_cast<uint8_t*>(b + o_hq);
   ctx->sc.hs = reinterpret_cast<uint8_t*>(b + o_hs);
+  ctx->sc.up_s = reinterpret_cast<uint8_t*>(b + o_up_s);
   ctx->sc.dpre = reinterpret_cast<uint16_t*>(b + o_dpre);
   eng.ctl.status = ctx->sc.status;
   ctx->eng = eng;
@@ -188,10 +190,23 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
   const FfnForwardArgs a{x,   gate_up, down, static_cast<const uint8_t*>(x_scales),
                          static_cast<const uint8_t*>(gate_up_scales), static_cast<const uint8_t*>(down_scales), y, pre};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const FfnScratch& sc = ctx->sc;
+  cudaError_t err = cudaSuccess;
+  if (mx) {
+    const uint8_t* up_s = a.gate_up_s + mx_scale_bytes(s.I, s.d);  // row tile I / 128 on
+    if (s.I % 128 != 0) {
+      err = launch_mx_up_scales(s, a.gate_up_s, sc.up_s, st);
+      ++ctx->launches;
+      up_s = sc.up_s;
+    }
+    if (err == cudaSuccess) err = launch_ffn_gate_up_mx(ctx->eng, s, a, up_s, sc.hq, sc.hs, st);
+    if (err == cudaSuccess) err = launch_ffn_down_mx(ctx->eng, s, sc.hq, sc.hs, a, st);
+    ctx->launches += 2;
+    return cuda_code(err);
+  }
   ctx->launches += 2;
-  if (mx) return cuda_code(launch_simple_forward(s, mx, a, ctx->sc, st));
-  cudaError_t err = launch_ffn_gate_up(ctx->eng, s, x, gate_up, ctx->sc.h, static_cast<uint16_t*>(pre), st);
-  if (err == cudaSuccess) err = launch_ffn_down(ctx->eng, s, ctx->sc.h, down, y, st);
+  err = launch_ffn_gate_up(ctx->eng, s, x, gate_up, sc.h, static_cast<uint16_t*>(pre), st);
+  if (err == cudaSuccess) err = launch_ffn_down(ctx->eng, s, sc.h, down, y, st);
   return cuda_code(err);
 }
 

@@ -27,6 +27,15 @@
 // dx, dgate_up and ddown read the forward pass's matrices where they lie, with
 // no transposed copies.  A ragged M, N or K reads zeros from TMA's bounds fill.
 //
+// The mx8 form of gate_up and down runs on the block-scaled 8-bit instruction
+// (kind::mxf8f6f4, one e8m0 scale per 32 values of k): a k block is 128 values,
+// the same 128 bytes.  The scale bytes are stored in the order in which
+// tcgen05.cp moves them into tensor memory, so a k block brings 512 bytes of
+// scales per 128 rows and three copies; each CTA needs its own rows' and all of
+// B's.  They take TMEM columns, so the two accumulators there share 32 columns:
+// the epilogue reads those first and the next tile's MMAs may then start.  h is
+// rounded to mx8 in the epilogue, where a thread holds a whole group of 32.
+//
 // Every wait is bounded; on expiry the kernel drains what it has in flight,
 // frees TMEM and returns (see the end of the kernel).
 #include "ffn_internal.h"
@@ -36,12 +45,16 @@ namespace {
 
 constexpr int kBM = 128;                    // rows of A per CTA
 constexpr int kBN = 256;                    // accumulator columns
-constexpr int kBK = 64;                     // k block: 128 bytes of bf16
-constexpr int kOpBytes = 128 * kBK * 2;     // one operand's half tile: 16 KB
+constexpr int kRowBytes = 128;              // a k block: 64 bf16 or 128 e4m3 values
+constexpr int kBK = 64;                     // k block of bf16
+constexpr int kOpBytes = 128 * kRowBytes;   // one operand's half tile: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kStoreBytes = 32 * 128;       // staging tile: 32 rows x 64 bf16
+constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
+constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
+constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
 enum { kEpiStore, kEpiGateUp, kEpiGrad };
@@ -50,6 +63,8 @@ struct GemmParams {
   CUtensorMap a, b;                // operands
   CUtensorMap out;                 // bf16 result: y / dx / dW, or h
   CUtensorMap out_g, out_u;        // the halves of pre (gate/up) or of dpre (grad)
+  CUtensorMap as, bs0, bs1;        // mx8 scales: of A, and of the two 128-row halves of B
+  uint8_t *hq, *hs;                // mx8 gate/up: codes and scales of h
   const uint16_t* pre;             // grad: [M, 2N] pre-activations
   int M, N, K;                     // N: columns of the result (gate/up: neurons)
   int act;
@@ -57,8 +72,10 @@ struct GemmParams {
   DevCtl ctl;
 };
 
-constexpr int stages_of(int epi) { return epi == kEpiStore ? 6 : 5; }
-constexpr int buffers_of(int epi) { return epi == kEpiStore ? 1 : 2; }  // staging tiles per epilogue warp
+constexpr int stages_of(int epi, bool mx) { return epi == kEpiStore && !mx ? 6 : 5; }
+constexpr int stage_bytes(bool mx) { return kStageBytes + (mx ? kScaleBytes : 0); }
+// staging tiles per epilogue warp
+constexpr int buffers_of(int epi, bool mx) { return epi == kEpiStore ? 1 : (mx ? 0 : 2); }
 
 struct __align__(8) Bars {
   uint64_t full[6];    // used in the first CTA: both CTAs' copies of a k block have landed
@@ -72,10 +89,13 @@ struct __align__(8) Bars {
   uint32_t peer_abort;
 };
 
-constexpr size_t smem_of(int epi) {
-  return 1024 + (size_t)stages_of(epi) * kStageBytes + (size_t)kEpiWarps * buffers_of(epi) * kStoreBytes + sizeof(Bars);
+constexpr size_t smem_of(int epi, bool mx) {
+  return 1024 + (size_t)stages_of(epi, mx) * stage_bytes(mx) + (size_t)kEpiWarps * buffers_of(epi, mx) * kStoreBytes +
+         sizeof(Bars);
 }
-static_assert(smem_of(kEpiStore) <= 227 * 1024 && smem_of(kEpiGateUp) <= 227 * 1024, "shared memory of one CTA");
+static_assert(smem_of(kEpiStore, false) <= 227 * 1024 && smem_of(kEpiGateUp, false) <= 227 * 1024 &&
+                  smem_of(kEpiStore, true) <= 227 * 1024 && smem_of(kEpiGateUp, true) <= 227 * 1024,
+              "shared memory of one CTA");
 
 MOE_DEV uint32_t cluster_rank() {
   uint32_t r;
@@ -136,6 +156,42 @@ MOE_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with e4m3 operands and e8m0 scales in TMEM (32 values of k, one scale each).
+MOE_DEV void mma_pair_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of the block-scaled form: e4m3 A and B (K-major), e8m0
+// scales, byte `id` of each row's four.
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int id) {
+  return (static_cast<uint32_t>(id) << 4)          // scale byte of B
+         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+         | (1u << 23)                              // e8m0 scales
+         | (static_cast<uint32_t>(M >> 4) << 24)   // M / 16
+         | (static_cast<uint32_t>(id) << 29);      // scale byte of A
+}
+// 512 bytes of scales (32 rows of 16 bytes) from the same place in both CTAs'
+// shared memory into 4 TMEM columns, repeated for the four lane quarters.
+MOE_DEV void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
+  uint64_t d = 0;  // no swizzle, 8-row groups of 128 bytes
+  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+// One 512-byte scale tile, counted on a barrier of the pair's first CTA.
+MOE_DEV void tma_load_scales_pair(void* dst, const CUtensorMap* m, int col, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(col), "r"(row), "r"(bar)
+      : "memory");
+}
 // Arrive on `bar` of both CTAs once this thread's earlier MMAs have finished.
 MOE_DEV void commit_pair(uint64_t* bar) {
   asm volatile(
@@ -161,21 +217,25 @@ MOE_DEV void stage16(uint8_t* tile, int lane, int c, uint4 v) {
   *reinterpret_cast<uint4*>(tile + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool MX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int S = stages_of(EPI), NB = buffers_of(EPI);
+  constexpr int S = stages_of(EPI, MX), NB = buffers_of(EPI, MX);
+  constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
+  constexpr int kDepth = MX ? kRowBytes : kBK;     // values of k per block
+  static_assert(!MX || (!A_MN && !B_MN && EPI != kEpiGrad), "mx8: forward products only");
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;  // result columns per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = base + S * kStageBytes;
-  Bars* bar = reinterpret_cast<Bars*>(staging + kEpiWarps * NB * kStoreBytes);
+  uint8_t* staging = base + S * kStageBytes;  // (the scales follow the staging tiles)
+  uint8_t* scales = staging + kEpiWarps * NB * kStoreBytes;
+  Bars* bar = reinterpret_cast<Bars*>(scales + (MX ? S * kScaleBytes : 0));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mt = (p.M + 2 * kBM - 1) / (2 * kBM), nt = (p.N + TN - 1) / TN, tiles = mt * nt;
-  const int KB = (p.K + kBK - 1) / kBK;
+  const int KB = (p.K + kDepth - 1) / kDepth;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) {
@@ -221,11 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kStageBytes);
+          if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kTx);
           const uint32_t fb = map_cta(&bar->full[st], 0);
           uint8_t* a = base + st * kStageBytes;
           uint8_t* b = a + kOpBytes;
-          const int k = kb * kBK;
+          const int k = kb * kDepth;
           if (A_MN) {
             tma_load_pair(a, &p.a, arow, k, fb);
             tma_load_pair(a + kOpBytes / 2, &p.a, arow + 64, k, fb);
@@ -237,6 +297,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_pair(b + kOpBytes / 2, &p.b, brow + 64, k, fb);
           } else {
             tma_load_pair(b, &p.b, k, brow, fb);
+          }
+          if (MX) {
+            uint8_t* sc = scales + st * kScaleBytes;
+            tma_load_scales_pair(sc, &p.as, kb, 2 * m + (int)rank, fb);
+            tma_load_scales_pair(sc + 512, &p.bs0, kb, EPI == kEpiGateUp ? n : 2 * n, fb);
+            tma_load_scales_pair(sc + 1024, &p.bs1, kb, EPI == kEpiGateUp ? n : 2 * n + 1, fb);
           }
           ++issued;
         }
@@ -253,12 +319,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
         const int acc = lt & 1;
-        if (!mbar_wait(&bar->tempty[acc], ((lt >> 1) & 1) ^ 1, p.ctl) || aborted(bar)) {
+        // bf16: the accumulator was read two tiles ago; mx8: the tile before has left the shared columns (which its
+        // epilogue warps reach only after the tile before that)
+        const bool free = MX ? lt == 0 || mbar_wait(&bar->tempty[0], (lt - 1) & 1, p.ctl)
+                             : mbar_wait(&bar->tempty[acc], ((lt >> 1) & 1) ^ 1, p.ctl);
+        if (!free || aborted(bar)) {
           set_abort(bar);
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + acc * kBN;
+        const uint32_t d = tmem + acc * (MX ? kBN - kSharedCols : kBN);
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int st = it % S;
           if (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar)) {
@@ -271,8 +341,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t da = A_MN ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
           // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
           constexpr uint64_t sa = A_MN ? 128 : 2, sb = B_MN ? 128 : 2;
+          if (MX) {
+            const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + (it & 1) * 16;
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, (kb | j) != 0);
+            for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_pair_mx(d, da + j * 2, db + j * 2, idesc_mx(2 * kBM, kBN, j), ts, ts + 4, (kb | j) != 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, (kb | j) != 0);
+          }
           commit_pair(&bar->empty[st]);
         }
         if (ok) commit_pair(&bar->tfull[acc]);
@@ -290,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int lt = 0, nbuf = 0;
     // a staging tile that no store reads any more
     auto next_tile = [&]() {
-      if (lane == 0) tma_store_wait_read<NB - 1>();
+      if (lane == 0) tma_store_wait_read<(NB > 1 ? NB - 1 : 0)>();
       __syncwarp();
       return tile0 + (NB > 1 ? (nbuf++ % NB) * kStoreBytes : 0);
     };
@@ -313,21 +392,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       __syncwarp();
-      const uint32_t src = tmem + lanes + acc * kBN;
+      const uint32_t src = tmem + lanes + acc * (MX ? kBN - kSharedCols : kBN);
+      // mx8: the part with the shared columns first (the last columns of accumulator 0, the first of 1)
+      const int first = MX && acc == 0 ? 1 : 0;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[acc], 0));
+        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], 0));
       };
       if (EPI == kEpiStore) {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {  // two boxes of 64 columns
+        for (int i = 0; i < 2; ++i) {  // two boxes of 64 columns
+          const int c = i ^ first;
           uint32_t r[2][32];
           tmem_ld32_async(src + half * 128 + c * 64, r[0]);
           tmem_ld32_async(src + half * 128 + c * 64 + 32, r[1]);
           uint8_t* tile = next_tile();
           tmem_ld_wait();
-          if (c == 1) release();
+          if (i == (MX ? 0 : 1)) release();
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             uint32_t w[4];
@@ -338,6 +420,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             stage16(tile, lane, q, make_uint4(w[0], w[1], w[2], w[3]));
           }
           put_tile(&p.out, tile, n * TN + half * 128 + c * 64, y);
+        }
+      } else if (EPI == kEpiGateUp && MX) {
+        const int row = y + lane;
+        uint32_t bytes = 0;  // the scales of this thread's two groups
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int c = i ^ first, x = n * TN + half * 64 + c * 32;
+          uint32_t g[32], u[32];
+          tmem_ld32_async(src + half * 64 + c * 32, g);
+          tmem_ld32_async(src + 128 + half * 64 + c * 32, u);
+          tmem_ld_wait();
+          if (i == 0) release();
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            g[e] = __float_as_uint(act_value(__uint_as_float(g[e]), p.act) * __uint_as_float(u[e]));
+            top = max(top, g[e] & 0x7fffffffu);
+          }
+          const uint32_t byte = mx_scale_byte(__uint_as_float(top));
+          const float k = mx_inverse_scale(byte);
+          bytes |= byte << (8 * c);
+          if (row < p.M && x < p.N) {
+            uint4* q = reinterpret_cast<uint4*>(p.hq + (size_t)row * p.N + x);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t* v = &g[o * 16 + e * 4];
+                w[e] = e4m3x4(__uint_as_float(v[0]) * k, __uint_as_float(v[1]) * k, __uint_as_float(v[2]) * k,
+                              __uint_as_float(v[3]) * k);
+              }
+              q[o] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        const int x = n * TN + half * 64;
+        if (row < p.M && x < p.N) {  // the second group may lie past the last column: its byte stays 0
+          if (x + 32 >= p.N) bytes &= 0xffu;
+          *reinterpret_cast<uint16_t*>(p.hs + mx_scale_word(row, x / 128, mx_tile_cols(p.N)) + half * 2) =
+              (uint16_t)bytes;
         }
       } else if (EPI == kEpiGateUp) {
         const int x = n * TN + half * 64;
@@ -440,10 +563,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int theirs = (int)bar->peer_issued, most = max(issued, theirs);
     for (int j = max(0, most - S); j < most; ++j) {
       uint64_t* fb = &bar->full[j % S];
-      if (j >= issued) mbar_expect_tx(fb, kStageBytes);  // only the other CTA's half was issued
+      if (j >= issued) mbar_expect_tx(fb, kTx);  // only the other CTA's half was issued
       if (j >= theirs)                                   // only this CTA's half was issued
         asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, 0)),
-                     "r"(kStageBytes)
+                     "r"(kTx)
                      : "memory");
       mbar_wait(fb, (j / S) & 1, drain);
     }
@@ -465,33 +588,59 @@ bool make_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+// mx8 codes [rows, K]; and scale tiles as [row tile][column tile][64 x 8 bytes].
+bool make_code_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows) {
+  const cuuint64_t dims[2] = {K, rows};
+  const cuuint64_t strides[1] = {K};
+  const cuuint32_t box[2] = {kRowBytes, 128};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t row_tiles) {
+  const uint64_t tile_cols = mx_tile_cols(cols);
+  const cuuint64_t dims[3] = {64, tile_cols, row_tiles};
+  const cuuint64_t strides[2] = {512, 512 * tile_cols};
+  const cuuint32_t box[3] = {64, 1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b, uint64_t b_rows, void* out,
                 cudaStream_t st) {
-  // a K-major operand is [rows, K], an MN-major one [K, rows]
-  bool ok = A_MN ? make_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK) : make_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
-  ok = ok && (B_MN ? make_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
-                   : make_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
-  ok = ok && make_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32);
+  bool ok;
+  if (MX) {
+    ok = make_code_map(e.encode, &p.a, a, p.K, p.M) && make_code_map(e.encode, &p.b, b, p.K, b_rows);
+  } else {  // a K-major operand is [rows, K], an MN-major one [K, rows]
+    ok = A_MN ? make_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK)
+              : make_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
+    ok = ok && (B_MN ? make_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
+                     : make_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
+  }
+  ok = ok && (!out || make_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
   if (!ok) return cudaErrorInvalidValue;
   p.ctl = e.ctl;
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
   const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
-  ffn_gemm_kernel<EPI, A_MN, B_MN><<<2 * pairs, kThreads, smem_of(EPI), st>>>(p);
+  ffn_gemm_kernel<EPI, A_MN, B_MN, MX><<<2 * pairs, kThreads, smem_of(EPI, MX), st>>>(p);
   return cudaGetLastError();
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t prepare(int* pairs) {
-  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN>;
-  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI));
+  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX>;
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI, MX));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_of(EPI);
+  cfg.dynamicSmemBytes = smem_of(EPI, MX);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = 2;
@@ -504,15 +653,68 @@ cudaError_t prepare(int* pairs) {
   return err;
 }
 
+// The scales of rows row0, row0 + 1, ... of a matrix as a matrix of their own
+// (row0 a multiple of 32 but not of 128, so that its tiles start elsewhere):
+// one 4-byte word per thread.
+__global__ void __launch_bounds__(256) shift_scales_kernel(const uint32_t* src, uint32_t* dst, int row0, int rows,
+                                                           int tile_cols, size_t words) {
+  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= words) return;
+  // word `at` of dst: tile, then row % 32, then row / 32 % 4
+  const size_t tile = at / 128, in = at % 128;
+  const size_t row = tile / tile_cols * 128 + in % 4 * 32 + in / 4, col = tile % tile_cols;
+  dst[at] = row < (size_t)rows ? src[mx_scale_word(row0 + row, col, tile_cols) / 4] : 0u;
+}
+
 }  // namespace
 
 cudaError_t prepare_ffn_gemm(int* pairs) {
-  cudaError_t err = prepare<kEpiGateUp, false, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, false, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiGrad, false, true>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, false, true>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, true, true>(pairs);
+  cudaError_t err = prepare<kEpiGateUp, false, false, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, false, false, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiGrad, false, true, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, false, true, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, true, true, false>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiGateUp, false, false, true>(pairs);
+  if (err == cudaSuccess) err = prepare<kEpiStore, false, false, true>(pairs);
   return err;
+}
+
+cudaError_t launch_mx_up_scales(const FfnShape& s, const uint8_t* gate_up_s, uint8_t* up_s, cudaStream_t st) {
+  const size_t words = mx_scale_bytes(s.I, s.d) / 4;
+  shift_scales_kernel<<<(unsigned)((words + 255) / 256), 256, 0, st>>>(
+      reinterpret_cast<const uint32_t*>(gate_up_s), reinterpret_cast<uint32_t*>(up_s), s.I, s.I, (int)mx_tile_cols(s.d),
+      words);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const FfnForwardArgs& a, const uint8_t* up_s,
+                                  uint8_t* hq, uint8_t* hs, cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.I;
+  p.K = s.d;
+  p.act = s.act;
+  p.hq = hq;
+  p.hs = hs;
+  const uint64_t tiles = (s.I + 127) / 128;
+  if (!make_scale_map(e.encode, &p.as, a.xs, s.d, (s.T + 127) / 128) ||
+      !make_scale_map(e.encode, &p.bs0, a.gate_up_s, s.d, tiles) || !make_scale_map(e.encode, &p.bs1, up_s, s.d, tiles))
+    return cudaErrorInvalidValue;
+  return run<kEpiGateUp, false, false, true>(e, p, a.x, a.gate_up, 2 * (uint64_t)s.I, nullptr, st);
+}
+
+cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint8_t* hq, const uint8_t* hs,
+                               const FfnForwardArgs& a, cudaStream_t st) {
+  GemmParams p{};
+  p.M = s.T;
+  p.N = s.d;
+  p.K = s.I;
+  const uint64_t tiles = (s.d + 127) / 128;
+  if (!make_scale_map(e.encode, &p.as, hs, s.I, (s.T + 127) / 128) ||
+      !make_scale_map(e.encode, &p.bs0, a.down_s, s.I, tiles))
+    return cudaErrorInvalidValue;
+  p.bs1 = p.bs0;
+  return run<kEpiStore, false, false, true>(e, p, hq, a.down, s.d, a.y, st);
 }
 
 cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void* x, const void* gate_up, uint16_t* h,
@@ -526,7 +728,7 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
   if (pre && (!make_map(e.encode, &p.out_g, pre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
               !make_map(e.encode, &p.out_u, pre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32)))
     return cudaErrorInvalidValue;
-  return run<kEpiGateUp, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
+  return run<kEpiGateUp, false, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
 }
 
 cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
@@ -535,7 +737,7 @@ cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_
   p.M = s.T;
   p.N = s.d;
   p.K = s.I;
-  return run<kEpiStore, false, false>(e, p, h, down, s.d, y, st);
+  return run<kEpiStore, false, false, false>(e, p, h, down, s.d, y, st);
 }
 
 cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint16_t* dy, const uint16_t* down,
@@ -549,7 +751,7 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint1
   if (!make_map(e.encode, &p.out_g, dpre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
       !make_map(e.encode, &p.out_u, dpre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32))
     return cudaErrorInvalidValue;
-  return run<kEpiGrad, false, true>(e, p, dy, down, s.I, h, st);
+  return run<kEpiGrad, false, true, false>(e, p, dy, down, s.I, h, st);
 }
 
 cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t* dpre, const uint16_t* gate_up,
@@ -558,7 +760,7 @@ cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t*
   p.M = s.T;
   p.N = s.d;
   p.K = 2 * s.I;
-  return run<kEpiStore, false, true>(e, p, dpre, gate_up, s.d, dx, st);
+  return run<kEpiStore, false, true, false>(e, p, dpre, gate_up, s.d, dx, st);
 }
 
 cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
@@ -567,7 +769,7 @@ cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M,
   p.M = M;
   p.N = N;
   p.K = T;
-  return run<kEpiStore, true, true>(e, p, a, b, N, dw, st);
+  return run<kEpiStore, true, true, false>(e, p, a, b, N, dw, st);
 }
 
 }  // namespace moe

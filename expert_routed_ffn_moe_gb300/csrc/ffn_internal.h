@@ -119,6 +119,7 @@ struct FfnScratch {
   uint16_t* h;       // [max_tokens, I] bf16 act(gate) * up
   uint8_t* hq;       // the same as mx8 codes
   uint8_t* hs;       // and scales
+  uint8_t* up_s;     // [I, d] scales of the up weights, where launch_mx_up_scales is needed
   uint16_t* dpre;    // [max_tokens, 2 I] bf16 gradients of the pre-activations (training)
   unsigned* status;  // device status word
 };
@@ -148,8 +149,13 @@ cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t*
 cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
                                    uint16_t* dw, cudaStream_t st);
 
-// ffn_simple.cu
-cudaError_t launch_simple_forward(const FfnShape& s, bool mx, const FfnForwardArgs& a, const FfnScratch& sc,
-                                  cudaStream_t st);
+// mx8.  up_s: the scales of gate_up's rows I .. 2I - 1 as a matrix of their own:
+// where I is a multiple of 128 they are one inside gate_up_s, else
+// launch_mx_up_scales lays them out.
+cudaError_t launch_mx_up_scales(const FfnShape& s, const uint8_t* gate_up_s, uint8_t* up_s, cudaStream_t st);
+cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const FfnForwardArgs& a, const uint8_t* up_s,
+                                  uint8_t* hq, uint8_t* hs, cudaStream_t st);
+cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint8_t* hq, const uint8_t* hs,
+                               const FfnForwardArgs& a, cudaStream_t st);
 
 }  // namespace moe
