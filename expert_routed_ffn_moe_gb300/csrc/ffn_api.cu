@@ -106,11 +106,12 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
   if (!(prop.major == 10 && prop.minor == 3)) return MOE_ERR_UNSUPPORTED;
 
   FfnEngine eng{};
+  eng.sms = prop.multiProcessorCount;
   eng.pairs = prop.multiProcessorCount / 2;
   eng.ctl.spin_limit = kDefaultSpinNs;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
-  if (prepare_ffn_gemm(&eng.pairs) != cudaSuccess || eng.pairs < 1 ||
+  if (prepare_ffn_gemm(&eng.pairs) != cudaSuccess || eng.pairs < 1 || prepare_ffn_skinny() != cudaSuccess ||
       cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
       q != cudaDriverEntryPointSuccess || !fn) {
     cudaGetLastError();
@@ -126,6 +127,9 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return o;
   };
   const size_t o_status = take(16);
+  const size_t o_tickets = take((size_t)skinny_tickets(c.d, c.inter) * 4);
+  const size_t zeroed = off;
+  const size_t o_parts = take(skinny_part_bytes(eng.sms, c.max_tokens));
   const size_t o_h = take(mx ? 0 : T * I * 2);
   const size_t o_hq = take(mx ? T * I : 0);
   const size_t o_hs = take(mx ? mx_scale_bytes(T, I) : 0);
@@ -140,8 +144,8 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return MOE_ERR_NOMEM;
   }
   char* b = static_cast<char*>(ctx->block);
-  // the status word, and the scale bytes past the last row and group, which no kernel writes
-  if (cudaMemset(b + o_status, 0, 16) != cudaSuccess ||
+  // the status word, the tickets, and the scale bytes past the last row and group, which no kernel writes
+  if (cudaMemset(b, 0, zeroed) != cudaSuccess ||
       (mx && cudaMemset(b + o_hs, 0, mx_scale_bytes(T, I)) != cudaSuccess) || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     cudaFree(ctx->block);
@@ -149,6 +153,8 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return MOE_ERR_CUDA;
   }
   ctx->sc.status = reinterpret_cast<unsigned*>(b + o_status);
+  ctx->sc.tickets = reinterpret_cast<unsigned*>(b + o_tickets);
+  ctx->sc.parts = reinterpret_cast<float*>(b + o_parts);
   ctx->sc.h = reinterpret_cast<uint16_t*>(b + o_h);
   ctx->sc.hq = reinterpret_cast<uint8_t*>(b + o_hq);
   ctx->sc.hs = reinterpret_cast<uint8_t*>(b + o_hs);
@@ -192,21 +198,26 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const FfnScratch& sc = ctx->sc;
   cudaError_t err = cudaSuccess;
+  const uint8_t* up_s = nullptr;
   if (mx) {
-    const uint8_t* up_s = a.gate_up_s + mx_scale_bytes(s.I, s.d);  // row tile I / 128 on
+    up_s = a.gate_up_s + mx_scale_bytes(s.I, s.d);  // row tile I / 128 on
     if (s.I % 128 != 0) {
       err = launch_mx_up_scales(s, a.gate_up_s, sc.up_s, st);
       ++ctx->launches;
       up_s = sc.up_s;
     }
-    if (err == cudaSuccess) err = launch_ffn_gate_up_mx(ctx->eng, s, a, up_s, sc.hq, sc.hs, st);
-    if (err == cudaSuccess) err = launch_ffn_down_mx(ctx->eng, s, sc.hq, sc.hs, a, st);
-    ctx->launches += 2;
-    return cuda_code(err);
   }
+  if (err != cudaSuccess) return cuda_code(err);
   ctx->launches += 2;
-  err = launch_ffn_gate_up(ctx->eng, s, x, gate_up, sc.h, static_cast<uint16_t*>(pre), st);
-  if (err == cudaSuccess) err = launch_ffn_down(ctx->eng, s, sc.h, down, y, st);
+  if (T <= kSkinnyTokens) {
+    err = launch_skinny_forward(ctx->eng, s, mx, a, up_s, sc, st);
+  } else if (mx) {
+    err = launch_ffn_gate_up_mx(ctx->eng, s, a, up_s, sc.hq, sc.hs, st);
+    if (err == cudaSuccess) err = launch_ffn_down_mx(ctx->eng, s, sc.hq, sc.hs, a, st);
+  } else {
+    err = launch_ffn_gate_up(ctx->eng, s, x, gate_up, sc.h, static_cast<uint16_t*>(pre), st);
+    if (err == cudaSuccess) err = launch_ffn_down(ctx->eng, s, sc.h, down, y, st);
+  }
   return cuda_code(err);
 }
 
@@ -256,7 +267,10 @@ int moe_ffn_status(moe_ffn* ctx) {
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   unsigned v = 0;
   if (cudaMemcpy(&v, ctx->sc.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  if (v && cudaMemset(ctx->sc.status, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
+  // a launch that gave up may have left arrivals in the tickets
+  if (v && (cudaMemset(ctx->sc.status, 0, 4) != cudaSuccess ||
+            cudaMemset(ctx->sc.tickets, 0, (size_t)skinny_tickets(ctx->cfg.d, ctx->cfg.inter) * 4) != cudaSuccess))
+    return MOE_ERR_CUDA;
   return v & kStatusTimeout ? MOE_ERR_TIMEOUT : (v & kStatusBounds ? MOE_ERR_BOUNDS : MOE_OK);
 }
 

@@ -166,22 +166,10 @@ MOE_DEV void mma_pair_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uin
       "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor of the block-scaled form: e4m3 A and B (K-major), e8m0
-// scales, byte `id` of each row's four.
-__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int id) {
-  return (static_cast<uint32_t>(id) << 4)          // scale byte of B
-         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
-         | (1u << 23)                              // e8m0 scales
-         | (static_cast<uint32_t>(M >> 4) << 24)   // M / 16
-         | (static_cast<uint32_t>(id) << 29);      // scale byte of A
-}
 // 512 bytes of scales (32 rows of 16 bytes) from the same place in both CTAs'
 // shared memory into 4 TMEM columns, repeated for the four lane quarters.
 MOE_DEV void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
-  uint64_t d = 0;  // no swizzle, 8-row groups of 128 bytes
-  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
-  d |= static_cast<uint64_t>(128 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
+  const uint64_t d = mx_scale_desc(saddr);
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 // One 512-byte scale tile, counted on a barrier of the pair's first CTA.
@@ -347,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_pair_mx(d, da + j * 2, db + j * 2, idesc_mx(2 * kBM, kBN, j), ts, ts + 4, (kb | j) != 0);
+              mma_pair_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(2 * kBM, kBN, j), ts, ts + 4, (kb | j) != 0);
           } else {
 #pragma unroll
             for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, (kb | j) != 0);
@@ -576,52 +564,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// A 2-D bf16 map: `inner` contiguous elements per row, rows `pitch` elements apart.
-bool make_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
-              uint32_t box_inner, uint32_t box_outer) {
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {pitch * 2};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// mx8 codes [rows, K]; and scale tiles as [row tile][column tile][64 x 8 bytes].
-bool make_code_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows) {
-  const cuuint64_t dims[2] = {K, rows};
-  const cuuint64_t strides[1] = {K};
-  const cuuint32_t box[2] = {kRowBytes, 128};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t row_tiles) {
-  const uint64_t tile_cols = mx_tile_cols(cols);
-  const cuuint64_t dims[3] = {64, tile_cols, row_tiles};
-  const cuuint64_t strides[2] = {512, 512 * tile_cols};
-  const cuuint32_t box[3] = {64, 1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b, uint64_t b_rows, void* out,
                 cudaStream_t st) {
   bool ok;
   if (MX) {
-    ok = make_code_map(e.encode, &p.a, a, p.K, p.M) && make_code_map(e.encode, &p.b, b, p.K, b_rows);
+    ok = make_code_map(e.encode, &p.a, a, p.K, p.M, 128) && make_code_map(e.encode, &p.b, b, p.K, b_rows, 128);
   } else {  // a K-major operand is [rows, K], an MN-major one [K, rows]
-    ok = A_MN ? make_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK)
-              : make_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
-    ok = ok && (B_MN ? make_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
-                     : make_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
+    ok = A_MN ? make_bf16_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK)
+              : make_bf16_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
+    ok = ok && (B_MN ? make_bf16_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
+                     : make_bf16_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
   }
-  ok = ok && (!out || make_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
+  ok = ok && (!out || make_bf16_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
   if (!ok) return cudaErrorInvalidValue;
   p.ctl = e.ctl;
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
@@ -725,8 +680,8 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
   p.K = s.d;
   p.act = s.act;
   p.store_pre = pre != nullptr;
-  if (pre && (!make_map(e.encode, &p.out_g, pre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
-              !make_map(e.encode, &p.out_u, pre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32)))
+  if (pre && (!make_bf16_map(e.encode, &p.out_g, pre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
+              !make_bf16_map(e.encode, &p.out_u, pre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32)))
     return cudaErrorInvalidValue;
   return run<kEpiGateUp, false, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
 }
@@ -748,8 +703,8 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint1
   p.K = s.d;
   p.act = s.act;
   p.pre = pre;
-  if (!make_map(e.encode, &p.out_g, dpre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
-      !make_map(e.encode, &p.out_u, dpre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32))
+  if (!make_bf16_map(e.encode, &p.out_g, dpre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
+      !make_bf16_map(e.encode, &p.out_u, dpre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32))
     return cudaErrorInvalidValue;
   return run<kEpiGrad, false, true, false>(e, p, dy, down, s.I, h, st);
 }

@@ -54,6 +54,31 @@ MOE_DEV uint32_t e4m3x2(float lo, float hi) {
 }
 MOE_DEV uint32_t e4m3x4(float a, float b, float c, float d) { return e4m3x2(a, b) | (e4m3x2(c, d) << 16); }
 
+// Instruction descriptor of the block-scaled form: e4m3 A and B (K-major), e8m0
+// scales, byte `id` of each row's four.
+__host__ __device__ constexpr uint32_t umma_idesc_mx(int M, int N, int id) {
+  return (static_cast<uint32_t>(id) << 4)          // scale byte of B
+         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+         | (1u << 23)                              // e8m0 scales
+         | (static_cast<uint32_t>(M >> 4) << 24)   // M / 16
+         | (static_cast<uint32_t>(id) << 29);      // scale byte of A
+}
+// Descriptor of 512 bytes of scales in shared memory, the source of tcgen05.cp:
+// no swizzle, 8-row groups of 128 bytes.
+MOE_DEV uint64_t mx_scale_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+// 16 consecutive fp32 columns of this thread's TMEM lane, valid after tmem_ld_wait().
+MOE_DEV void tmem_ld16_async(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- activations
 // silu(g) = g sigmoid(g); gelu in its tanh form, 0.5 g (1 + tanh z) =
 // g sigmoid(2 z): both from the fast exponential and division of sigmoid
@@ -121,6 +146,8 @@ struct FfnScratch {
   uint8_t* hs;       // and scales
   uint8_t* up_s;     // [I, d] scales of the up weights, where launch_mx_up_scales is needed
   uint16_t* dpre;    // [max_tokens, 2 I] bf16 gradients of the pre-activations (training)
+  float* parts;      // few tokens: partial sums of row tiles shared by several CTAs
+  unsigned* tickets; // few tokens: arrivals per row tile
   unsigned* status;  // device status word
 };
 
@@ -129,8 +156,43 @@ struct FfnScratch {
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// A 2-D bf16 map: `inner` contiguous elements per row, rows `pitch` elements apart.
+inline bool make_bf16_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
+                          uint64_t pitch, uint32_t box_inner, uint32_t box_outer) {
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {pitch * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// mx8 codes [rows, K]; and scale tiles as [row tile][column tile][64 x 8 bytes].
+inline bool make_code_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t K, uint64_t rows,
+                          uint32_t box_rows) {
+  const cuuint64_t dims[2] = {K, rows};
+  const cuuint64_t strides[1] = {K};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t row_tiles) {
+  const uint64_t tile_cols = mx_tile_cols(cols);
+  const cuuint64_t dims[3] = {64, tile_cols, row_tiles};
+  const cuuint64_t strides[2] = {512, 512 * tile_cols};
+  const cuuint32_t box[3] = {64, 1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct FfnEngine {
   EncodeTiledFn encode;
+  int sms;
   int pairs;  // CTA pairs that run at a time
   DevCtl ctl;
 };
@@ -157,5 +219,13 @@ cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const F
                                   uint8_t* hq, uint8_t* hs, cudaStream_t st);
 cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint8_t* hq, const uint8_t* hs,
                                const FfnForwardArgs& a, cudaStream_t st);
+
+// ffn_skinny.cu: the whole forward call for few tokens
+constexpr int kSkinnyTokens = 64;
+size_t skinny_part_bytes(int sms, int tokens);
+int skinny_tickets(int d, int inter);
+cudaError_t prepare_ffn_skinny();
+cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
+                                  const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);
 
 }  // namespace moe

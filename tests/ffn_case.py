@@ -23,11 +23,10 @@ def act(g, gelu):
 
 
 def act_grad(g, gelu):
-    if gelu:
-        t = torch.tanh(C * (g + 0.044715 * g ** 3))
-        return 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * C * (1 + 3 * 0.044715 * g * g)
-    s = torch.sigmoid(g)
-    return s * (1 + g * (1 - s))
+    # 0.5 (1 + tanh z) = sigmoid(2 z): the form whose far negative tail does not cancel
+    s = torch.sigmoid(2 * C * (g + 0.044715 * g ** 3) if gelu else g)
+    inner = 2 * C * (1 + 3 * 0.044715 * g * g) if gelu else 1.0
+    return s * (1 + g * (1 - s) * inner)
 
 
 def product_bound(a, b, rounded, extra=2.0 ** -18):
