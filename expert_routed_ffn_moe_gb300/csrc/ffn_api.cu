@@ -127,9 +127,6 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return o;
   };
   const size_t o_status = take(16);
-  const size_t o_tickets = take((size_t)skinny_tickets(c.d, c.inter) * 4);
-  const size_t zeroed = off;
-  const size_t o_parts = take(skinny_part_bytes(eng.sms, c.max_tokens));
   const size_t o_h = take(mx ? 0 : T * I * 2);
   const size_t o_hq = take(mx ? T * I : 0);
   const size_t o_hs = take(mx ? mx_scale_bytes(T, I) : 0);
@@ -144,8 +141,8 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return MOE_ERR_NOMEM;
   }
   char* b = static_cast<char*>(ctx->block);
-  // the status word, the tickets, and the scale bytes past the last row and group, which no kernel writes
-  if (cudaMemset(b, 0, zeroed) != cudaSuccess ||
+  // the status word, and the scale bytes past the last row and group, which no kernel writes
+  if (cudaMemset(b + o_status, 0, 16) != cudaSuccess ||
       (mx && cudaMemset(b + o_hs, 0, mx_scale_bytes(T, I)) != cudaSuccess) || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     cudaFree(ctx->block);
@@ -153,8 +150,6 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
     return MOE_ERR_CUDA;
   }
   ctx->sc.status = reinterpret_cast<unsigned*>(b + o_status);
-  ctx->sc.tickets = reinterpret_cast<unsigned*>(b + o_tickets);
-  ctx->sc.parts = reinterpret_cast<float*>(b + o_parts);
   ctx->sc.h = reinterpret_cast<uint16_t*>(b + o_h);
   ctx->sc.hq = reinterpret_cast<uint8_t*>(b + o_hq);
   ctx->sc.hs = reinterpret_cast<uint8_t*>(b + o_hs);
@@ -267,10 +262,7 @@ int moe_ffn_status(moe_ffn* ctx) {
   if (cudaDeviceSynchronize() != cudaSuccess) return MOE_ERR_CUDA;
   unsigned v = 0;
   if (cudaMemcpy(&v, ctx->sc.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-  // a launch that gave up may have left arrivals in the tickets
-  if (v && (cudaMemset(ctx->sc.status, 0, 4) != cudaSuccess ||
-            cudaMemset(ctx->sc.tickets, 0, (size_t)skinny_tickets(ctx->cfg.d, ctx->cfg.inter) * 4) != cudaSuccess))
-    return MOE_ERR_CUDA;
+  if (v && cudaMemset(ctx->sc.status, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
   return v & kStatusTimeout ? MOE_ERR_TIMEOUT : (v & kStatusBounds ? MOE_ERR_BOUNDS : MOE_OK);
 }
 

@@ -97,23 +97,6 @@ static_assert(smem_of(kEpiStore, false) <= 227 * 1024 && smem_of(kEpiGateUp, fal
                   smem_of(kEpiStore, true) <= 227 * 1024 && smem_of(kEpiGateUp, true) <= 227 * 1024,
               "shared memory of one CTA");
 
-MOE_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-MOE_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Address of `p` (this CTA's shared memory) in the pair's CTA `rank`.
-MOE_DEV uint32_t map_cta(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-MOE_DEV void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }

@@ -79,6 +79,25 @@ MOE_DEV void tmem_ld16_async(uint32_t taddr, float (&r)[16]) {
       : "memory");
 }
 
+// ---------------------------------------------------------------- clusters
+MOE_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of `p` (this CTA's shared memory) in the cluster's CTA `rank`.
+MOE_DEV uint32_t map_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+MOE_DEV void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ---------------------------------------------------------------- activations
 // silu(g) = g sigmoid(g); gelu in its tanh form, 0.5 g (1 + tanh z) =
 // g sigmoid(2 z): both from the fast exponential and division of sigmoid
@@ -146,8 +165,6 @@ struct FfnScratch {
   uint8_t* hs;       // and scales
   uint8_t* up_s;     // [I, d] scales of the up weights, where launch_mx_up_scales is needed
   uint16_t* dpre;    // [max_tokens, 2 I] bf16 gradients of the pre-activations (training)
-  float* parts;      // few tokens: partial sums of row tiles shared by several CTAs
-  unsigned* tickets; // few tokens: arrivals per row tile
   unsigned* status;  // device status word
 };
 
@@ -222,8 +239,6 @@ cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint
 
 // ffn_skinny.cu: the whole forward call for few tokens
 constexpr int kSkinnyTokens = 64;
-size_t skinny_part_bytes(int sms, int tokens);
-int skinny_tickets(int d, int inter);
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);

@@ -398,8 +398,7 @@ long long moe_ffn_launch_count(moe_ffn* ctx);
 int moe_ffn_set_spin_limit(moe_ffn* ctx, long long limit);
 int moe_ffn_inject_stall(moe_ffn* ctx, int on);
 
-/* As moe_status, for a moe_ffn context.  After a timeout the context is usable
- * again only once this has reported it. */
+/* As moe_status, for a moe_ffn context. */
 int moe_ffn_status(moe_ffn* ctx);
 
 /* Free the context and its workspace (synchronises the device first).  NULL is
