@@ -12,8 +12,10 @@
 // computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA loads its
 // own 128 rows of A and half of B's 256 rows, so a 64-deep k block costs each
 // SM 32 KB of shared-memory fill for 256 cycles of MMA (a lone CTA's 128 x 256
-// tile takes 48 KB for the same work).  Per CTA 10 warps:
-//   warp 0     TMA producer (one thread) of a ring of k blocks, 128-byte swizzle;
+// tile takes 48 KB for the same work).  Per CTA 11 warps (12 for mx8):
+//   warps 0, 10, 11  TMA producers (one thread each) of a ring of k blocks,
+//              128-byte swizzle: A, B, and mx8's scales.  One thread alone takes
+//              longer for all of a k block's copies than its MMAs do;
 //   warp 1     allocates all 512 TMEM columns: two fp32 accumulators of 256
 //              columns; in the pair's first CTA one thread issues the MMAs;
 //   warps 2-9  epilogue: two warps for each quarter of the TMEM lanes, each
@@ -50,7 +52,8 @@ constexpr int kBK = 64;                     // k block of bf16
 constexpr int kOpBytes = 128 * kRowBytes;   // one operand's half tile: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kBWarp = 2 + kEpiWarps, kScaleWarp = kBWarp + 1;  // producers of B and of the scales (A: warp 0)
+constexpr int threads_of(bool mx) { return (mx ? kScaleWarp + 1 : kBWarp + 1) * 32; }
 constexpr int kStoreBytes = 32 * 128;       // staging tile: 32 rows x 64 bf16
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
@@ -85,7 +88,7 @@ struct __align__(8) Bars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t peer_issued;  // first CTA, after an abort: k blocks that the other CTA has loaded
+  uint32_t issued[2][3];  // k blocks loaded by each CTA's producers of A, B and scales (first CTA: both's)
   uint32_t peer_abort;
 };
 
@@ -189,7 +192,7 @@ MOE_DEV void stage16(uint8_t* tile, int lane, int c, uint4 v) {
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool MX>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = stages_of(EPI, MX), NB = buffers_of(EPI, MX);
   constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
@@ -219,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar->mma_done, 1);
     bar->abort_flag = 0;
-    bar->peer_issued = bar->peer_abort = 0;
+    bar->peer_abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -232,13 +235,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
-  int issued = 0;  // producer thread: k blocks loaded
 
-  if (warp == 0) {
+  if (warp == 0 || warp >= kBWarp) {
     if (lane == 0) {
-      tma_prefetch_desc(&p.a);
-      tma_prefetch_desc(&p.b);
+      const int role = warp == 0 ? 0 : warp - kBWarp + 1;  // A, B, scales
+      tma_prefetch_desc(role == 0 ? &p.a : role == 1 ? &p.b : &p.as);
       bool ok = true;
+      int issued = 0;
       for (int t = pair; t < tiles && ok; t += pairs) {
         int m, n;
         tile_of(t, mt, nt, m, n);
@@ -252,24 +255,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kTx);
           const uint32_t fb = map_cta(&bar->full[st], 0);
           uint8_t* a = base + st * kStageBytes;
           uint8_t* b = a + kOpBytes;
           const int k = kb * kDepth;
-          if (A_MN) {
-            tma_load_pair(a, &p.a, arow, k, fb);
-            tma_load_pair(a + kOpBytes / 2, &p.a, arow + 64, k, fb);
-          } else {
-            tma_load_pair(a, &p.a, k, arow, fb);
-          }
-          if (B_MN) {
-            tma_load_pair(b, &p.b, brow, k, fb);
-            tma_load_pair(b + kOpBytes / 2, &p.b, brow + 64, k, fb);
-          } else {
-            tma_load_pair(b, &p.b, k, brow, fb);
-          }
-          if (MX) {
+          if (role == 0) {
+            if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kTx);  // everything, both CTAs'
+            if (A_MN) {
+              tma_load_pair(a, &p.a, arow, k, fb);
+              tma_load_pair(a + kOpBytes / 2, &p.a, arow + 64, k, fb);
+            } else {
+              tma_load_pair(a, &p.a, k, arow, fb);
+            }
+          } else if (role == 1) {
+            if (B_MN) {
+              tma_load_pair(b, &p.b, brow, k, fb);
+              tma_load_pair(b + kOpBytes / 2, &p.b, brow + 64, k, fb);
+            } else {
+              tma_load_pair(b, &p.b, k, brow, fb);
+            }
+          } else if (MX) {
             uint8_t* sc = scales + st * kScaleBytes;
             tma_load_scales_pair(sc, &p.as, kb, 2 * m + (int)rank, fb);
             tma_load_scales_pair(sc + 512, &p.bs0, kb, EPI == kEpiGateUp ? n : 2 * n, fb);
@@ -278,12 +283,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++issued;
         }
       }
+      bar->issued[rank][role] = issued;
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       int it = 0, lt = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
         set_abort(bar);
         ok = false;
@@ -302,11 +308,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + acc * (MX ? kBN - kSharedCols : kBN);
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int st = it % S;
-          if (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar)) {
+          if (!ready && (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar))) {
             set_abort(bar);
             ok = false;
             break;
           }
+          // asked for before this block's MMAs: a load from shared memory queues behind their operand reads
+          ready = mbar_try_wait(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
           tc_fence_after();
           const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
           const uint64_t da = A_MN ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
@@ -520,24 +528,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Leave together: the other CTA's shared memory is the target of remote
   // arrivals and of the MMAs' reads.  On the normal path every copy has landed
   // (an MMA waited for it).  After an abort copies may be in flight: the second
-  // CTA reports how many k blocks it has loaded, and the first waits for both
-  // CTAs' copies block by block -- a barrier that expects a half that was never
-  // issued is credited with it.
+  // CTA reports what its producers have issued, and the first waits for both
+  // CTAs' copies block by block, crediting a barrier with what never was.
+  constexpr int kRoles = MX ? 3 : 2;
   if (threadIdx.x == 0 && rank == 1) {
-    store_cluster(map_cta(&bar->peer_issued, 0), (uint32_t)issued);
+    for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], 0), bar->issued[1][r]);
     store_cluster(map_cta(&bar->peer_abort, 0), (uint32_t)bar->abort_flag);
   }
   cluster_sync();
   if (threadIdx.x == 0 && rank == 0 && (bar->abort_flag || bar->peer_abort)) {
     DevCtl drain = p.ctl;
     drain.spin_limit = 1000000000LL;
-    const int theirs = (int)bar->peer_issued, most = max(issued, theirs);
+    constexpr uint32_t bytes[3] = {kOpBytes, kOpBytes, kScaleBytes};
+    int most = 0;
+    for (int r = 0; r < 2 * kRoles; ++r) most = max(most, (int)bar->issued[r / kRoles][r % kRoles]);
     for (int j = max(0, most - S); j < most; ++j) {
       uint64_t* fb = &bar->full[j % S];
-      if (j >= issued) mbar_expect_tx(fb, kTx);  // only the other CTA's half was issued
-      if (j >= theirs)                                   // only this CTA's half was issued
+      uint32_t missing = 0;
+      for (int r = 0; r < 2 * kRoles; ++r)
+        if (j >= (int)bar->issued[r / kRoles][r % kRoles]) missing += bytes[r % kRoles];
+      if (j >= (int)bar->issued[0][0]) mbar_expect_tx(fb, 2 * kTx);
+      if (missing)
         asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, 0)),
-                     "r"(kTx)
+                     "r"(missing)
                      : "memory");
       mbar_wait(fb, (j / S) & 1, drain);
     }
@@ -566,7 +579,7 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
   const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
-  ffn_gemm_kernel<EPI, A_MN, B_MN, MX><<<2 * pairs, kThreads, smem_of(EPI, MX), st>>>(p);
+  ffn_gemm_kernel<EPI, A_MN, B_MN, MX><<<2 * pairs, threads_of(MX), smem_of(EPI, MX), st>>>(p);
   return cudaGetLastError();
 }
 
@@ -577,7 +590,7 @@ cudaError_t prepare(int* pairs) {
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(MX));
   cfg.dynamicSmemBytes = smem_of(EPI, MX);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;

@@ -4,9 +4,16 @@
 // The weight rows are the tensor cores' 128 rows and the tokens their N columns
 // (D[row, token] = W x^T, N = T rounded up to 16, 32 or 64), so no MMA work and
 // no shared memory goes to rows that do not exist, and one multiply per weight
-// row block serves every token.  Warp 0 streams 128 x 128-byte weight blocks
-// and the matching x block through a TMA ring, warp 1 issues the MMAs, warps
-// 2-5 read the accumulators (one weight row per thread).
+// row block serves every token.  128 x 128-byte weight blocks and the matching x
+// blocks go through a TMA ring.  A thread takes ~0.3 us to wait for a stage and
+// to issue its copies, about as long as 16 KB take at an SM's share of the
+// memory rate, so four warps share that: 0 and 6 bring the even and odd steps'
+// weights, 7 and 8 their x blocks.  Warps 1 and 9 issue the even and odd steps'
+// MMAs, into accumulators of their own: a wait for a stage queues behind the
+// shared-memory operand reads of the MMAs before it, and one thread alone got
+// through 16 KB per 0.30 us (0.40 us with mx8's scales), less than an SM's share
+// of the memory rate.  Warps 2-5 read the accumulators (one weight row per
+// thread).
 //
 // A tile of 128 weight rows belongs to a cluster of up to 8 CTAs, each of which
 // streams a contiguous part of the row's length, so that about every SM has a
@@ -19,10 +26,11 @@
 // rows alternate into two accumulators, and the activation, the product and
 // h's rounding (with mx8: a group of 32 neurons is one warp) finish here.
 //
-// The two kernels overlap by programmatic launch.  Once every gate/up CTA has
-// asked for its last weights, the down kernel's CTAs start beside them (two fit
-// an SM), fill their rings, pull the rest of their weights into L2, and only
-// then wait for h: memory is busy while the gate/up product is summed up.
+// The two kernels overlap by programmatic launch: the down kernel's CTAs start
+// beside the gate/up kernel's (one of each fits an SM), fill their rings with
+// weights and only then wait for h.  A gate/up CTA that has asked for its last
+// weights pulls its share of down's into L2, so memory stays busy while the
+// gate/up product is summed up.
 #include "ffn_internal.h"
 
 namespace moe {
@@ -30,45 +38,50 @@ namespace {
 
 constexpr int kRows = 128;                 // weight rows of a tile
 constexpr int kBlockBytes = kRows * 128;   // a weight block: 128 rows x 128 bytes of k
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kMaxCluster = 8;
-// a gate/up CTA and a down CTA share an SM (228 KB, 1 KB of it the system's for each)
-constexpr int kSmemGate = 126 * 1024, kSmemDown = 100 * 1024;
+constexpr int kMaxStages = 6;
 
 struct SkinnyParams {
   CUtensorMap w, x;                // weights [rows, K]; x or h [T, K]
+  CUtensorMap next;                // gate/up: the weights of down, [next_rows, next_K]
+  int next_rows, next_K;
   CUtensorMap ws, us, xs;          // mx8 scales: of the rows (gate), of the up rows, of x or h
   uint16_t *h, *pre, *y;
   uint8_t *hq, *hs;
   int T, N, K;                     // N: neurons (gate/up) or rows of down
   int act;
+  int log_cluster;                 // CTAs per tile: 1 << log_cluster
   DevCtl ctl;
 };
 
 constexpr int stage_bytes(bool mx, int nt) { return kBlockBytes + nt * 128 + (mx ? 1024 : 0); }
 constexpr int exchange_bytes(bool gate, int nt) { return nt * (gate ? 2 : 1) * kRows * 4; }
-constexpr int stages_of(bool mx, bool gate, int nt) {
-  if (nt > 32) return 4;  // one CTA per SM
-  const int n = ((gate ? kSmemGate : kSmemDown) - 2048 - exchange_bytes(gate, nt)) / stage_bytes(mx, nt);
-  return n > 8 ? 8 : n;
-}
-constexpr uint32_t tmem_cols(bool mx, bool gate, int nt) {
-  const int need = (gate ? 2 : 1) * nt + (mx ? 16 : 0);
+// Stages of the ring.  An even number: the even and the odd steps then have
+// stages of their own, so that each stage's phases are waited for by one thread
+// in their order (a wait by parity for a phase after the next would return at
+// once).  Up to 32 tokens a gate/up and a down CTA fit an SM together.
+constexpr int stages_of(bool gate, int nt) { return nt <= 16 ? (gate ? 6 : 4) : nt <= 32 ? 4 : 6; }
+constexpr uint32_t tmem_cols(bool mx, int nt) {
+  const int need = 2 * nt + (mx ? 16 : 0);
   return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
 }
 
 struct __align__(8) Bars {
-  uint64_t full[8], empty[8], tfull, mma_done;
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull, mma_done;
   uint64_t parts;  // all parts of this CTA's tokens have been pushed here
   uint32_t tmem_base;
   int abort_flag;
+  int issued[2][2];  // by the producers of weights and of tokens, of even and odd steps
 };
 constexpr size_t smem_of(bool mx, bool gate, int nt) {
-  return 1024 + (size_t)stages_of(mx, gate, nt) * stage_bytes(mx, nt) + exchange_bytes(gate, nt) + sizeof(Bars);
+  return 1024 + (size_t)stages_of(gate, nt) * stage_bytes(mx, nt) + exchange_bytes(gate, nt) + sizeof(Bars);
 }
-static_assert(smem_of(false, true, 32) <= kSmemGate && smem_of(true, true, 32) <= kSmemGate &&
-                  smem_of(false, false, 32) <= kSmemDown && smem_of(true, false, 32) <= kSmemDown &&
-                  smem_of(true, true, 64) <= 227 * 1024 && stages_of(true, false, 32) >= 3,
+constexpr bool share_an_sm(bool mx, int nt) {  // 228 KB, 1 KB of it the system's for each CTA
+  return smem_of(mx, true, nt) + smem_of(mx, false, nt) + 2048 <= 228 * 1024;
+}
+static_assert(share_an_sm(false, 16) && share_an_sm(true, 16) && share_an_sm(false, 32) && share_an_sm(true, 32) &&
+                  smem_of(true, true, 64) <= 227 * 1024 && smem_of(true, false, 64) <= 227 * 1024,
               "shared memory");
 
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
@@ -108,11 +121,12 @@ MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const DevCtl& c) 
 }
 
 template <bool MX, bool GATE, int NT>
-__global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_constant__ SkinnyParams p) {
-  constexpr int S = stages_of(MX, GATE, NT), kStage = stage_bytes(MX, NT);
-  constexpr uint32_t kCols = tmem_cols(MX, GATE, NT);
+__global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_constant__ SkinnyParams p) {
+  static_assert(stages_of(GATE, NT) % 2 == 0 && stages_of(GATE, NT) <= kMaxStages, "see stages_of");
+  constexpr int S = stages_of(GATE, NT), kStage = stage_bytes(MX, NT);
+  constexpr uint32_t kCols = tmem_cols(MX, NT);
   constexpr int kDepth = MX ? 128 : 64;  // values of k per block
-  constexpr int kParts = GATE ? 2 : 1;   // accumulators, and weight blocks per k block
+  constexpr int kParts = GATE ? 2 : 1;   // weight blocks per k block
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // weight blocks, then x blocks, then scales (1024-byte aligned tiles first), then the exchange
@@ -122,20 +136,19 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
   Bars* bar = reinterpret_cast<Bars*>(base + S * kStage + exchange_bytes(GATE, NT));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t rank, C;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
-  const int unit = blockIdx.x / C;
+  const int rank = (int)cluster_rank(), C = 1 << p.log_cluster;
+  const int unit = blockIdx.x >> p.log_cluster;
   const int KB = (p.K + kDepth - 1) / kDepth;
-  const int kb0 = (int)((long long)rank * KB / C), steps = ((int)((long long)(rank + 1) * KB / C) - kb0) * kParts;
+  const int kb0 = (int)((long long)rank * KB >> p.log_cluster);
+  const int steps = ((int)((long long)(rank + 1) * KB >> p.log_cluster) - kb0) * kParts;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->full[i], 2);  // the weights' and the tokens' producer
       mbar_init(&bar->empty[i], 1);
     }
-    mbar_init(&bar->tfull, 1);
-    mbar_init(&bar->mma_done, 1);
+    mbar_init(&bar->tfull, 2);
+    mbar_init(&bar->mma_done, 2);
     mbar_init(&bar->parts, 4 * C);
     bar->abort_flag = 0;
     fence_mbar_init();
@@ -147,53 +160,53 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
   const uint32_t tmem = bar->tmem_base;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first push
 
-  if (warp == 0) {
+  if (warp == 0 || (warp > 5 && warp < 9)) {
     if (lane == 0) {
+      const bool tokens = warp > 6;
+      const int odd = warp == 6 || warp == 8 ? 1 : 0;
       const uint64_t once = policy_evict_first(), keep = policy_evict_last();
       const int row0 = unit * kRows;
-      auto weights = [&](int s) {  // the weight block of step s and its scales
+      auto load = [&](int s) {
         const int st = s % S, kb = kb0 + s / kParts, which = s % kParts;
-        mbar_expect_tx(&bar->full[st], kStage);
-        tma_load_2d(base + st * kBlockBytes, &p.w, kb * kDepth, row0 + which * p.N, &bar->full[st], once);
-        if (MX) tma_load_scales(sc0 + st * 1024, which ? &p.us : &p.ws, kb, unit, &bar->full[st]);
+        if (tokens) {
+          mbar_expect_tx(&bar->full[st], NT * 128 + (MX ? 512 : 0));
+          tma_load_2d(xs0 + st * NT * 128, &p.x, kb * kDepth, 0, &bar->full[st], keep);
+          if (MX) tma_load_scales(sc0 + st * 1024 + 512, &p.xs, kb, 0, &bar->full[st]);
+        } else {
+          mbar_expect_tx(&bar->full[st], kBlockBytes + (MX ? 512 : 0));
+          tma_load_2d(base + st * kBlockBytes, &p.w, kb * kDepth, row0 + which * p.N, &bar->full[st], once);
+          if (MX) tma_load_scales(sc0 + st * 1024, which ? &p.us : &p.ws, kb, unit, &bar->full[st]);
+        }
       };
-      auto tokens = [&](int s) {
-        const int st = s % S, kb = kb0 + s / kParts;
-        tma_load_2d(xs0 + st * NT * 128, &p.x, kb * kDepth, 0, &bar->full[st], keep);
-        if (MX) tma_load_scales(sc0 + st * 1024 + 512, &p.xs, kb, 0, &bar->full[st]);
-      };
-      const int ahead = steps < S ? steps : S;
-      // gate/up: the kernel before may have written anything; down: only h, so its weights come first
-      if (GATE) asm volatile("griddepcontrol.wait;" ::: "memory");
-      for (int s = 0; s < ahead; ++s) weights(s);
-      if (!GATE) {
-        for (int s = ahead; s < steps; ++s) tma_prefetch_2d(&p.w, (kb0 + s) * kDepth, row0);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-      }
-      for (int s = 0; s < ahead; ++s) tokens(s);
-      int s = ahead;
-      for (; s < steps; ++s) {
-        if (!mbar_wait(&bar->empty[s % S], ((s / S) & 1) ^ 1, p.ctl) || aborted(bar)) {
+      // gate/up: the kernel before may have written anything; down: only h, so its weights do not wait
+      if (GATE || tokens) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      int s = odd;
+      for (; s < steps; s += 2) {
+        if (s >= S && (!mbar_wait(&bar->empty[s % S], ((s / S) & 1) ^ 1, p.ctl) || aborted(bar))) {
           set_abort(bar);
           break;
         }
-        weights(s);
-        tokens(s);
+        load(s);
       }
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-      // the copies land before the CTA leaves
-      DevCtl drain = p.ctl;
-      drain.spin_limit = 1000000000LL;
-      for (int j = s > S ? s - S : 0; j < s; ++j) mbar_wait(&bar->full[j % S], (j / S) & 1, drain);
+      if (GATE && !tokens) {
+        const int nkb = (p.next_K + kDepth - 1) / kDepth, blocks = (p.next_rows + kRows - 1) / kRows * nkb;
+        for (int b = 2 * blockIdx.x + odd; b < blocks; b += 2 * gridDim.x)
+          tma_prefetch_2d(&p.next, b % nkb * kDepth, b / nkb * kRows);
+      }
+      if (!GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      bar->issued[tokens][odd] = s;  // steps odd, odd + 2, ... below s
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 9) {
     if (lane == 0) {
+      const int odd = warp == 9 ? 1 : 0;
       bool ok = true;
       if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
         set_abort(bar);
         ok = false;
       }
-      for (int s = 0; s < steps && ok; ++s) {
+      const uint32_t d = tmem + odd * NT;  // gate/up: even steps are gate blocks, odd ones up blocks
+      for (int s = odd; s < steps && ok; s += 2) {
         const int st = s % S;
         if (!mbar_wait(&bar->full[st], (s / S) & 1, p.ctl) || aborted(bar)) {
           set_abort(bar);
@@ -201,20 +214,19 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (s % kParts) * NT;
         const uint64_t da = umma_desc_sw128(smem_u32(base + st * kBlockBytes));
         const uint64_t db = umma_desc_sw128(smem_u32(xs0 + st * NT * 128));
         if (MX) {
-          const uint32_t ts = tmem + kParts * NT + (s & 1) * 8, sc = smem_u32(sc0 + st * 1024);
+          const uint32_t ts = tmem + 2 * NT + odd * 8, sc = smem_u32(sc0 + st * 1024);
           copy_scales(ts, sc);
           copy_scales(ts + 4, sc + 512);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(kRows, NT, j), ts, ts + 4, s >= kParts || j != 0);
+            mma_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(kRows, NT, j), ts, ts + 4, s > odd || j != 0);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_bf16(d, da + j * 2, db + j * 2, umma_idesc_bf16(kRows, NT), s >= kParts || j != 0);
+            umma_bf16(d, da + j * 2, db + j * 2, umma_idesc_bf16(kRows, NT), s > odd || j != 0);
         }
         umma_commit(&bar->empty[st]);
       }
@@ -226,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
   __syncwarp();
   // every CTA of the cluster has set up its barriers: pushes may begin
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (warp >= 2) {
+  if (warp >= 2 && warp <= 5) {
     const int part = warp & 3, row = part * 32 + lane;  // this thread's weight row of the tile
-    const int T = p.T, own = (T + (int)C - 1) / (int)C;  // tokens per CTA
+    const int T = p.T, own = (T + C - 1) >> p.log_cluster;  // tokens per CTA
     const int n = unit * kRows + row;
     const bool in = n < p.N;
     // token t's results: gate (or down) value v, up value u
@@ -263,8 +275,12 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
       for (int t0 = 0; t0 < T; t0 += 16) {
         float v[16], u[16];
         tmem_ld16_async(src + t0, v);
-        if (GATE) tmem_ld16_async(src + NT + t0, u);
+        tmem_ld16_async(src + NT + t0, u);
         tmem_ld_wait();
+        if (!GATE && steps > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += u[i];
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int t = t0 + i;
@@ -273,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
             finish(t, v[i], u[i]);
           } else {
             const uint32_t at =
-                map_cta(exchange + (((int)rank * own + t / (int)C) * kParts) * kRows + row, (uint32_t)t % C);
+                map_cta(exchange + ((rank * own + (t >> p.log_cluster)) * kParts) * kRows + row, t & (C - 1));
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[i]) : "memory");
             if (GATE) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + kRows * 4), "f"(u[i]) : "memory");
           }
@@ -282,16 +298,16 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
       if (C > 1) {
         asm volatile("fence.acq_rel.cluster;" ::: "memory");
         __syncwarp();
-        if (lane < (int)C) arrive_cluster(map_cta(&bar->parts, lane));
-        ok = (int)rank >= T || mbar_wait_cluster(&bar->parts, 0, p.ctl);
+        if (lane < C) arrive_cluster(map_cta(&bar->parts, lane));
+        ok = rank >= T || mbar_wait_cluster(&bar->parts, 0, p.ctl);
         if (!__all_sync(0xffffffffu, ok)) {
           set_abort(bar);
         } else {
-          for (int t = (int)rank, i = 0; t < T; t += (int)C, ++i) {
+          for (int t = rank, i = 0; t < T; t += C, ++i) {
             float v = 0.f, u = 0.f;
 #pragma unroll
             for (int c = 0; c < kMaxCluster; ++c)
-              if (c < (int)C) {
+              if (c < C) {
                 const float* q = exchange + ((c * own + i) * kParts) * kRows + row;
                 v += q[0];
                 if (GATE) u += q[kRows];
@@ -306,6 +322,20 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_skinny_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (threadIdx.x == 0 && bar->abort_flag) {
+    // After an abort copies may be in flight (otherwise an MMA has waited for each): the last step of every stage
+    // that anyone has issued must land before the CTA leaves.
+    DevCtl drain = p.ctl;
+    drain.spin_limit = 1000000000LL;
+    for (int st = 0; st < S; ++st)
+      for (int j = st + (steps - 1) / S * S; j >= 0; j -= S) {
+        const bool w = j < bar->issued[0][j & 1], t = j < bar->issued[1][j & 1];
+        if (!w && !t) continue;
+        if (!w || !t) mbar_arrive(&bar->full[st]);  // for the producer that did not get there
+        mbar_wait(&bar->full[st], (j / S) & 1, drain);
+        break;
+      }
+  }
   cluster_sync();  // no CTA leaves while another may still push to it
 }
 
@@ -319,9 +349,10 @@ int cluster_of(int tiles, int KB, int sms) {
 }
 
 template <bool MX, bool GATE, int NT>
-cudaError_t run(const FfnEngine& e, const SkinnyParams& p, cudaStream_t st) {
+cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
   const int depth = MX ? 128 : 64;
   const int tiles = (p.N + kRows - 1) / kRows, C = cluster_of(tiles, (p.K + depth - 1) / depth, e.sms);
+  p.log_cluster = C == 8 ? 3 : C >> 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * C);
   cfg.blockDim = dim3(kThreads);
@@ -343,8 +374,13 @@ cudaError_t run_nt(const FfnEngine& e, const SkinnyParams& p, cudaStream_t st) {
 }
 template <bool MX, bool GATE, int NT>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(ffn_skinny_kernel<MX, GATE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)smem_of(MX, GATE, NT));
+  cudaError_t err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, GATE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem_of(MX, GATE, NT));
+  // the SM keeps all its shared memory open, so that the other kernel's CTA fits beside this one's
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, GATE, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+  return err;
 }
 template <bool MX, bool GATE>
 cudaError_t prepare_nt() {
@@ -400,6 +436,9 @@ cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx
     g.pre = static_cast<uint16_t*>(a.pre);
   }
   d.y = static_cast<uint16_t*>(a.y);
+  g.next = d.w;
+  g.next_rows = s.d;
+  g.next_K = s.I;
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t err = mx ? run_nt<true, true>(e, g, st) : run_nt<false, true>(e, g, st);
   if (err == cudaSuccess) err = mx ? run_nt<true, false>(e, d, st) : run_nt<false, false>(e, d, st);
