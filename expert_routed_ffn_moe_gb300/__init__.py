@@ -343,18 +343,51 @@ class MoeLayer:
 
 
 # ---------------------------------------------------------------- feed-forward block and its norm
-def _dtype_code(t, name):
-    import torch
-
-    known = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-    if t.dtype not in known:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return known[t.dtype]
+# These calls take a few microseconds on the device, so the checks are kept
+# cheap: tensors' properties are compared directly, and the stream's handle is
+# read without making a stream object.
+_torch = None
+_DTYPES = {}  # torch dtype -> MOE_F32 / MOE_BF16
 
 
-def _need_shape(t, name, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _DTYPES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16})
+        _torch = torch
+    return _torch
+
+
+def _handle(stream, t):
+    return _t()._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+
+
+def _checked(t, name, shape, dtype=None):
+    """t's address, after the checks; None for None.  Without ``dtype`` t is float32 or bfloat16."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is None:
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _rows(t, name, cols=None):
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must have shape [rows, {'cols' if cols is None else cols}], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _mx_bytes(rows, cols):
+    return (rows + 127) // 128 * ((cols + 127) // 128) * 512
 
 
 def moe_mx_scale_bytes(rows: int, cols: int) -> int:
@@ -362,85 +395,79 @@ def moe_mx_scale_bytes(rows: int, cols: int) -> int:
     return lib().moe_mx_scale_bytes(rows, cols)
 
 
-def _mx_pair(pair, name, rows, cols):
-    """(codes, scales) of an mx8 matrix, checked."""
-    import torch
-
+def _mx_checked(pair, name, rows, cols):
+    """Addresses of the codes and scales of an mx8 matrix, after the checks."""
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise ValueError(f"{name} must be a pair (codes, scales)")
     codes, scales = pair
-    _need_cuda(codes, f"{name} codes")
-    _need_cuda(scales, f"{name} scales")
-    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if not (codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name} codes and scales must be contiguous CUDA tensors")
+    if codes.dtype != _t().float8_e4m3fn and codes.dtype != _torch.uint8:
         raise ValueError(f"{name} codes must be float8_e4m3fn or uint8, got {codes.dtype}")
-    if scales.element_size() != 1:
-        raise ValueError(f"{name} scales must be bytes, got {scales.dtype}")
-    _need_shape(codes, f"{name} codes", (rows, cols))
-    if scales.numel() != moe_mx_scale_bytes(rows, cols):
-        raise ValueError(f"{name} scales must be {moe_mx_scale_bytes(rows, cols)} bytes, got {scales.numel()}")
-    return codes, scales
+    if codes.shape != (rows, cols):
+        raise ValueError(f"{name} codes must have shape {(rows, cols)}, got {tuple(codes.shape)}")
+    if scales.element_size() != 1 or scales.numel() != _mx_bytes(rows, cols):
+        raise ValueError(f"{name} scales must be {_mx_bytes(rows, cols)} bytes, got {scales.numel()} of {scales.dtype}")
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _mx_empty(rows, cols, device):
-    import torch
-
+    torch = _t()
     return (torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=device),
-            torch.empty(moe_mx_scale_bytes(rows, cols), dtype=torch.uint8, device=device))
+            torch.empty(_mx_bytes(rows, cols), dtype=torch.uint8, device=device))
 
 
 def moe_quantize_mx(v, codes=None, scales=None, stream=None):
     """Round a float32 or bfloat16 matrix to mx8: (codes, scales); see moe.h."""
-    _need_cuda(v, "v")
-    rows, cols = v.shape
-    dt = _dtype_code(v, "v")
+    _t()
+    rows, cols = _rows(v, "v")
+    pv = _checked(v, "v", v.shape)
     if codes is None or scales is None:
         codes, scales = _mx_empty(rows, cols, v.device)
-    _mx_pair((codes, scales), "output", rows, cols)
-    _check(lib().moe_quantize_mx(_ptr(v), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(stream)),
-           "moe_quantize_mx")
+    pc, ps = _mx_checked((codes, scales), "output", rows, cols)
+    _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(stream, v)), "moe_quantize_mx")
     return codes, scales
 
 
 def moe_add_norm(x, residual, weight, eps, s_out, y, y_scales=None, stream=None) -> None:
     """See moe.h.  ``y`` is float32, bfloat16, or float8_e4m3fn codes with ``y_scales``."""
-    import torch
-
-    T, d = x.shape
-    for name, t in (("x", x), ("residual", residual), ("weight", weight), ("s_out", s_out), ("y", y),
-                    ("y_scales", y_scales)):
-        _need_cuda(t, name)
-    for name, t in (("residual", residual), ("s_out", s_out), ("y", y)):
-        _need_shape(t, name, (T, d))
-    _need_shape(weight, "weight", (d,))
-    if residual is not None and s_out is not None and residual.dtype != s_out.dtype:
-        raise ValueError(f"s_out must be {residual.dtype}, got {s_out.dtype}")
-    stream_t = residual if residual is not None else s_out
-    s_dtype = MOE_F32 if stream_t is None else _dtype_code(stream_t, "residual")
+    torch = _t()
+    shape = _rows(x, "x")
+    T, d = shape
+    px, pr = _checked(x, "x", shape), _checked(residual, "residual", shape)
+    ps = _checked(s_out, "s_out", shape, None if residual is None else residual.dtype)
+    pw = _checked(weight, "weight", (d,))
     if y.dtype == torch.float8_e4m3fn:
+        if y_scales is None:
+            raise ValueError("y_scales are needed for float8_e4m3fn codes")
+        py, pys = _mx_checked((y, y_scales), "y", T, d)
         y_dtype = MOE_MX8
-        if y_scales is not None and d % 32 == 0:
-            _mx_pair((y, y_scales), "y", T, d)
     else:
-        y_dtype = _dtype_code(y, "y")
-    _check(lib().moe_add_norm(_ptr(x), _dtype_code(x, "x"), _ptr(residual), s_dtype, _ptr(weight),
-                              _dtype_code(weight, "weight"), T, d, eps, _ptr(s_out), _ptr(y), y_dtype, _ptr(y_scales),
-                              _stream(stream)), "moe_add_norm")
+        py, pys = _checked(y, "y", shape), None if y_scales is None else y_scales.data_ptr()
+        y_dtype = _DTYPES[y.dtype]
+    s_like = residual if residual is not None else s_out
+    _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, MOE_F32 if s_like is None else _DTYPES[s_like.dtype], pw,
+                              _DTYPES[weight.dtype], T, d, eps, ps, py, y_dtype, pys, _handle(stream, x)),
+           "moe_add_norm")
 
 
 def moe_add_norm_backward(s, weight, dy, ds, eps, dx, dweight, workspace, stream=None) -> None:
-    T, d = s.shape
-    for name, t in (("s", s), ("dy", dy), ("ds", ds), ("dx", dx)):
-        _need_cuda(t, name, s.dtype)
-        _need_shape(t, name, (T, d))
-    for name, t in (("weight", weight), ("dweight", dweight)):
-        _need_cuda(t, name, weight.dtype)
-        _need_shape(t, name, (d,))
-    _need_cuda(workspace, "workspace")
-    if workspace is not None and workspace.numel() * workspace.element_size() < lib().moe_add_norm_workspace(d):
-        raise ValueError("workspace is smaller than moe_add_norm_workspace(d) bytes")
-    _check(lib().moe_add_norm_backward(_ptr(s), _ptr(weight), _ptr(dy), _ptr(ds), _dtype_code(s, "s"),
-                                       _dtype_code(weight, "weight"), T, d, eps, _ptr(dx), _ptr(dweight),
-                                       _ptr(workspace), _stream(stream)), "moe_add_norm_backward")
+    """See moe.h.  ``ds``, ``dx`` and ``dweight`` may be None."""
+    _t()
+    shape = _rows(s, "s")
+    T, d = shape
+    ps, pw = _checked(s, "s", shape), _checked(weight, "weight", (d,))
+    pdy, pds, pdx = (_checked(t, n, shape, s.dtype) for n, t in (("dy", dy), ("ds", ds), ("dx", dx)))
+    pdw = _checked(dweight, "dweight", (d,), weight.dtype)
+    pws = None
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.numel() * workspace.element_size() < lib().moe_add_norm_workspace(d):
+            raise ValueError("workspace is smaller than moe_add_norm_workspace(d) bytes")
+        pws = workspace.data_ptr()
+    _check(lib().moe_add_norm_backward(ps, pw, pdy, pds, _DTYPES[s.dtype], _DTYPES[weight.dtype], T, d, eps, pdx, pdw,
+                                       pws, _handle(stream, s)), "moe_add_norm_backward")
 
 
 class AddNorm:
@@ -456,26 +483,27 @@ class AddNorm:
     def forward(self, x, residual, weight, y_dtype=MOE_BF16, s_out=None, stream=None):
         """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
         in the residual's dtype (x's without a residual)."""
-        import torch
-
-        if y_dtype not in (MOE_F32, MOE_BF16, MOE_MX8):
-            raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
-        _need_shape(x, "x", (x.shape[0], self.d))
+        torch = _t()
+        _rows(x, "x", self.d)
         if s_out is None:
             s_out = torch.empty_like(x if residual is None else residual)
-        if y_dtype == MOE_MX8:
-            y, scales = _mx_empty(x.shape[0], self.d, x.device)
+        if y_dtype == MOE_BF16:
+            y = torch.empty_like(x, dtype=torch.bfloat16)
+        elif y_dtype == MOE_F32:
+            y = torch.empty_like(x, dtype=torch.float32)
+        elif y_dtype == MOE_MX8:
+            pair = _mx_empty(x.shape[0], self.d, x.device)
+            moe_add_norm(x, residual, weight, self.eps, s_out, *pair, stream)
+            return pair, s_out
         else:
-            y = torch.empty(x.shape, dtype=torch.float32 if y_dtype == MOE_F32 else torch.bfloat16, device=x.device)
-            scales = None
-        moe_add_norm(x, residual, weight, self.eps, s_out, y, scales, stream)
-        return ((y, scales) if y_dtype == MOE_MX8 else y), s_out
+            raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
+        moe_add_norm(x, residual, weight, self.eps, s_out, y, None, stream)
+        return y, s_out
 
     def backward(self, s, weight, dy, ds=None, stream=None):
         """(dx, dweight); dx is the gradient of x and of the residual alike."""
-        import torch
-
-        _need_shape(s, "s", (s.shape[0], self.d))
+        torch = _t()
+        _rows(s, "s", self.d)
         if self._workspace is None or self._workspace.device != s.device:
             self._workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
         dx, dweight = torch.empty_like(s), torch.empty_like(weight)
@@ -520,52 +548,45 @@ class GatedFfn:
         self.d, self.inter, self.mx = d, inter, weight_format == MOE_W_MX8
         self.ctx = moe_ffn_init(d, inter, max_tokens, activation, weight_format, training)
 
-    def _operand(self, t, name, rows, cols):
-        import torch
-
-        if self.mx:
-            return _mx_pair(t, name, rows, cols)
-        _need_cuda(t, name, torch.bfloat16)
-        _need_shape(t, name, (rows, cols))
-        return t, None
-
     def forward(self, x, gate_up, down, y=None, pre=None, save=False, stream=None):
         """y, or (y, pre) with ``save`` (pre: the pre-activations that ``backward`` needs)."""
-        import torch
-
-        rows = x[0] if isinstance(x, (tuple, list)) else x
-        T = rows.shape[0]
-        x, xs = self._operand(x, "x", T, self.d)
-        gu, gus = self._operand(gate_up, "gate_up", 2 * self.inter, self.d)
-        dn, dns = self._operand(down, "down", self.d, self.inter)
+        torch = _t()
+        d, I, bf16 = self.d, self.inter, torch.bfloat16
+        if self.mx:
+            rows = x[0] if isinstance(x, (tuple, list)) else x
+            T = _rows(rows, "x", d)[0]
+            px, pxs = _mx_checked(x, "x", T, d)
+            pg, pgs = _mx_checked(gate_up, "gate_up", 2 * I, d)
+            pd, pds = _mx_checked(down, "down", d, I)
+        else:
+            rows = x
+            T = _rows(x, "x", d)[0]
+            px, pg, pd = _checked(x, "x", (T, d), bf16), _checked(gate_up, "gate_up", (2 * I, d), bf16), \
+                _checked(down, "down", (d, I), bf16)
+            pxs = pgs = pds = None
         if y is None:
-            y = torch.empty(T, self.d, dtype=torch.bfloat16, device=x.device)
+            y = torch.empty(T, d, dtype=bf16, device=rows.device) if self.mx else torch.empty_like(x)
         if pre is None and save:
-            pre = torch.empty(T, 2 * self.inter, dtype=torch.bfloat16, device=x.device)
-        for name, t, cols in (("y", y, self.d), ("pre", pre, 2 * self.inter)):
-            _need_cuda(t, name, torch.bfloat16)
-            _need_shape(t, name, (T, cols))
-        _check(lib().moe_ffn_forward(self.ctx, _ptr(x), _ptr(xs), T, _ptr(gu), _ptr(gus), _ptr(dn), _ptr(dns), _ptr(y),
-                                     _ptr(pre), _stream(stream)), "moe_ffn_forward")
+            pre = torch.empty(T, 2 * I, dtype=bf16, device=rows.device)
+        py, pp = _checked(y, "y", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16)
+        _check(lib().moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(stream, rows)),
+               "moe_ffn_forward")
         return (y, pre) if pre is not None else y
 
     def backward(self, x, pre, gate_up, down, dy, dx=None, dgate_up=None, ddown=None, stream=None):
         """(dx, dgate_up, ddown); pass ``False`` for one of them to leave it out (None comes back)."""
-        import torch
-
-        T = x.shape[0]
-        given = dict(x=(x, (T, self.d)), pre=(pre, (T, 2 * self.inter)), gate_up=(gate_up, (2 * self.inter, self.d)),
-                     down=(down, (self.d, self.inter)), dy=(dy, (T, self.d)))
+        torch = _t()
+        d, I, bf16 = self.d, self.inter, torch.bfloat16
+        T = _rows(x, "x", d)[0]
+        ins = [_checked(x, "x", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16), T,
+               _checked(gate_up, "gate_up", (2 * I, d), bf16), _checked(down, "down", (d, I), bf16),
+               _checked(dy, "dy", (T, d), bf16)]
         outs = []
         for name, t, like in (("dx", dx, x), ("dgate_up", dgate_up, gate_up), ("ddown", ddown, down)):
             t = None if t is False else torch.empty_like(like) if t is None else t
             outs.append(t)
-            given[name] = (t, tuple(like.shape))
-        for name, (t, shape) in given.items():
-            _need_cuda(t, name, torch.bfloat16)
-            _need_shape(t, name, shape)
-        _check(lib().moe_ffn_backward(self.ctx, _ptr(x), _ptr(pre), T, _ptr(gate_up), _ptr(down), _ptr(dy),
-                                      *(_ptr(t) for t in outs), _stream(stream)), "moe_ffn_backward")
+            ins.append(_checked(t, name, like.shape, bf16))
+        _check(lib().moe_ffn_backward(self.ctx, *ins, _handle(stream, x)), "moe_ffn_backward")
         return tuple(outs)
 
     def status(self) -> int:
