@@ -107,11 +107,10 @@ int moe_ffn_init(const moe_ffn_config* cfg, moe_ffn** out) {
 
   FfnEngine eng{};
   eng.sms = prop.multiProcessorCount;
-  eng.pairs = prop.multiProcessorCount / 2;
   eng.ctl.spin_limit = kDefaultSpinNs;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
-  if (prepare_ffn_gemm(&eng.pairs) != cudaSuccess || eng.pairs < 1 || prepare_ffn_skinny() != cudaSuccess ||
+  if (prepare_ffn_gemm(&eng) != cudaSuccess || prepare_ffn_skinny() != cudaSuccess ||
       cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
       q != cudaDriverEntryPointSuccess || !fn) {
     cudaGetLastError();

@@ -25,6 +25,12 @@
 // product B's first half holds gate rows and the second half the up rows of the
 // same 128 neurons, so the activation finishes in the accumulator's columns.
 //
+// A product with fewer tiles than pairs splits the reduction over 2 or 4 pairs
+// of one cluster (SPLIT).  Each pair ends with fp32 sums of the whole tile; the
+// columns are divided among the pairs, every CTA sends its sums of the others'
+// columns to them through distributed shared memory (the ring's memory, free by
+// then), and each adds its columns' sums in the order of k and finishes them.
+//
 // Operands may lie K-major (the reduction contiguous in memory) or MN-major:
 // dx, dgate_up and ddown read the forward pass's matrices where they lie, with
 // no transposed copies.  A ragged M, N or K reads zeros from TMA's bounds fill.
@@ -58,6 +64,7 @@ constexpr int kStoreBytes = 32 * 128;       // staging tile: 32 rows x 64 bf16
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
+constexpr int kTileCost = 10, kSplitCost = 6; // of a tile besides its k blocks, in k blocks (~0.27 us), see run()
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
 enum { kEpiStore, kEpiGateUp, kEpiGrad };
@@ -69,16 +76,17 @@ struct GemmParams {
   CUtensorMap as, bs0, bs1;        // mx8 scales: of A, and of the two 128-row halves of B
   uint8_t *hq, *hs;                // mx8 gate/up: codes and scales of h
   const uint16_t* pre;             // grad: [M, 2N] pre-activations
+  uint16_t *y, *pre_out, *dpre;    // SPLIT: the result (or h), pre and dpre by address
   int M, N, K;                     // N: columns of the result (gate/up: neurons)
   int act;
   int store_pre;
   DevCtl ctl;
 };
 
-constexpr int stages_of(int epi, bool mx) { return epi == kEpiStore && !mx ? 6 : 5; }
+constexpr int stages_of(int epi, bool mx, int split = 1) { return split > 1 || (epi == kEpiStore && !mx) ? 6 : 5; }
 constexpr int stage_bytes(bool mx) { return kStageBytes + (mx ? kScaleBytes : 0); }
 // staging tiles per epilogue warp
-constexpr int buffers_of(int epi, bool mx) { return epi == kEpiStore ? 1 : (mx ? 0 : 2); }
+constexpr int buffers_of(int epi, bool mx, int split = 1) { return split > 1 ? 0 : epi == kEpiStore ? 1 : (mx ? 0 : 2); }
 
 struct __align__(8) Bars {
   uint64_t full[6];    // used in the first CTA: both CTAs' copies of a k block have landed
@@ -86,18 +94,21 @@ struct __align__(8) Bars {
   uint64_t tfull[2];   // an accumulator is complete (both CTAs)
   uint64_t tempty[2];  // used in the first CTA: both CTAs' epilogues have read an accumulator
   uint64_t mma_done;
+  uint64_t free[4];          // SPLIT: the cluster's i-th pair takes in sums now
+  uint64_t recv[kEpiWarps];  // SPLIT: the other pairs' sums of an epilogue warp's columns have come
   uint32_t tmem_base;
   int abort_flag;
   uint32_t issued[2][3];  // k blocks loaded by each CTA's producers of A, B and scales (first CTA: both's)
   uint32_t peer_abort;
 };
 
-constexpr size_t smem_of(int epi, bool mx) {
-  return 1024 + (size_t)stages_of(epi, mx) * stage_bytes(mx) + (size_t)kEpiWarps * buffers_of(epi, mx) * kStoreBytes +
-         sizeof(Bars);
+constexpr size_t smem_of(int epi, bool mx, int split = 1) {
+  return 1024 + (size_t)stages_of(epi, mx, split) * stage_bytes(mx) +
+         (size_t)kEpiWarps * buffers_of(epi, mx, split) * kStoreBytes + sizeof(Bars);
 }
 static_assert(smem_of(kEpiStore, false) <= 227 * 1024 && smem_of(kEpiGateUp, false) <= 227 * 1024 &&
-                  smem_of(kEpiStore, true) <= 227 * 1024 && smem_of(kEpiGateUp, true) <= 227 * 1024,
+                  smem_of(kEpiStore, true) <= 227 * 1024 && smem_of(kEpiGateUp, true) <= 227 * 1024 &&
+                  smem_of(kEpiStore, true, 4) <= 227 * 1024,
               "shared memory of one CTA");
 
 MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
@@ -167,14 +178,45 @@ MOE_DEV void tma_load_scales_pair(void* dst, const CUtensorMap* m, int col, int 
       : "memory");
 }
 // Arrive on `bar` of both CTAs once this thread's earlier MMAs have finished.
-MOE_DEV void commit_pair(uint64_t* bar) {
+MOE_DEV void commit_pair(uint64_t* bar, uint16_t both) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(both)
       : "memory");
 }
 
+// Whether a phase has completed, without waiting.
+MOE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Whether `ok` holds in all 256 threads of the epilogue warps.
+MOE_DEV bool all_of_256(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// `bytes` of this CTA's shared memory to another CTA of the cluster (addresses there: dst, bar).
+MOE_DEV void copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
 MOE_DEV void set_abort(Bars* b) { *reinterpret_cast<volatile int*>(&b->abort_flag) = 1; }
 
@@ -191,10 +233,10 @@ MOE_DEV void stage16(uint8_t* tile, int lane, int c, uint4 v) {
   *reinterpret_cast<uint4*>(tile + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool MX>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+__global__ void __launch_bounds__(threads_of(MX), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int S = stages_of(EPI, MX), NB = buffers_of(EPI, MX);
+  constexpr int S = stages_of(EPI, MX, SPLIT), NB = buffers_of(EPI, MX, SPLIT);
   constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
   constexpr int kDepth = MX ? kRowBytes : kBK;     // values of k per block
   static_assert(!MX || (!A_MN && !B_MN && EPI != kEpiGrad), "mx8: forward products only");
@@ -206,10 +248,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
   Bars* bar = reinterpret_cast<Bars*>(scales + (MX ? S * kScaleBytes : 0));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;  // rank in the pair, its first CTA
+  const int slot = SPLIT > 1 ? (int)crank >> 1 : 0;                             // the pair's part of the reduction
+  const int pair = blockIdx.x / (2 * SPLIT), pairs = gridDim.x / (2 * SPLIT);   // (SPLIT: a cluster has one tile)
   const int mt = (p.M + 2 * kBM - 1) / (2 * kBM), nt = (p.N + TN - 1) / TN, tiles = mt * nt;
-  const int KB = (p.K + kDepth - 1) / kDepth;
+  const int blocks = (p.K + kDepth - 1) / kDepth;
+  const int kb0 = slot * blocks / SPLIT, kb1 = (slot + 1) * blocks / SPLIT;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) {
@@ -221,6 +265,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
       mbar_init(&bar->tempty[i], 2 * kEpiWarps);
     }
     mbar_init(&bar->mma_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar->free[i], 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(&bar->recv[i], 1);
     bar->abort_flag = 0;
     bar->peer_abort = 0;
     fence_mbar_init();
@@ -248,14 +294,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
         const int arow = (2 * m + (int)rank) * kBM;
         // B's half: gate rows in the first CTA, up rows in the second
         const int brow = EPI == kEpiGateUp ? n * TN + (int)rank * p.N : n * TN + (int)rank * 128;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           const int st = issued % S;
           if (!mbar_wait(&bar->empty[st], ((issued / S) & 1) ^ 1, p.ctl) || aborted(bar)) {
             set_abort(bar);
             ok = false;
             break;
           }
-          const uint32_t fb = map_cta(&bar->full[st], 0);
+          const uint32_t fb = map_cta(&bar->full[st], lead);
           uint8_t* a = base + st * kStageBytes;
           uint8_t* b = a + kOpBytes;
           const int k = kb * kDepth;
@@ -288,6 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      const uint16_t both = (uint16_t)(3u << lead);  // the pair's CTAs in the cluster
       int it = 0, lt = 0;
       bool ok = true, ready = false;
       if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
@@ -306,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + acc * (MX ? kBN - kSharedCols : kBN);
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int st = it % S;
           if (!ready && (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar))) {
             set_abort(bar);
@@ -314,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
             break;
           }
           // asked for before this block's MMAs: a load from shared memory queues behind their operand reads
-          ready = mbar_try_wait(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
+          ready = mbar_test(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
           tc_fence_after();
           const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
           const uint64_t da = A_MN ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
@@ -326,20 +373,185 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
             for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_pair_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(2 * kBM, kBN, j), ts, ts + 4, (kb | j) != 0);
+              mma_pair_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(2 * kBM, kBN, j), ts, ts + 4, kb != kb0 || j != 0);
           } else {
 #pragma unroll
-            for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, (kb | j) != 0);
+            for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, kb != kb0 || j != 0);
           }
-          commit_pair(&bar->empty[st]);
+          commit_pair(&bar->empty[st], both);
         }
-        if (ok) commit_pair(&bar->tfull[acc]);
+        if (ok) commit_pair(&bar->tfull[acc], both);
       }
       // the MMAs issued so far are done before TMEM is freed and shared memory left
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                        smem_u32(&bar->mma_done))
                    : "memory");
       mbar_wait(&bar->mma_done, 0, p.ctl);
+    }
+  } else if (SPLIT > 1) {
+    // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
+    constexpr int W = kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
+    const int ew = warp - 2, part = warp & 3, half = ew >> 2;
+    auto a0_of = [&](int owner) { return EPI == kEpiGateUp ? (owner * 2 + half) * W : (owner * 2 + half) * 2 * W; };
+    auto b0_of = [&](int owner) { return a0_of(owner) + (EPI == kEpiGateUp ? kBN / 2 : W); };
+    const uint32_t src = tmem + ((uint32_t)(part * 32) << 16);
+    uint8_t* send = base;                                            // [SPLIT - 1][warp] x kSendBytes
+    uint8_t* recv = base + (SPLIT - 1) * kEpiWarps * kSendBytes;     // the same, by sender
+    static_assert(2 * (SPLIT - 1) * kEpiWarps * kSendBytes <= S * kStageBytes, "the exchange fits the ring");
+    // Place of column c of row `lane`: 16-byte pieces of 4 columns, rows side by side.
+    auto at = [&](uint8_t* buf, int c) { return reinterpret_cast<float4*>(buf + ((c >> 2) * 32 + lane) * 16); };
+    bool ok = mbar_wait(&bar->tfull[0], 0, p.ctl) && !aborted(bar);
+    if (lane == 0) mbar_expect_tx(&bar->recv[ew], (SPLIT - 1) * kSendBytes);
+    ok = all_of_256(ok);  // (all give up or none)
+    if (ok) {
+      tc_fence_after();
+      // the pair's MMAs are done, so its ring's memory takes in the others' sums now
+      if (warp == 2 && lane < SPLIT && lane != slot) arrive_cluster(map_cta(&bar->free[slot], 2 * lane + rank));
+#pragma unroll 1
+      for (int i = 1; i < SPLIT; ++i) {
+        const int owner = (slot + i) % SPLIT;
+        uint8_t* out = send + ((i - 1) * kEpiWarps + ew) * kSendBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int c = 0; c < W; c += 16) {
+            float v[16];
+            tmem_ld16_async(src + (h ? b0_of(owner) : a0_of(owner)) + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) *at(out, h * W + c + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          }
+        }
+        fence_proxy_async_shared_cta();
+        __syncwarp();
+        if (lane == 0) {
+          if (!mbar_wait(&bar->free[owner], 0, p.ctl)) {
+            set_abort(bar);
+          } else {
+            const int by = slot < owner ? slot : slot - 1;  // this pair among the owner's senders
+            const uint32_t to = (uint32_t)(2 * owner) + rank;
+            copy_to_cta(map_cta(recv + (by * kEpiWarps + ew) * kSendBytes, to), out, kSendBytes,
+                        map_cta(&bar->recv[ew], to));
+          }
+        }
+      }
+      ok = mbar_wait(&bar->recv[ew], 0, p.ctl);
+      if (!ok) {
+        DevCtl drain = p.ctl;
+        drain.spin_limit = 1000000000LL;
+        mbar_wait(&bar->recv[ew], 0, drain);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok) {
+      set_abort(bar);
+    } else if (pair < tiles) {
+      int m, n;
+      tile_of(pair, mt, nt, m, n);
+      const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
+      constexpr int kPer = 16;  // columns of a (and of b) at a time
+      uint32_t top = 0;         // mx8: the group's largest magnitude, and its values
+      float hv[W];
+#pragma unroll
+      for (int c = 0; c < W; c += kPer) {
+        float a[kPer], b[kPer];
+#pragma unroll
+        for (int k = 0; k < SPLIT; ++k) {  // in the order of k
+          float x[kPer], y[kPer];
+          if (k == slot) {
+            tmem_ld16_async(src + a0_of(slot) + c, x);
+            tmem_ld16_async(src + b0_of(slot) + c, y);
+            tmem_ld_wait();
+          } else {
+            uint8_t* in = recv + ((k < slot ? k : k - 1) * kEpiWarps + ew) * kSendBytes;
+#pragma unroll
+            for (int q = 0; q < kPer; q += 4) {
+              const float4 f = *at(in, c + q), g = *at(in, W + c + q);
+              x[q] = f.x, x[q + 1] = f.y, x[q + 2] = f.z, x[q + 3] = f.w;
+              y[q] = g.x, y[q + 1] = g.y, y[q + 2] = g.z, y[q + 3] = g.w;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            a[q] = k == 0 ? x[q] : a[q] + x[q];
+            b[q] = k == 0 ? y[q] : b[q] + y[q];
+          }
+        }
+        auto store = [&](uint16_t* to, int pitch, int col, const float(&v)[kPer]) {
+#pragma unroll
+          for (int q = 0; q < kPer; q += 8)
+            if (row < p.M && col + q < p.N)
+              *reinterpret_cast<uint4*>(to + (size_t)row * pitch + col + q) =
+                  make_uint4(pack_bf16x2(v[q], v[q + 1]), pack_bf16x2(v[q + 2], v[q + 3]),
+                             pack_bf16x2(v[q + 4], v[q + 5]), pack_bf16x2(v[q + 6], v[q + 7]));
+        };
+        if (EPI == kEpiStore) {
+          store(p.y, p.N, n * TN + a0_of(slot) + c, a);
+          store(p.y, p.N, n * TN + b0_of(slot) + c, b);
+        } else if (EPI == kEpiGateUp) {
+          const int col = n * TN + a0_of(slot) + c;
+          if (!MX && p.store_pre) {
+            store(p.pre_out, 2 * p.N, col, a);
+            // (the up half starts N columns further: pointer moved, column bound the same)
+            store(p.pre_out + p.N, 2 * p.N, col, b);
+          }
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) a[q] = act_value(a[q], p.act) * b[q];
+          if (!MX) {
+            store(p.y, p.N, col, a);
+          } else {  // W = 32: one group of 32 neurons, its second half follows
+            static_assert(SPLIT == 1 || !MX || EPI != kEpiGateUp || W == 32, "a warp holds whole groups");
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+              top = max(top, mag_bits(a[q]));
+              hv[(c + q) % W] = a[q];
+            }
+          }
+        } else {
+          auto grads = [&](int col, const float(&dh)[kPer]) {
+            float g[kPer], u[kPer], h[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; q += 8) {
+              const bool in = row < p.M && col + q < p.N;
+              const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + col + q;
+              const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
+              const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + p.N) : make_uint4(0, 0, 0, 0);
+              const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
+                const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
+                float act, da;
+                act_and_grad(gv, p.act, act, da);
+                g[q + e] = dh[q + e] * uv * da;
+                u[q + e] = dh[q + e] * act;
+                h[q + e] = act * uv;
+              }
+            }
+            store(p.dpre, 2 * p.N, col, g);
+            store(p.dpre + p.N, 2 * p.N, col, u);
+            store(p.y, p.N, col, h);
+          };
+          grads(n * TN + a0_of(slot) + c, a);
+          grads(n * TN + b0_of(slot) + c, b);
+        }
+      }
+      if (EPI == kEpiGateUp && MX) {
+        const int col = n * TN + a0_of(slot);
+        if (row < p.M && col < p.N) {
+          const uint32_t byte = mx_scale_byte(__uint_as_float(top));
+          const float k = mx_inverse_scale(byte);
+          uint32_t w[8];
+#pragma unroll
+          for (int q = 0; q < 32; q += 4) {
+            w[q >> 2] = e4m3x4(hv[q % W] * k, hv[(q + 1) % W] * k, hv[(q + 2) % W] * k, hv[(q + 3) % W] * k);
+          }
+          uint4* to = reinterpret_cast<uint4*>(p.hq + (size_t)row * p.N + col);
+          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          p.hs[mx_scale_word(row, col / 128, mx_tile_cols(p.N)) + col / 32 % 4] = (uint8_t)byte;
+        }
+      }
     }
   } else {
     const int ew = warp - 2, part = warp & 3, half = ew >> 2;
@@ -377,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], 0));
+        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], lead));
       };
       if (EPI == kEpiStore) {
 #pragma unroll 1
@@ -532,8 +744,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
   // CTAs' copies block by block, crediting a barrier with what never was.
   constexpr int kRoles = MX ? 3 : 2;
   if (threadIdx.x == 0 && rank == 1) {
-    for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], 0), bar->issued[1][r]);
-    store_cluster(map_cta(&bar->peer_abort, 0), (uint32_t)bar->abort_flag);
+    for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], lead), bar->issued[1][r]);
+    store_cluster(map_cta(&bar->peer_abort, lead), (uint32_t)bar->abort_flag);
   }
   cluster_sync();
   if (threadIdx.x == 0 && rank == 0 && (bar->abort_flag || bar->peer_abort)) {
@@ -549,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
         if (j >= (int)bar->issued[r / kRoles][r % kRoles]) missing += bytes[r % kRoles];
       if (j >= (int)bar->issued[0][0]) mbar_expect_tx(fb, 2 * kTx);
       if (missing)
-        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, 0)),
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, lead)),
                      "r"(missing)
                      : "memory");
       mbar_wait(fb, (j / S) & 1, drain);
@@ -560,6 +772,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MX), 1)
 }
 
 // ------------------------------------------------------------------ host side
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* at) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * SPLIT * clusters);
+  cfg.blockDim = dim3(threads_of(MX));
+  cfg.dynamicSmemBytes = smem_of(EPI, MX, SPLIT);
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = 2 * SPLIT;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+cudaError_t launch(const GemmParams& p, int clusters, cudaStream_t st) {
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(clusters, &at);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>, p);
+}
+
 template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b, uint64_t b_rows, void* out,
                 cudaStream_t st) {
@@ -572,35 +806,58 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
     ok = ok && (B_MN ? make_bf16_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
                      : make_bf16_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
   }
-  ok = ok && (!out || make_bf16_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
-  if (!ok) return cudaErrorInvalidValue;
   p.ctl = e.ctl;
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
   const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
-  ffn_gemm_kernel<EPI, A_MN, B_MN, MX><<<2 * pairs, threads_of(MX), smem_of(EPI, MX), st>>>(p);
-  return cudaGetLastError();
+  const int blocks = (p.K + (MX ? 127 : 63)) / (MX ? 128 : 64);
+  // Pairs that a tile's reduction is split over: time of a pair ~ rounds of tiles x (k blocks + what a tile costs
+  // besides them, in k blocks); a split adds the exchange.
+  constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
+  int split = 1;
+  double best = 1e30;
+  for (int s = 1; s <= kMost && s <= blocks; s *= 2) {
+    const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : e.pairs4;  // clusters that run at a time
+    if (fit < 1) break;
+    const double rounds = (double)((tiles + fit - 1) / fit);
+    const double cost = rounds * ((blocks + s - 1) / s + kTileCost + (s > 1 ? kSplitCost : 0));
+    if (cost < best) best = cost, split = s;
+  }
+  if (split == 1) {
+    ok = ok && (!out || make_bf16_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
+    if (EPI != kEpiStore && !MX) {
+      uint16_t* pre = EPI == kEpiGrad ? p.dpre : p.pre_out;
+      if (pre)
+        ok = ok && make_bf16_map(e.encode, &p.out_g, pre, p.N, p.M, 2 * (uint64_t)p.N, 64, 32) &&
+             make_bf16_map(e.encode, &p.out_u, pre + p.N, p.N, p.M, 2 * (uint64_t)p.N, 64, 32);
+    }
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  p.y = static_cast<uint16_t*>(out);
+  if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? (int)tiles : e.pairs, st);
+  if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, (int)tiles, st);
+  if constexpr (kMost == 4) return launch<EPI, A_MN, B_MN, MX, 4>(p, (int)tiles, st);
+  return cudaErrorInvalidValue;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool MX>
-cudaError_t prepare(int* pairs) {
-  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX>;
-  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI, MX));
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+cudaError_t prepare(int* clusters) {
+  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>;
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI, MX, SPLIT));
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(threads_of(MX));
-  cfg.dynamicSmemBytes = smem_of(EPI, MX);
   cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(1, &at);
   int n = 0;
   err = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
-  if (err == cudaSuccess && n < *pairs) *pairs = n;
+  if (err == cudaSuccess && n < *clusters) *clusters = n;
+  return err;
+}
+template <int EPI, bool A_MN, bool B_MN, bool MX>
+cudaError_t prepare_splits(FfnEngine* e) {
+  cudaError_t err = prepare<EPI, A_MN, B_MN, MX, 1>(&e->pairs);
+  if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 2>(&e->pairs2);
+  if constexpr (!(MX && EPI == kEpiGateUp))
+    if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 4>(&e->pairs4);
   return err;
 }
 
@@ -619,15 +876,16 @@ __global__ void __launch_bounds__(256) shift_scales_kernel(const uint32_t* src, 
 
 }  // namespace
 
-cudaError_t prepare_ffn_gemm(int* pairs) {
-  cudaError_t err = prepare<kEpiGateUp, false, false, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, false, false, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiGrad, false, true, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, false, true, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, true, true, false>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiGateUp, false, false, true>(pairs);
-  if (err == cudaSuccess) err = prepare<kEpiStore, false, false, true>(pairs);
-  return err;
+cudaError_t prepare_ffn_gemm(FfnEngine* e) {
+  e->pairs = e->pairs2 = e->pairs4 = e->sms / 2;
+  cudaError_t err = prepare_splits<kEpiGateUp, false, false, false>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, false, false>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiGrad, false, true, false>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, true, false>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiStore, true, true, false>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiGateUp, false, false, true>(e);
+  if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, false, true>(e);
+  return err == cudaSuccess && e->pairs < 1 ? cudaErrorInvalidConfiguration : err;
 }
 
 cudaError_t launch_mx_up_scales(const FfnShape& s, const uint8_t* gate_up_s, uint8_t* up_s, cudaStream_t st) {
@@ -676,9 +934,7 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
   p.K = s.d;
   p.act = s.act;
   p.store_pre = pre != nullptr;
-  if (pre && (!make_bf16_map(e.encode, &p.out_g, pre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
-              !make_bf16_map(e.encode, &p.out_u, pre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32)))
-    return cudaErrorInvalidValue;
+  p.pre_out = pre;
   return run<kEpiGateUp, false, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
 }
 
@@ -699,9 +955,7 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint1
   p.K = s.d;
   p.act = s.act;
   p.pre = pre;
-  if (!make_bf16_map(e.encode, &p.out_g, dpre, s.I, s.T, 2 * (uint64_t)s.I, 64, 32) ||
-      !make_bf16_map(e.encode, &p.out_u, dpre + s.I, s.I, s.T, 2 * (uint64_t)s.I, 64, 32))
-    return cudaErrorInvalidValue;
+  p.dpre = dpre;
   return run<kEpiGrad, false, true, false>(e, p, dy, down, s.I, h, st);
 }
 

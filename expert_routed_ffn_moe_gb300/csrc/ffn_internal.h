@@ -210,12 +210,12 @@ inline bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr
 struct FfnEngine {
   EncodeTiledFn encode;
   int sms;
-  int pairs;  // CTA pairs that run at a time
+  int pairs, pairs2, pairs4;  // clusters of 1, 2 and 4 CTA pairs that run at a time
   DevCtl ctl;
 };
 
 // ffn_gemm.cu
-cudaError_t prepare_ffn_gemm(int* pairs);  // kernel attributes; lowers *pairs to what the device runs at a time
+cudaError_t prepare_ffn_gemm(FfnEngine* e);  // kernel attributes; fills in e->pairs*
 cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void* x, const void* gate_up, uint16_t* h,
                                uint16_t* pre, cudaStream_t st);
 cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
