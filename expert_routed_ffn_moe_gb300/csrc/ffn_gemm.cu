@@ -99,7 +99,7 @@ struct __align__(8) Bars {
   uint32_t tmem_base;
   int abort_flag;
   uint32_t issued[2][3];  // k blocks loaded by each CTA's producers of A, B and scales (first CTA: both's)
-  uint32_t peer_abort;
+  uint32_t any_abort;     // some CTA of the cluster has given up
 };
 
 constexpr size_t smem_of(int epi, bool mx, int split = 1) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     for (int i = 0; i < 4; ++i) mbar_init(&bar->free[i], 1);
     for (int i = 0; i < kEpiWarps; ++i) mbar_init(&bar->recv[i], 1);
     bar->abort_flag = 0;
-    bar->peer_abort = 0;
+    bar->any_abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -281,6 +281,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  // Launched while the kernel before may still run: the setup above overlaps its end, everything below follows it.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0 || warp >= kBWarp) {
     if (lane == 0) {
@@ -739,57 +742,63 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   __syncthreads();
   // Leave together: the other CTA's shared memory is the target of remote
   // arrivals and of the MMAs' reads.  On the normal path every copy has landed
-  // (an MMA waited for it).  After an abort copies may be in flight: the second
-  // CTA reports what its producers have issued, and the first waits for both
-  // CTAs' copies block by block, crediting a barrier with what never was.
+  // (an MMA waited for it).  After an abort, which every CTA of the cluster is
+  // told, copies may be in flight: a pair's second CTA reports what its
+  // producers have issued, and the first waits for both CTAs' copies block by
+  // block, crediting a barrier with what never was.
   constexpr int kRoles = MX ? 3 : 2;
-  if (threadIdx.x == 0 && rank == 1) {
-    for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], lead), bar->issued[1][r]);
-    store_cluster(map_cta(&bar->peer_abort, lead), (uint32_t)bar->abort_flag);
-  }
+  if (threadIdx.x == 0 && bar->abort_flag)
+    for (uint32_t r = 0; r < 2 * SPLIT; ++r) store_cluster(map_cta(&bar->any_abort, r), 1u);
   cluster_sync();
-  if (threadIdx.x == 0 && rank == 0 && (bar->abort_flag || bar->peer_abort)) {
-    DevCtl drain = p.ctl;
-    drain.spin_limit = 1000000000LL;
-    constexpr uint32_t bytes[3] = {kOpBytes, kOpBytes, kScaleBytes};
-    int most = 0;
-    for (int r = 0; r < 2 * kRoles; ++r) most = max(most, (int)bar->issued[r / kRoles][r % kRoles]);
-    for (int j = max(0, most - S); j < most; ++j) {
-      uint64_t* fb = &bar->full[j % S];
-      uint32_t missing = 0;
-      for (int r = 0; r < 2 * kRoles; ++r)
-        if (j >= (int)bar->issued[r / kRoles][r % kRoles]) missing += bytes[r % kRoles];
-      if (j >= (int)bar->issued[0][0]) mbar_expect_tx(fb, 2 * kTx);
-      if (missing)
-        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, lead)),
-                     "r"(missing)
-                     : "memory");
-      mbar_wait(fb, (j / S) & 1, drain);
+  if (bar->any_abort) {
+    if (threadIdx.x == 0 && rank == 1)
+      for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], lead), bar->issued[1][r]);
+    cluster_sync();
+    if (threadIdx.x == 0 && rank == 0) {
+      DevCtl drain = p.ctl;
+      drain.spin_limit = 1000000000LL;
+      constexpr uint32_t bytes[3] = {kOpBytes, kOpBytes, kScaleBytes};
+      int most = 0;
+      for (int r = 0; r < 2 * kRoles; ++r) most = max(most, (int)bar->issued[r / kRoles][r % kRoles]);
+      for (int j = max(0, most - S); j < most; ++j) {
+        uint64_t* fb = &bar->full[j % S];
+        uint32_t missing = 0;
+        for (int r = 0; r < 2 * kRoles; ++r)
+          if (j >= (int)bar->issued[r / kRoles][r % kRoles]) missing += bytes[r % kRoles];
+        if (j >= (int)bar->issued[0][0]) mbar_expect_tx(fb, 2 * kTx);
+        if (missing)
+          asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(map_cta(fb, lead)),
+                       "r"(missing)
+                       : "memory");
+        mbar_wait(fb, (j / S) & 1, drain);
+      }
     }
+    cluster_sync();
   }
-  cluster_sync();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // ------------------------------------------------------------------ host side
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
-cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* at) {
+cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * SPLIT * clusters);
   cfg.blockDim = dim3(threads_of(MX));
   cfg.dynamicSmemBytes = smem_of(EPI, MX, SPLIT);
-  at->id = cudaLaunchAttributeClusterDimension;
-  at->val.clusterDim.x = 2 * SPLIT;
-  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2 * SPLIT;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
 cudaError_t launch(const GemmParams& p, int clusters, cudaStream_t st) {
-  cudaLaunchAttribute at;
-  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(clusters, &at);
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(clusters, at);
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>, p);
 }
@@ -845,8 +854,9 @@ cudaError_t prepare(int* clusters) {
   auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>;
   cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI, MX, SPLIT));
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute at;
-  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(1, &at);
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(1, at);
+  cfg.numAttrs = 1;
   int n = 0;
   err = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
   if (err == cudaSuccess && n < *clusters) *clusters = n;

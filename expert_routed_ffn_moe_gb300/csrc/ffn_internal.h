@@ -238,7 +238,7 @@ cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint
                                const FfnForwardArgs& a, cudaStream_t st);
 
 // ffn_skinny.cu: the whole forward call for few tokens
-constexpr int kSkinnyTokens = 64;
+constexpr int kSkinnyTokens = 32;
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);

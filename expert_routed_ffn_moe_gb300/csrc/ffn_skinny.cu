@@ -1,8 +1,8 @@
-// The gated feed-forward block for few tokens (T <= 64): both products bound by
+// The gated feed-forward block for few tokens (T <= 32): both products bound by
 // reading the weights once.
 //
 // The weight rows are the tensor cores' 128 rows and the tokens their N columns
-// (D[row, token] = W x^T, N = T rounded up to 16, 32 or 64), so no MMA work and
+// (D[row, token] = W x^T, N = T rounded up to 16 or 32), so no MMA work and
 // no shared memory goes to rows that do not exist, and one multiply per weight
 // row block serves every token.  128 x 128-byte weight blocks and the matching x
 // blocks go through a TMA ring.  A thread takes ~0.3 us to wait for a stage and
@@ -60,11 +60,11 @@ constexpr int exchange_bytes(bool gate, int nt) { return nt * (gate ? 2 : 1) * k
 // Stages of the ring.  An even number: the even and the odd steps then have
 // stages of their own, so that each stage's phases are waited for by one thread
 // in their order (a wait by parity for a phase after the next would return at
-// once).  Up to 32 tokens a gate/up and a down CTA fit an SM together.
-constexpr int stages_of(bool gate, int nt) { return nt <= 16 ? (gate ? 6 : 4) : nt <= 32 ? 4 : 6; }
+// once).  A gate/up and a down CTA fit an SM together.
+constexpr int stages_of(bool gate, int nt) { return gate && nt <= 16 ? 6 : 4; }
 constexpr uint32_t tmem_cols(bool mx, int nt) {
   const int need = 2 * nt + (mx ? 16 : 0);
-  return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
+  return need <= 32 ? 32 : need <= 64 ? 64 : 128;
 }
 
 struct __align__(8) Bars {
@@ -80,8 +80,7 @@ constexpr size_t smem_of(bool mx, bool gate, int nt) {
 constexpr bool share_an_sm(bool mx, int nt) {  // 228 KB, 1 KB of it the system's for each CTA
   return smem_of(mx, true, nt) + smem_of(mx, false, nt) + 2048 <= 228 * 1024;
 }
-static_assert(share_an_sm(false, 16) && share_an_sm(true, 16) && share_an_sm(false, 32) && share_an_sm(true, 32) &&
-                  smem_of(true, true, 64) <= 227 * 1024 && smem_of(true, false, 64) <= 227 * 1024,
+static_assert(share_an_sm(false, 16) && share_an_sm(true, 16) && share_an_sm(false, 32) && share_an_sm(true, 32),
               "shared memory");
 
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
@@ -370,7 +369,7 @@ cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
 }
 template <bool MX, bool GATE>
 cudaError_t run_nt(const FfnEngine& e, const SkinnyParams& p, cudaStream_t st) {
-  return p.T <= 16 ? run<MX, GATE, 16>(e, p, st) : p.T <= 32 ? run<MX, GATE, 32>(e, p, st) : run<MX, GATE, 64>(e, p, st);
+  return p.T <= 16 ? run<MX, GATE, 16>(e, p, st) : run<MX, GATE, 32>(e, p, st);
 }
 template <bool MX, bool GATE, int NT>
 cudaError_t prepare() {
@@ -386,11 +385,10 @@ template <bool MX, bool GATE>
 cudaError_t prepare_nt() {
   cudaError_t err = prepare<MX, GATE, 16>();
   if (err == cudaSuccess) err = prepare<MX, GATE, 32>();
-  if (err == cudaSuccess) err = prepare<MX, GATE, 64>();
   return err;
 }
 
-uint32_t token_rows(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+uint32_t token_rows(int T) { return T <= 16 ? 16 : 32; }
 
 SkinnyParams params(const FfnEngine& e, const FfnShape& s, bool gate) {
   SkinnyParams p{};
