@@ -19,8 +19,8 @@
 //   warp 1     allocates all 512 TMEM columns: two fp32 accumulators of 256
 //              columns; in the pair's first CTA one thread issues the MMAs;
 //   warps 2-9  epilogue: two warps for each quarter of the TMEM lanes, each
-//              taking one half of the columns, through a swizzled staging tile
-//              per warp and TMA stores (which clip ragged edges).
+//              taking one half of the columns; a thread has a row and writes
+//              16 columns (32 bytes) at a time.
 // The epilogue of tile i overlaps the main loop of tile i + 1.  In the gate/up
 // product B's first half holds gate rows and the second half the up rows of the
 // same 128 neurons, so the activation finishes in the accumulator's columns.
@@ -60,7 +60,6 @@ constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
 constexpr int kEpiWarps = 8;
 constexpr int kBWarp = 2 + kEpiWarps, kScaleWarp = kBWarp + 1;  // producers of B and of the scales (A: warp 0)
 constexpr int threads_of(bool mx) { return (mx ? kScaleWarp + 1 : kBWarp + 1) * 32; }
-constexpr int kStoreBytes = 32 * 128;       // staging tile: 32 rows x 64 bf16
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
@@ -71,22 +70,20 @@ enum { kEpiStore, kEpiGateUp, kEpiGrad };
 
 struct GemmParams {
   CUtensorMap a, b;                // operands
-  CUtensorMap out;                 // bf16 result: y / dx / dW, or h
-  CUtensorMap out_g, out_u;        // the halves of pre (gate/up) or of dpre (grad)
   CUtensorMap as, bs0, bs1;        // mx8 scales: of A, and of the two 128-row halves of B
   uint8_t *hq, *hs;                // mx8 gate/up: codes and scales of h
-  const uint16_t* pre;             // grad: [M, 2N] pre-activations
-  uint16_t *y, *pre_out, *dpre;    // SPLIT: the result (or h), pre and dpre by address
+  uint16_t* y;                     // bf16 result [M, N]: y / dx / dW, or h
+  uint16_t* pre_out;               // gate/up: pre [M, 2N], or NULL
+  const uint16_t* pre;             // grad: pre [M, 2N]
+  uint16_t* dpre;                  // grad: [M, 2N]
   int M, N, K;                     // N: columns of the result (gate/up: neurons)
   int act;
-  int store_pre;
+  int wide;                        // rows of the results are 32-byte aligned: N is a multiple of 16
   DevCtl ctl;
 };
 
-constexpr int stages_of(int epi, bool mx, int split = 1) { return split > 1 || (epi == kEpiStore && !mx) ? 6 : 5; }
+constexpr int kStages = 6;
 constexpr int stage_bytes(bool mx) { return kStageBytes + (mx ? kScaleBytes : 0); }
-// staging tiles per epilogue warp
-constexpr int buffers_of(int epi, bool mx, int split = 1) { return split > 1 ? 0 : epi == kEpiStore ? 1 : (mx ? 0 : 2); }
 
 struct __align__(8) Bars {
   uint64_t full[6];    // used in the first CTA: both CTAs' copies of a k block have landed
@@ -102,14 +99,8 @@ struct __align__(8) Bars {
   uint32_t any_abort;     // some CTA of the cluster has given up
 };
 
-constexpr size_t smem_of(int epi, bool mx, int split = 1) {
-  return 1024 + (size_t)stages_of(epi, mx, split) * stage_bytes(mx) +
-         (size_t)kEpiWarps * buffers_of(epi, mx, split) * kStoreBytes + sizeof(Bars);
-}
-static_assert(smem_of(kEpiStore, false) <= 227 * 1024 && smem_of(kEpiGateUp, false) <= 227 * 1024 &&
-                  smem_of(kEpiStore, true) <= 227 * 1024 && smem_of(kEpiGateUp, true) <= 227 * 1024 &&
-                  smem_of(kEpiStore, true, 4) <= 227 * 1024,
-              "shared memory of one CTA");
+constexpr size_t smem_of(bool mx) { return 1024 + (size_t)kStages * stage_bytes(mx) + sizeof(Bars); }
+static_assert(smem_of(true) <= 227 * 1024, "shared memory of one CTA");
 
 MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -122,16 +113,10 @@ MOE_DEV void tma_load_pair(void* dst, const CUtensorMap* m, int x, int y, uint32
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-MOE_DEV void tma_store(const CUtensorMap* m, int x, int y, const void* src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y), "r"(smem_u32(src))
+MOE_DEV void store32(void* to, const uint32_t(&w)[8]) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
-}
-MOE_DEV void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-MOE_DEV void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 // Shared-memory matrix descriptor of an MN-major bf16 operand, 128-byte swizzle:
 // each k is a 128-byte row of 64 elements along m (or n), 8 k rows make a
@@ -228,23 +213,17 @@ MOE_DEV void tile_of(int t, int mt, int nt, int& m, int& n) {
   n = r / gm;
 }
 
-// 16 bytes (8 bf16) into a swizzled staging tile: row `lane`, 16-byte column c.
-MOE_DEV void stage16(uint8_t* tile, int lane, int c, uint4 v) {
-  *reinterpret_cast<uint4*>(tile + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
-}
-
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
 __global__ void __launch_bounds__(threads_of(MX), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int S = stages_of(EPI, MX, SPLIT), NB = buffers_of(EPI, MX, SPLIT);
+  constexpr int S = kStages;
   constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
   constexpr int kDepth = MX ? kRowBytes : kBK;     // values of k per block
   static_assert(!MX || (!A_MN && !B_MN && EPI != kEpiGrad), "mx8: forward products only");
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;  // result columns per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = base + S * kStageBytes;  // (the scales follow the staging tiles)
-  uint8_t* scales = staging + kEpiWarps * NB * kStoreBytes;
+  uint8_t* scales = base + S * kStageBytes;
   Bars* bar = reinterpret_cast<Bars*>(scales + (MX ? S * kScaleBytes : 0));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,352 +370,242 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
                    : "memory");
       mbar_wait(&bar->mma_done, 0, p.ctl);
     }
-  } else if (SPLIT > 1) {
-    // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
-    constexpr int W = kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
-    const int ew = warp - 2, part = warp & 3, half = ew >> 2;
-    auto a0_of = [&](int owner) { return EPI == kEpiGateUp ? (owner * 2 + half) * W : (owner * 2 + half) * 2 * W; };
-    auto b0_of = [&](int owner) { return a0_of(owner) + (EPI == kEpiGateUp ? kBN / 2 : W); };
-    const uint32_t src = tmem + ((uint32_t)(part * 32) << 16);
-    uint8_t* send = base;                                            // [SPLIT - 1][warp] x kSendBytes
-    uint8_t* recv = base + (SPLIT - 1) * kEpiWarps * kSendBytes;     // the same, by sender
-    static_assert(2 * (SPLIT - 1) * kEpiWarps * kSendBytes <= S * kStageBytes, "the exchange fits the ring");
-    // Place of column c of row `lane`: 16-byte pieces of 4 columns, rows side by side.
-    auto at = [&](uint8_t* buf, int c) { return reinterpret_cast<float4*>(buf + ((c >> 2) * 32 + lane) * 16); };
-    bool ok = mbar_wait(&bar->tfull[0], 0, p.ctl) && !aborted(bar);
-    if (lane == 0) mbar_expect_tx(&bar->recv[ew], (SPLIT - 1) * kSendBytes);
-    ok = all_of_256(ok);  // (all give up or none)
-    if (ok) {
-      tc_fence_after();
-      // the pair's MMAs are done, so its ring's memory takes in the others' sums now
-      if (warp == 2 && lane < SPLIT && lane != slot) arrive_cluster(map_cta(&bar->free[slot], 2 * lane + rank));
-#pragma unroll 1
-      for (int i = 1; i < SPLIT; ++i) {
-        const int owner = (slot + i) % SPLIT;
-        uint8_t* out = send + ((i - 1) * kEpiWarps + ew) * kSendBytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int c = 0; c < W; c += 16) {
-            float v[16];
-            tmem_ld16_async(src + (h ? b0_of(owner) : a0_of(owner)) + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 16; q += 4) *at(out, h * W + c + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-          }
-        }
-        fence_proxy_async_shared_cta();
-        __syncwarp();
-        if (lane == 0) {
-          if (!mbar_wait(&bar->free[owner], 0, p.ctl)) {
-            set_abort(bar);
-          } else {
-            const int by = slot < owner ? slot : slot - 1;  // this pair among the owner's senders
-            const uint32_t to = (uint32_t)(2 * owner) + rank;
-            copy_to_cta(map_cta(recv + (by * kEpiWarps + ew) * kSendBytes, to), out, kSendBytes,
-                        map_cta(&bar->recv[ew], to));
-          }
-        }
-      }
-      ok = mbar_wait(&bar->recv[ew], 0, p.ctl);
-      if (!ok) {
-        DevCtl drain = p.ctl;
-        drain.spin_limit = 1000000000LL;
-        mbar_wait(&bar->recv[ew], 0, drain);
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    if (!ok) {
-      set_abort(bar);
-    } else if (pair < tiles) {
-      int m, n;
-      tile_of(pair, mt, nt, m, n);
-      const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
-      constexpr int kPer = 16;  // columns of a (and of b) at a time
-      uint32_t top = 0;         // mx8: the group's largest magnitude, and its values
-      float hv[W];
-#pragma unroll
-      for (int c = 0; c < W; c += kPer) {
-        float a[kPer], b[kPer];
-#pragma unroll
-        for (int k = 0; k < SPLIT; ++k) {  // in the order of k
-          float x[kPer], y[kPer];
-          if (k == slot) {
-            tmem_ld16_async(src + a0_of(slot) + c, x);
-            tmem_ld16_async(src + b0_of(slot) + c, y);
-            tmem_ld_wait();
-          } else {
-            uint8_t* in = recv + ((k < slot ? k : k - 1) * kEpiWarps + ew) * kSendBytes;
-#pragma unroll
-            for (int q = 0; q < kPer; q += 4) {
-              const float4 f = *at(in, c + q), g = *at(in, W + c + q);
-              x[q] = f.x, x[q + 1] = f.y, x[q + 2] = f.z, x[q + 3] = f.w;
-              y[q] = g.x, y[q + 1] = g.y, y[q + 2] = g.z, y[q + 3] = g.w;
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < kPer; ++q) {
-            a[q] = k == 0 ? x[q] : a[q] + x[q];
-            b[q] = k == 0 ? y[q] : b[q] + y[q];
-          }
-        }
-        auto store = [&](uint16_t* to, int pitch, int col, const float(&v)[kPer]) {
-#pragma unroll
-          for (int q = 0; q < kPer; q += 8)
-            if (row < p.M && col + q < p.N)
-              *reinterpret_cast<uint4*>(to + (size_t)row * pitch + col + q) =
-                  make_uint4(pack_bf16x2(v[q], v[q + 1]), pack_bf16x2(v[q + 2], v[q + 3]),
-                             pack_bf16x2(v[q + 4], v[q + 5]), pack_bf16x2(v[q + 6], v[q + 7]));
-        };
-        if (EPI == kEpiStore) {
-          store(p.y, p.N, n * TN + a0_of(slot) + c, a);
-          store(p.y, p.N, n * TN + b0_of(slot) + c, b);
-        } else if (EPI == kEpiGateUp) {
-          const int col = n * TN + a0_of(slot) + c;
-          if (!MX && p.store_pre) {
-            store(p.pre_out, 2 * p.N, col, a);
-            // (the up half starts N columns further: pointer moved, column bound the same)
-            store(p.pre_out + p.N, 2 * p.N, col, b);
-          }
-#pragma unroll
-          for (int q = 0; q < kPer; ++q) a[q] = act_value(a[q], p.act) * b[q];
-          if (!MX) {
-            store(p.y, p.N, col, a);
-          } else {  // W = 32: one group of 32 neurons, its second half follows
-            static_assert(SPLIT == 1 || !MX || EPI != kEpiGateUp || W == 32, "a warp holds whole groups");
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-              top = max(top, mag_bits(a[q]));
-              hv[(c + q) % W] = a[q];
-            }
-          }
-        } else {
-          auto grads = [&](int col, const float(&dh)[kPer]) {
-            float g[kPer], u[kPer], h[kPer];
-#pragma unroll
-            for (int q = 0; q < kPer; q += 8) {
-              const bool in = row < p.M && col + q < p.N;
-              const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + col + q;
-              const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
-              const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + p.N) : make_uint4(0, 0, 0, 0);
-              const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
-                const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
-                float act, da;
-                act_and_grad(gv, p.act, act, da);
-                g[q + e] = dh[q + e] * uv * da;
-                u[q + e] = dh[q + e] * act;
-                h[q + e] = act * uv;
-              }
-            }
-            store(p.dpre, 2 * p.N, col, g);
-            store(p.dpre + p.N, 2 * p.N, col, u);
-            store(p.y, p.N, col, h);
-          };
-          grads(n * TN + a0_of(slot) + c, a);
-          grads(n * TN + b0_of(slot) + c, b);
-        }
-      }
-      if (EPI == kEpiGateUp && MX) {
-        const int col = n * TN + a0_of(slot);
-        if (row < p.M && col < p.N) {
-          const uint32_t byte = mx_scale_byte(__uint_as_float(top));
-          const float k = mx_inverse_scale(byte);
-          uint32_t w[8];
-#pragma unroll
-          for (int q = 0; q < 32; q += 4) {
-            w[q >> 2] = e4m3x4(hv[q % W] * k, hv[(q + 1) % W] * k, hv[(q + 2) % W] * k, hv[(q + 3) % W] * k);
-          }
-          uint4* to = reinterpret_cast<uint4*>(p.hq + (size_t)row * p.N + col);
-          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          p.hs[mx_scale_word(row, col / 128, mx_tile_cols(p.N)) + col / 32 % 4] = (uint8_t)byte;
-        }
-      }
-    }
   } else {
     const int ew = warp - 2, part = warp & 3, half = ew >> 2;
-    uint8_t* tile0 = staging + ew * NB * kStoreBytes;
     const uint32_t lanes = (uint32_t)(part * 32) << 16;
-    int lt = 0, nbuf = 0;
-    // a staging tile that no store reads any more
-    auto next_tile = [&]() {
-      if (lane == 0) tma_store_wait_read<(NB > 1 ? NB - 1 : 0)>();
-      __syncwarp();
-      return tile0 + (NB > 1 ? (nbuf++ % NB) * kStoreBytes : 0);
-    };
-    auto put_tile = [&](const CUtensorMap* map, const uint8_t* tile, int x, int y) {
-      fence_proxy_async_shared_cta();
-      __syncwarp();
-      if (lane == 0) {
-        if (x < p.N && y < p.M) tma_store(map, x, y, tile);
-        tma_store_commit();  // also without a store, so that groups and staging tiles stay in step
-      }
-    };
-    for (int t = pair; t < tiles; t += pairs, ++lt) {
-      int m, n;
-      tile_of(t, mt, nt, m, n);
-      const int acc = lt & 1;
-      const int y = (2 * m + (int)rank) * kBM + part * 32;
-      if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
-        set_abort(bar);
-        break;
-      }
-      tc_fence_after();
-      __syncwarp();
-      const uint32_t src = tmem + lanes + acc * (MX ? kBN - kSharedCols : kBN);
-      // mx8: the part with the shared columns first (the last columns of accumulator 0, the first of 1)
-      const int first = MX && acc == 0 ? 1 : 0;
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], lead));
-      };
-      if (EPI == kEpiStore) {
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {  // two boxes of 64 columns
-          const int c = i ^ first;
-          uint32_t r[2][32];
-          tmem_ld32_async(src + half * 128 + c * 64, r[0]);
-          tmem_ld32_async(src + half * 128 + c * 64 + 32, r[1]);
-          uint8_t* tile = next_tile();
-          tmem_ld_wait();
-          if (i == (MX ? 0 : 1)) release();
+    // 16 columns of a row as bf16; N is a multiple of 8, and of 16 where p.wide says so
+    auto store16 = [&](uint16_t* to, int pitch, int row, int col, const float(&v)[16]) {
+      if (row >= p.M) return;
+      uint32_t w[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(r[q >> 2][(q & 3) * 8 + 2 * i]),
-                                 __uint_as_float(r[q >> 2][(q & 3) * 8 + 2 * i + 1]));
-            stage16(tile, lane, q, make_uint4(w[0], w[1], w[2], w[3]));
-          }
-          put_tile(&p.out, tile, n * TN + half * 128 + c * 64, y);
-        }
-      } else if (EPI == kEpiGateUp && MX) {
-        const int row = y + lane;
-        uint32_t bytes = 0;  // the scales of this thread's two groups
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int c = i ^ first, x = n * TN + half * 64 + c * 32;
-          uint32_t g[32], u[32];
-          tmem_ld32_async(src + half * 64 + c * 32, g);
-          tmem_ld32_async(src + 128 + half * 64 + c * 32, u);
-          tmem_ld_wait();
-          if (i == 0) release();
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            g[e] = __float_as_uint(act_value(__uint_as_float(g[e]), p.act) * __uint_as_float(u[e]));
-            top = max(top, g[e] & 0x7fffffffu);
-          }
-          const uint32_t byte = mx_scale_byte(__uint_as_float(top));
-          const float k = mx_inverse_scale(byte);
-          bytes |= byte << (8 * c);
-          if (row < p.M && x < p.N) {
-            uint4* q = reinterpret_cast<uint4*>(p.hq + (size_t)row * p.N + x);
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t* v = &g[o * 16 + e * 4];
-                w[e] = e4m3x4(__uint_as_float(v[0]) * k, __uint_as_float(v[1]) * k, __uint_as_float(v[2]) * k,
-                              __uint_as_float(v[3]) * k);
-              }
-              q[o] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        const int x = n * TN + half * 64;
-        if (row < p.M && x < p.N) {  // the second group may lie past the last column: its byte stays 0
-          if (x + 32 >= p.N) bytes &= 0xffu;
-          *reinterpret_cast<uint16_t*>(p.hs + mx_scale_word(row, x / 128, mx_tile_cols(p.N)) + half * 2) =
-              (uint16_t)bytes;
-        }
-      } else if (EPI == kEpiGateUp) {
-        const int x = n * TN + half * 64;
-        auto stage_all = [&](const CUtensorMap* map, auto&& value) {
-          uint8_t* tile = next_tile();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t g[32], u[32];
-            tmem_ld32_async(src + half * 64 + c * 32, g);
-            tmem_ld32_async(src + 128 + half * 64 + c * 32, u);
-            tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int e = q * 8 + 2 * i;
-                w[i] = pack_bf16x2(value(__uint_as_float(g[e]), __uint_as_float(u[e])),
-                                   value(__uint_as_float(g[e + 1]), __uint_as_float(u[e + 1])));
-              }
-              stage16(tile, lane, c * 4 + q, make_uint4(w[0], w[1], w[2], w[3]));
-            }
-          }
-          put_tile(map, tile, x, y);
-        };
-        if (p.store_pre) {
-          stage_all(&p.out_g, [](float g, float) { return g; });
-          stage_all(&p.out_u, [](float, float u) { return u; });
-        }
-        const int act = p.act;
-        stage_all(&p.out, [act](float g, float u) { return act_value(g, act) * u; });
-        release();
+      for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+      uint16_t* at = to + (size_t)row * pitch + col;
+      if (p.wide) {
+        if (col < p.N) store32(at, w);
       } else {
-        // gradients of 128 neurons: dh in the accumulator, g and u from memory
+        if (col < p.N) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (col + 8 < p.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    };
+    // One row's results: 16 columns of a product or of dh, or gate and up values of 16 neurons
+    auto finish = [&](int row, int col, float(&v)[16], const float(&u)[16]) {
+      if (EPI == kEpiStore) {
+        store16(p.y, p.N, row, col, v);
+      } else if (EPI == kEpiGateUp) {
+        if (p.pre_out) {  // (the up half lies N columns further)
+          store16(p.pre_out, 2 * p.N, row, col, v);
+          store16(p.pre_out + p.N, 2 * p.N, row, col, u);
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = act_value(v[q], p.act) * u[q];
+        store16(p.y, p.N, row, col, v);
+      } else {
+        float dg[16], du[16], h[16];
+#pragma unroll
+        for (int q = 0; q < 16; q += 8) {
+          const bool in = row < p.M && col + q < p.N;
+          const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + col + q;
+          const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
+          const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + p.N) : make_uint4(0, 0, 0, 0);
+          const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
+            const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
+            float a, da;
+            act_and_grad(gv, p.act, a, da);
+            dg[q + e] = v[q + e] * uv * da;
+            du[q + e] = v[q + e] * a;
+            h[q + e] = a * uv;
+          }
+        }
+        store16(p.dpre, 2 * p.N, row, col, dg);
+        store16(p.dpre + p.N, 2 * p.N, row, col, du);
+        store16(p.y, p.N, row, col, h);
+      }
+    };
+    // mx8 gate/up: one row's 32 neurons, a group
+    auto finish_mx = [&](int row, int col, float(&h)[32], const float(&u)[32]) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        h[e] = act_value(h[e], p.act) * u[e];
+        top = max(top, mag_bits(h[e]));
+      }
+      const uint32_t byte = mx_scale_byte(__uint_as_float(top));
+      const float k = mx_inverse_scale(byte);
+      if (row >= p.M || col >= p.N) return;
+      uint32_t w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = e4m3x4(h[4 * q] * k, h[4 * q + 1] * k, h[4 * q + 2] * k, h[4 * q + 3] * k);
+      store32(p.hq + (size_t)row * p.N + col, w);
+      p.hs[mx_scale_word(row, col / 128, mx_tile_cols(p.N)) + col / 32 % 4] = (uint8_t)byte;
+    };
+
+    if constexpr (SPLIT == 1) {
+      int lt = 0;
+      for (int t = pair; t < tiles; t += pairs, ++lt) {
+        int m, n;
+        tile_of(t, mt, nt, m, n);
+        const int acc = lt & 1;
+        const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
+        if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
+          set_abort(bar);
+          break;
+        }
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t src = tmem + lanes + acc * (MX ? kBN - kSharedCols : kBN);
+        // mx8: the part with the shared columns first (the last columns of accumulator 0, the first of 1)
+        const bool back = MX && acc == 0;
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], lead));
+        };
+        if (EPI == kEpiGateUp && MX) {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int x = n * TN + half * 128 + c * 64;
-          const int row = y + lane;
-          uint32_t dg[32], du[32], hh[32];  // bf16 pairs
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t r[32];
-            tmem_ld32_async(src + half * 128 + c * 64 + q * 32, r);
-            uint4 g4[4], u4[4];
-            const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + x + q * 32;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool in = row < p.M && x + q * 32 + i * 8 < p.N;
-              g4[i] = in ? *reinterpret_cast<const uint4*>(gp + i * 8) : make_uint4(0, 0, 0, 0);
-              u4[i] = in ? *reinterpret_cast<const uint4*>(gp + p.N + i * 8) : make_uint4(0, 0, 0, 0);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int c = half * 64 + (back ? 1 - i : i) * 32;
+            float g[32], u[32];
+            tmem_ld16_async(src + c, g);
+            tmem_ld16_async(src + c + 16, g + 16);
+            tmem_ld16_async(src + 128 + c, u);
+            tmem_ld16_async(src + 128 + c + 16, u + 16);
             tmem_ld_wait();
-            if (c == 1 && q == 1) release();
+            if (i == 0) release();
+            finish_mx(row, n * TN + c, g, u);
+          }
+        } else {
+          // 16 columns (neurons) at a time in a compact loop: straight-line code for the whole tile takes longer to
+          // fetch than to run where a CTA has one tile or two
+          constexpr int kChunks = EPI == kEpiGateUp ? 4 : 8;
+          constexpr int kShared = MX ? kSharedCols / 16 : kChunks;  // chunks after which the accumulator is released
+          float v[16], u[16];
+          auto load = [&](int i) {
+            const int c = (half * kChunks + (back ? kChunks - 1 - i : i)) * 16;
+            tmem_ld16_async(src + c, v);
+            if (EPI == kEpiGateUp) tmem_ld16_async(src + 128 + c, u);
+          };
+          load(0);
+#pragma unroll 1
+          for (int i = 0; i < kChunks; ++i) {
+            tmem_ld_wait();
+            float x[16], y[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint4 gv = g4[i >> 2], uv = u4[i >> 2];
-              const uint32_t gw = (i & 3) == 0 ? gv.x : (i & 3) == 1 ? gv.y : (i & 3) == 2 ? gv.z : gv.w;
-              const uint32_t uw = (i & 3) == 0 ? uv.x : (i & 3) == 1 ? uv.y : (i & 3) == 2 ? uv.z : uv.w;
-              float a0, d0, a1, d1;
-              act_and_grad(bf16_lo(gw), p.act, a0, d0);
-              act_and_grad(bf16_hi(gw), p.act, a1, d1);
-              const float h0 = __uint_as_float(r[2 * i]), h1 = __uint_as_float(r[2 * i + 1]);
-              const float u0 = bf16_lo(uw), u1 = bf16_hi(uw);
-              dg[q * 16 + i] = pack_bf16x2(h0 * u0 * d0, h1 * u1 * d1);
-              du[q * 16 + i] = pack_bf16x2(h0 * a0, h1 * a1);
-              hh[q * 16 + i] = pack_bf16x2(a0 * u0, a1 * u1);
+            for (int q = 0; q < 16; ++q) x[q] = v[q], y[q] = u[q];
+            if (i == kShared - 1) release();
+            if (i + 1 < kChunks) load(i + 1);
+            finish(row, n * TN + (half * kChunks + (back ? kChunks - 1 - i : i)) * 16, x, y);
+          }
+        }
+      }
+    } else {
+      // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
+      constexpr int W = kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
+      auto a0_of = [&](int owner) { return EPI == kEpiGateUp ? (owner * 2 + half) * W : (owner * 2 + half) * 2 * W; };
+      auto b0_of = [&](int owner) { return a0_of(owner) + (EPI == kEpiGateUp ? kBN / 2 : W); };
+      const uint32_t src = tmem + lanes;
+      uint8_t* send = base;                                         // [SPLIT - 1][warp] x kSendBytes
+      uint8_t* recv = base + (SPLIT - 1) * kEpiWarps * kSendBytes;  // the same, by sender
+      static_assert(2 * (SPLIT - 1) * kEpiWarps * kSendBytes <= S * kStageBytes, "the exchange fits the ring");
+      // Place of column c of row `lane`: 16-byte pieces of 4 columns, rows side by side.
+      auto at = [&](uint8_t* buf, int c) { return reinterpret_cast<float4*>(buf + ((c >> 2) * 32 + lane) * 16); };
+      bool ok = mbar_wait(&bar->tfull[0], 0, p.ctl) && !aborted(bar);
+      if (lane == 0) mbar_expect_tx(&bar->recv[ew], (SPLIT - 1) * kSendBytes);
+      __syncwarp();
+      ok = all_of_256(ok);  // (all give up or none)
+      if (ok) {
+        tc_fence_after();
+        // the pair's MMAs are done, so its ring's memory takes in the others' sums now
+        if (warp == 2 && lane < SPLIT && lane != slot) arrive_cluster(map_cta(&bar->free[slot], 2 * lane + rank));
+#pragma unroll 1
+        for (int i = 1; i < SPLIT; ++i) {
+          const int owner = (slot + i) % SPLIT;
+          uint8_t* out = send + ((i - 1) * kEpiWarps + ew) * kSendBytes;
+#pragma unroll 1
+          for (int c = 0; c < 2 * W; c += 16) {
+            float v[16];
+            tmem_ld16_async(src + (c < W ? a0_of(owner) + c : b0_of(owner) + c - W), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) *at(out, c + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          }
+          fence_proxy_async_shared_cta();
+          __syncwarp();
+          if (lane == 0) {
+            if (!mbar_wait(&bar->free[owner], 0, p.ctl)) {
+              set_abort(bar);
+            } else {
+              const int by = slot < owner ? slot : slot - 1;  // this pair among the owner's senders
+              const uint32_t to = (uint32_t)(2 * owner) + rank;
+              copy_to_cta(map_cta(recv + (by * kEpiWarps + ew) * kSendBytes, to), out, kSendBytes,
+                          map_cta(&bar->recv[ew], to));
             }
           }
-          auto put = [&](const CUtensorMap* map, const uint32_t(&v)[32]) {
-            uint8_t* tile = next_tile();
+          __syncwarp();
+        }
+        ok = mbar_wait(&bar->recv[ew], 0, p.ctl);
+        if (!ok) {
+          DevCtl drain = p.ctl;
+          drain.spin_limit = 1000000000LL;
+          mbar_wait(&bar->recv[ew], 0, drain);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) {
+        set_abort(bar);
+      } else if (pair < tiles) {
+        int m, n;
+        tile_of(pair, mt, nt, m, n);
+        const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
+        // 16 columns' sums over the pairs in the order of k; place c in the exchange, TMEM column col
+        auto sum16 = [&](int c, int col, float* v) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              stage16(tile, lane, q, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-            put_tile(map, tile, x, y);
-          };
-          put(&p.out_g, dg);
-          put(&p.out_u, du);
-          put(&p.out, hh);
+          for (int k = 0; k < SPLIT; ++k) {
+            float x[16];
+            if (k == slot) {
+              tmem_ld16_async(src + col, x);
+              tmem_ld_wait();
+            } else {
+              uint8_t* in = recv + ((k < slot ? k : k - 1) * kEpiWarps + ew) * kSendBytes;
+#pragma unroll
+              for (int q = 0; q < 16; q += 4) {
+                const float4 f = *at(in, c + q);
+                x[q] = f.x, x[q + 1] = f.y, x[q + 2] = f.z, x[q + 3] = f.w;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = k == 0 ? x[q] : v[q] + x[q];
+          }
+        };
+        const int a0 = a0_of(slot), b0 = b0_of(slot);
+        if constexpr (EPI == kEpiGateUp && MX) {
+          static_assert(W == 32, "a warp holds whole groups");
+          float g[32], u[32];
+          sum16(0, a0, g);
+          sum16(16, a0 + 16, g + 16);
+          sum16(32, b0, u);
+          sum16(48, b0 + 16, u + 16);
+          finish_mx(row, n * TN + a0, g, u);
+        } else if (EPI == kEpiGateUp) {
+#pragma unroll 1
+          for (int c = 0; c < W; c += 16) {
+            float g[16], u[16];
+            sum16(c, a0 + c, g);
+            sum16(W + c, b0 + c, u);
+            finish(row, n * TN + a0 + c, g, u);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 2 * W; c += 16) {
+            float v[16];
+            sum16(c, a0 + c, v);
+            finish(row, n * TN + a0 + c, v, v);
+          }
         }
       }
     }
-    if (lane == 0) tma_store_wait_read<0>();
   }
 
   __syncthreads();
@@ -784,7 +653,7 @@ cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * SPLIT * clusters);
   cfg.blockDim = dim3(threads_of(MX));
-  cfg.dynamicSmemBytes = smem_of(EPI, MX, SPLIT);
+  cfg.dynamicSmemBytes = smem_of(MX);
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2 * SPLIT;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -832,17 +701,9 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
     const double cost = rounds * ((blocks + s - 1) / s + kTileCost + (s > 1 ? kSplitCost : 0));
     if (cost < best) best = cost, split = s;
   }
-  if (split == 1) {
-    ok = ok && (!out || make_bf16_map(e.encode, &p.out, out, p.N, p.M, p.N, 64, 32));
-    if (EPI != kEpiStore && !MX) {
-      uint16_t* pre = EPI == kEpiGrad ? p.dpre : p.pre_out;
-      if (pre)
-        ok = ok && make_bf16_map(e.encode, &p.out_g, pre, p.N, p.M, 2 * (uint64_t)p.N, 64, 32) &&
-             make_bf16_map(e.encode, &p.out_u, pre + p.N, p.N, p.M, 2 * (uint64_t)p.N, 64, 32);
-    }
-  }
   if (!ok) return cudaErrorInvalidValue;
   p.y = static_cast<uint16_t*>(out);
+  p.wide = p.N % 16 == 0;
   if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? (int)tiles : e.pairs, st);
   if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, (int)tiles, st);
   if constexpr (kMost == 4) return launch<EPI, A_MN, B_MN, MX, 4>(p, (int)tiles, st);
@@ -852,7 +713,7 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
 cudaError_t prepare(int* clusters) {
   auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>;
-  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(EPI, MX, SPLIT));
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(MX));
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(1, at);
@@ -943,7 +804,6 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
   p.N = s.I;
   p.K = s.d;
   p.act = s.act;
-  p.store_pre = pre != nullptr;
   p.pre_out = pre;
   return run<kEpiGateUp, false, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
 }

@@ -70,7 +70,7 @@ MOE_DEV uint64_t mx_scale_desc(uint32_t saddr) {
          (static_cast<uint64_t>(1) << 46);
 }
 // 16 consecutive fp32 columns of this thread's TMEM lane, valid after tmem_ld_wait().
-MOE_DEV void tmem_ld16_async(uint32_t taddr, float (&r)[16]) {
+MOE_DEV void tmem_ld16_async(uint32_t taddr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
