@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           store16(p.pre_out, 2 * p.N, row, col, v);
           store16(p.pre_out + p.N, 2 * p.N, row, col, u);
         }
+        with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = act_value(v[q], p.act) * u[q];
+          for (int q = 0; q < 16; ++q) v[q] = act_value<decltype(act)::value>(v[q]) * u[q];
+        });
         store16(p.y, p.N, row, col, v);
       } else {
         float dg[16], du[16], h[16];
@@ -408,16 +410,18 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
           const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + p.N) : make_uint4(0, 0, 0, 0);
           const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+          with_act(p.act, [&](auto act) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
-            const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
-            float a, da;
-            act_and_grad(gv, p.act, a, da);
-            dg[q + e] = v[q + e] * uv * da;
-            du[q + e] = v[q + e] * a;
-            h[q + e] = a * uv;
-          }
+            for (int e = 0; e < 8; ++e) {
+              const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
+              const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
+              float a, da;
+              act_and_grad<decltype(act)::value>(gv, a, da);
+              dg[q + e] = v[q + e] * uv * da;
+              du[q + e] = v[q + e] * a;
+              h[q + e] = a * uv;
+            }
+          });
         }
         store16(p.dpre, 2 * p.N, row, col, dg);
         store16(p.dpre + p.N, 2 * p.N, row, col, du);
@@ -427,11 +431,13 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     // mx8 gate/up: one row's 32 neurons, a group
     auto finish_mx = [&](int row, int col, float(&h)[32], const float(&u)[32]) {
       uint32_t top = 0;
+      with_act(p.act, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        h[e] = act_value(h[e], p.act) * u[e];
-        top = max(top, mag_bits(h[e]));
-      }
+        for (int e = 0; e < 32; ++e) {
+          h[e] = act_value<decltype(act)::value>(h[e]) * u[e];
+          top = max(top, mag_bits(h[e]));
+        }
+      });
       const uint32_t byte = mx_scale_byte(__uint_as_float(top));
       const float k = mx_inverse_scale(byte);
       if (row >= p.M || col >= p.N) return;
@@ -461,7 +467,12 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         auto release = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(map_cta(&bar->tempty[MX ? 0 : acc], lead));
+          // relaxed: only the TMEM reads above come before it, which have completed (a release would first wait for the
+          // rows stored so far, ~1 us)
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             map_cta(&bar->tempty[MX ? 0 : acc], lead))
+                         : "memory");
         };
         if (EPI == kEpiGateUp && MX) {
 #pragma unroll 1

@@ -103,15 +103,23 @@ MOE_DEV void arrive_cluster(uint32_t bar) {
 // g sigmoid(2 z): both from the fast exponential and division of sigmoid
 // (~2^-21 relative).
 // The logistic function, 0 below e^-80 (so that a huge negative g gives 0 and
-// not g e^-80; NaN stays NaN through the product with g).
-MOE_DEV float logistic(float z) { return z < -80.0f ? 0.0f : sigmoid(z); }
-MOE_DEV float act_value(float g, int act) {
-  if (act == MOE_ACT_SILU) return g * logistic(g);
+// not g e^-80; NaN stays NaN through the product with g).  Computed first and
+// selected after: as a branch every value would wait out the exponential's and
+// the division's latency alone.
+MOE_DEV float logistic(float z) {
+  const float p = sigmoid(z);
+  return z < -80.0f ? 0.0f : p;
+}
+// act(g), and the second form with its derivative.  ACT is a constant so that
+// the loops over values have no branch; with_act() picks it once per loop.
+template <int ACT>
+MOE_DEV float act_value(float g) {
+  if (ACT == MOE_ACT_SILU) return g * logistic(g);
   return g * logistic(1.5957691216057308f * (g + 0.044715f * g * g * g));
 }
-// act(g) and its derivative
-MOE_DEV void act_and_grad(float g, int act, float& a, float& da) {
-  if (act == MOE_ACT_SILU) {
+template <int ACT>
+MOE_DEV void act_and_grad(float g, float& a, float& da) {
+  if (ACT == MOE_ACT_SILU) {
     const float p = logistic(g);
     a = g * p;
     da = p + a * (1.0f - p);
@@ -122,6 +130,17 @@ MOE_DEV void act_and_grad(float g, int act, float& a, float& da) {
     // beyond |g| = 10 p is 0 or 1 to fp32 and the second term vanishes; the bound keeps an overflowing g^2 out
     da = p + a * (1.0f - p) * (1.5957691216057308f * (1.0f + 0.134145f * fminf(g2, 100.0f)));
   }
+}
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+template <typename F>
+MOE_DEV void with_act(int act, F&& f) {
+  if (act == MOE_ACT_SILU)
+    f(ActTag<MOE_ACT_SILU>());
+  else
+    f(ActTag<MOE_ACT_GELU>());
 }
 
 struct FfnShape {

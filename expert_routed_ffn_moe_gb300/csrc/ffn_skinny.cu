@@ -242,26 +242,43 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
     const int T = p.T, own = (T + C - 1) >> p.log_cluster;  // tokens per CTA
     const int n = unit * kRows + row;
     const bool in = n < p.N;
-    // token t's results: gate (or down) value v, up value u
-    auto finish = [&](int t, float v, float u) {
-      if (!GATE) {
-        if (in) p.y[(size_t)t * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-        return;
+    // The results of n tokens t, t + step, ...: gate (or down) values v, up values u.  No branch between the tokens, so
+    // that their activations' latencies overlap.
+    auto finish = [&](int t, int step, auto& v, const auto& u) {
+      constexpr int n_tok = sizeof(v) / sizeof(float);
+      if (GATE) {
+        with_act(p.act, [&](auto act) {
+#pragma unroll
+          for (int i = 0; i < n_tok; ++i) {
+            const float g = v[i];
+            const size_t at = (size_t)(t + i * step) * 2 * p.N + n;
+            if (!MX && p.pre && in && t + i * step < T) {
+              p.pre[at] = __bfloat16_as_ushort(__float2bfloat16_rn(g));
+              p.pre[at + p.N] = __bfloat16_as_ushort(__float2bfloat16_rn(u[i]));
+            }
+            v[i] = act_value<decltype(act)::value>(g) * u[i];
+          }
+        });
       }
-      const float h = act_value(v, p.act) * u;
-      if (MX) {
-        // N is a multiple of 32: the warp's group is all in or all out
-        const uint32_t byte = mx_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, mag_bits(h))));
-        if (in) {
-          p.hq[(size_t)t * p.N + n] = (uint8_t)e4m3x2(h * mx_inverse_scale(byte), 0.f);
-          if (lane == 0) p.hs[mx_scale_word(t, unit, mx_tile_cols(p.N)) + part] = (uint8_t)byte;
+      if (GATE && MX) {
+        uint32_t byte[n_tok];  // N is a multiple of 32: the warp's group is all in or all out
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i)
+          byte[i] = mx_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, mag_bits(v[i]))));
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i) {
+          const int ti = t + i * step;
+          if (in && ti < T) {
+            p.hq[(size_t)ti * p.N + n] = (uint8_t)e4m3x2(v[i] * mx_inverse_scale(byte[i]), 0.f);
+            if (lane == 0) p.hs[mx_scale_word(ti, unit, mx_tile_cols(p.N)) + part] = (uint8_t)byte[i];
+          }
         }
-      } else if (in) {
-        p.h[(size_t)t * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
-        if (p.pre) {
-          p.pre[(size_t)t * 2 * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-          p.pre[(size_t)t * 2 * p.N + p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(u));
-        }
+      } else {
+        uint16_t* out = GATE ? p.h : p.y;
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i)
+          if (in && t + i * step < T)
+            out[(size_t)(t + i * step) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
       }
     };
     bool ok = mbar_wait(&bar->tfull, 0, p.ctl) && !aborted(bar);
@@ -280,17 +297,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] += u[i];
         }
+        if (C == 1) {
+          finish(t0, 1, v, u);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = t0 + i;
-          if (t >= T) break;
-          if (C == 1) {
-            finish(t, v[i], u[i]);
-          } else {
-            const uint32_t at =
-                map_cta(exchange + ((rank * own + (t >> p.log_cluster)) * kParts) * kRows + row, t & (C - 1));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[i]) : "memory");
-            if (GATE) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + kRows * 4), "f"(u[i]) : "memory");
+          for (int i = 0; i < 16; ++i) {
+            const int t = t0 + i;
+            if (t < T) {
+              const uint32_t at =
+                  map_cta(exchange + ((rank * own + (t >> p.log_cluster)) * kParts) * kRows + row, t & (C - 1));
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[i]) : "memory");
+              if (GATE) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + kRows * 4), "f"(u[i]) : "memory");
+            }
           }
         }
       }
@@ -302,16 +320,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
         if (!__all_sync(0xffffffffu, ok)) {
           set_abort(bar);
         } else {
-          for (int t = rank, i = 0; t < T; t += C, ++i) {
-            float v = 0.f, u = 0.f;
+#pragma unroll 1
+          for (int i0 = 0; rank + i0 * C < T; i0 += 4) {  // four of this CTA's tokens, parts in the order of k
+            float v[4] = {}, u[4] = {};
+#pragma unroll 2
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int c = 0; c < kMaxCluster; ++c)
-              if (c < C) {
-                const float* q = exchange + ((c * own + i) * kParts) * kRows + row;
-                v += q[0];
-                if (GATE) u += q[kRows];
+              for (int j = 0; j < 4; ++j) {
+                const float* q = exchange + ((c * own + min(i0 + j, own - 1)) * kParts) * kRows + row;
+                v[j] += q[0];
+                if (GATE) u[j] += q[kRows];
               }
-            finish(t, v, u);
+            finish(rank + i0 * C, C, v, u);
           }
         }
       }
