@@ -484,20 +484,28 @@ class AddNorm:
         """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
         in the residual's dtype (x's without a residual)."""
         torch = _t()
-        _rows(x, "x", self.d)
+        shape = _rows(x, "x", self.d)
+        T, d = shape
+        px, pr, pw = _checked(x, "x", shape), _checked(residual, "residual", shape), _checked(weight, "weight", (d,))
+        like = x if residual is None else residual
         if s_out is None:
-            s_out = torch.empty_like(x if residual is None else residual)
+            s_out = torch.empty_like(like)
+        else:
+            _checked(s_out, "s_out", shape, like.dtype)
+        pys = None
         if y_dtype == MOE_BF16:
             y = torch.empty_like(x, dtype=torch.bfloat16)
+            py = y.data_ptr()
         elif y_dtype == MOE_F32:
             y = torch.empty_like(x, dtype=torch.float32)
+            py = y.data_ptr()
         elif y_dtype == MOE_MX8:
-            pair = _mx_empty(x.shape[0], self.d, x.device)
-            moe_add_norm(x, residual, weight, self.eps, s_out, *pair, stream)
-            return pair, s_out
+            y = _mx_empty(T, d, x.device)
+            py, pys = y[0].data_ptr(), y[1].data_ptr()
         else:
             raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
-        moe_add_norm(x, residual, weight, self.eps, s_out, y, None, stream)
+        _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T, d, self.eps,
+                                  s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x)), "moe_add_norm")
         return y, s_out
 
     def backward(self, s, weight, dy, ds=None, stream=None):
@@ -565,10 +573,13 @@ class GatedFfn:
                 _checked(down, "down", (d, I), bf16)
             pxs = pgs = pds = None
         if y is None:
-            y = torch.empty(T, d, dtype=bf16, device=rows.device) if self.mx else torch.empty_like(x)
+            y = torch.empty_like(rows, dtype=bf16) if self.mx else torch.empty_like(x)
+            py = y.data_ptr()
+        else:
+            py = _checked(y, "y", (T, d), bf16)
         if pre is None and save:
             pre = torch.empty(T, 2 * I, dtype=bf16, device=rows.device)
-        py, pp = _checked(y, "y", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16)
+        pp = _checked(pre, "pre", (T, 2 * I), bf16)
         _check(lib().moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(stream, rows)),
                "moe_ffn_forward")
         return (y, pre) if pre is not None else y

@@ -149,7 +149,7 @@ struct FfnShape {
 
 // ffn_norm.cu
 constexpr int kMaxNormWidth = 16384;
-constexpr int kNormPartials = 608;  // rows of partial weight gradients (4 blocks for each of 152 SMs)
+constexpr int kNormPartials = 1216;  // rows of partial weight gradients (8 for each of 152 SMs)
 struct NormArgs {
   const void *x, *res, *w;
   void *s, *y;

@@ -7,14 +7,19 @@
 //
 // Both are bound by memory: one pass over the rows, which stay in registers
 // between the reduction and the output (s is never read back).  A row belongs
-// to R threads, each holding C chunks of 8 neighbouring columns (16-byte loads
-// of bf16, two of fp32); R and C follow from the width alone (row_layout).  All
-// sums are fp32: 8 C columns per thread, then a shuffle tree, then the warps'
-// sums in order.  y is computed from the unrounded s and rounded once.
+// to R threads, each holding up to two chunks of 8 neighbouring columns
+// (16-byte loads of bf16, two of fp32); R follows from the width alone.  Blocks
+// walk over rows and ask for the next row before they reduce the present one:
+// without that a block waits out the memory's latency once per row, and the
+// rows in flight do not cover the bandwidth.  All sums are fp32: a thread's
+// columns, then a shuffle tree, then the warps' sums in order.  y is computed
+// from the unrounded s and rounded once.
 //
 // A width that is not a multiple of 8 leaves rows unaligned; the chunks are
 // then the aligned 16-byte windows of the whole matrix that cover the row, with
-// the neighbours' columns masked, so the loads stay wide (ODD).
+// the neighbours' columns masked, so the loads stay wide (ODD).  The weight is
+// not aligned with those windows; it lies in shared memory by (column mod 8),
+// where neighbouring threads' columns are neighbours.
 #include "ffn_internal.h"
 
 namespace moe {
@@ -24,18 +29,34 @@ struct F8 {
   float v[8];
 };
 
+// A chunk as it lies in memory.
 template <typename T>
-MOE_DEV F8 load8(const T* p);
+struct Raw;
 template <>
-MOE_DEV F8 load8<float>(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
+struct Raw<float> {
+  float4 a, b;
+  MOE_DEV void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  MOE_DEV void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  MOE_DEV F8 get() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
 template <>
-MOE_DEV F8 load8<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  return F8{{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w),
-             bf16_hi(a.w)}};
+struct Raw<__nv_bfloat16> {
+  uint4 a;
+  MOE_DEV void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  MOE_DEV void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  MOE_DEV F8 get() const {
+    return F8{{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w),
+               bf16_hi(a.w)}};
+  }
+};
+template <typename T>
+MOE_DEV F8 load8(const T* p) {
+  Raw<T> r;
+  r.load(p);
+  return r.get();
 }
 MOE_DEV void store8(float* p, const F8& f) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
@@ -50,21 +71,17 @@ MOE_DEV float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 MOE_DEV void put(float* p, float v) { *p = v; }
 MOE_DEV void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The chunk of 8 columns at e of a matrix of n values; columns outside [lo, hi) read 0.
-template <typename T, bool ODD>
-MOE_DEV F8 load_chunk(const T* p, size_t e, size_t n, size_t lo, size_t hi) {
-  if (!ODD) return load8(p + e);
-  F8 f;
-  if (e + 8 <= n) {
-    f = load8(p + e);
+// The chunk of 8 columns at e of a matrix of n values; what lies past its end reads 0.
+template <bool ODD, typename T>
+MOE_DEV void load_raw(Raw<T>& r, const T* p, size_t e, size_t n) {
+  if (!ODD || e + 8 <= n) {
+    r.load(p + e);
   } else {
+    __align__(16) T t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f.v[i] = e + i < n ? to_f(p[e + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) put(t + i, e + i < n ? to_f(p[e + i]) : 0.f);
+    r.load(t);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e + i < lo || e + i >= hi) f.v[i] = 0.f;
-  return f;
 }
 template <typename T, bool ODD>
 MOE_DEV void store_chunk(T* p, size_t e, size_t lo, size_t hi, const F8& f) {
@@ -77,15 +94,21 @@ MOE_DEV void store_chunk(T* p, size_t e, size_t lo, size_t hi, const F8& f) {
   }
 }
 
-// The sum over the R threads of a row, in every one of them.
-template <int R>
-MOE_DEV float row_sum(float v, float* red) {
-  v = warp_sum(v);
-  if (R == 32) return v;
+// The sums over the R threads of a row, in every one of them.  `red` is another
+// half of its memory from one row to the next, so one barrier per row suffices.
+template <int R, int N>
+MOE_DEV void row_sums(float (&v)[N], float (*red)[N][32]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  if (R == 32) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[warp] = v;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) (*red)[i][warp] = v[i];
+  }
   __syncthreads();
-  return warp_sum(lane < R / 32 ? red[lane] : 0.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < R / 32 ? (*red)[i][lane] : 0.f);
 }
 
 // The scale and the codes of this thread's 8 columns of a group of 32 (4
@@ -110,239 +133,246 @@ MOE_DEV uint32_t gather_scales(uint32_t byte) {
 
 template <typename XT, typename ST, int R, int C, bool ODD>
 __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
-  __shared__ float red[32];
+  __shared__ float red[2][1][32];
+  extern __shared__ float wsm[];  // ODD: the weight, [8][(d + 7) / 8]
   constexpr int kRows = R == 32 ? 4 : 1;
-  const int row = blockIdx.x * kRows + (R == 32 ? threadIdx.x >> 5 : 0);
   const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x;
   const size_t tile_cols = mx_tile_cols(a.d);
-  if (row >= a.T) {
-    // rows that only pad the last scale tile
-    if (a.y_dtype == MOE_MX8 && row < (a.T + 127) / 128 * 128)
-      for (size_t w = tid; w < tile_cols; w += R)
-        *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(row, w, tile_cols)) = 0u;
-    return;
-  }
-  const size_t n = (size_t)a.T * a.d, lo = (size_t)row * a.d, hi = lo + a.d;
-  const size_t c0 = lo / 8;
-  const int chunks = (int)((hi + 7) / 8 - c0);
-  const XT* x = static_cast<const XT*>(a.x);
-  const ST* res = static_cast<const ST*>(a.res);
+  const size_t n = (size_t)a.T * a.d;
+  const XT* x_in = static_cast<const XT*>(a.x);
+  const ST* r_in = static_cast<const ST*>(a.res);
   ST* s_out = static_cast<ST*>(a.s);
+  const int wpitch = (a.d + 7) / 8;
+  const int rows = a.y_dtype == MOE_MX8 ? (a.T + 127) / 128 * 128 : a.T;  // (the last scale tile's padding too)
+  const int stride = gridDim.x * kRows;
+  int row = blockIdx.x * kRows + (R == 32 ? threadIdx.x >> 5 : 0);
 
-  F8 s[C];
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int c = tid + j * R;
-    if (c < chunks) {
-      s[j] = load_chunk<XT, ODD>(x, (c0 + c) * 8, n, lo, hi);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[j].v[i] = 0.f;
-    }
-  }
-  if (res) {
+  auto load_row = [&](int r, Raw<XT>(&x)[C], Raw<ST>(&res)[C]) {
+    const size_t lo = (size_t)r * a.d, c0 = lo / 8;
+    const int chunks = (int)((lo + a.d + 7) / 8 - c0);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const int c = tid + j * R;
       if (c < chunks) {
-        const F8 r = load_chunk<ST, ODD>(res, (c0 + c) * 8, n, lo, hi);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[j].v[i] += r.v[i];
+        load_raw<ODD>(x[j], x_in, (c0 + c) * 8, n);
+        if (r_in) load_raw<ODD>(res[j], r_in, (c0 + c) * 8, n);
+      } else {
+        x[j].zero();
+        res[j].zero();
       }
     }
+  };
+  Raw<XT> x[C];
+  Raw<ST> res[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) res[j].zero();
+  if (row < a.T) load_row(row, x, res);
+  F8 w[C];
+  auto weight = [&](int k) {
+    return a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
+                                 : static_cast<const float*>(a.w)[k];
+  };
+  if (ODD) {
+    for (int k = threadIdx.x; k < a.d; k += blockDim.x) wsm[(k & 7) * wpitch + (k >> 3)] = weight(k);
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if ((tid + j * R) * 8 < a.d)
+        w[j] = a.w_dtype == MOE_BF16 ? load8(static_cast<const __nv_bfloat16*>(a.w) + (tid + j * R) * 8)
+                                     : load8(static_cast<const float*>(a.w) + (tid + j * R) * 8);
   }
-  float ss = 0.f;
+
+  for (int it = 0; row < rows; row += stride, it ^= 1) {
+    if (row >= a.T) {  // (a row of the padding: R threads leave together)
+      for (size_t q = tid; q < tile_cols; q += R)
+        *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(row, q, tile_cols)) = 0u;
+      continue;
+    }
+    const size_t lo = (size_t)row * a.d, hi = lo + a.d, c0 = lo / 8;
+    const int chunks = (int)((hi + 7) / 8 - c0);
+    F8 s[C];
+    float sum[1] = {0.f};
 #pragma unroll
-  for (int j = 0; j < C; ++j)
+    for (int j = 0; j < C; ++j) {
+      s[j] = x[j].get();
+      const F8 r = res[j].get();
+      const size_t e = (c0 + tid + j * R) * 8;
+      const bool edge = ODD && (e < lo || e + 8 > hi);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += s[j].v[i] * s[j].v[i];
-  if (s_out) {
+      for (int i = 0; i < 8; ++i) {
+        s[j].v[i] += r.v[i];
+        if (edge && (e + i < lo || e + i >= hi)) s[j].v[i] = 0.f;
+        sum[0] += s[j].v[i] * s[j].v[i];
+      }
+    }
+    if (row + stride < a.T) load_row(row + stride, x, res);  // in flight while this row is finished
+    if (s_out) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (tid + j * R < chunks) store_chunk<ST, ODD>(s_out, (c0 + tid + j * R) * 8, lo, hi, s[j]);
+    }
+    row_sums<R>(sum, &red[it]);
+    const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const int c = tid + j * R;
-      if (c < chunks) store_chunk<ST, ODD>(s_out, (c0 + c) * 8, lo, hi, s[j]);
-    }
-  }
-  const float rstd = rsqrtf(row_sum<R>(ss, red) / (float)a.d + a.eps);
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int c = tid + j * R;
-    const bool in = c < chunks;
-    const size_t e = (c0 + c) * 8;
-    F8 y;
-    if (in) {
-      F8 w;
-      if (!ODD) {
-        w = a.w_dtype == MOE_BF16 ? load8(static_cast<const __nv_bfloat16*>(a.w) + c * 8)
-                                  : load8(static_cast<const float*>(a.w) + c * 8);
-      } else {  // the weight's columns are not aligned with the windows
+      const bool in = c < chunks;
+      const size_t e = (c0 + c) * 8;
+      F8 y;
+      if (ODD) {
+        // column e + i - lo of the weight: the same residue mod 8 in every thread
+        const int k0 = (int)((ptrdiff_t)e - (ptrdiff_t)lo);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool ok = e + i >= lo && e + i < hi;
-          const int k = ok ? (int)(e + i - lo) : 0;
-          const float v = a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
-                                                : static_cast<const float*>(a.w)[k];
-          w.v[i] = ok ? v : 0.f;
+          const int k = k0 + i;
+          y.v[i] = in && k >= 0 && k < a.d ? s[j].v[i] * rstd * wsm[(k & 7) * wpitch + (k >> 3)] : 0.f;
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y.v[i] = in ? s[j].v[i] * rstd * w[j].v[i] : 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y.v[i] = s[j].v[i] * rstd * w.v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y.v[i] = 0.f;
-    }
-    if (a.y_dtype == MOE_MX8) {
-      uint32_t byte;
-      const uint2 q = quantize8(y, byte);
-      if (!in) byte = 0u;  // groups past the last column
-      const uint32_t word = gather_scales(byte);
-      if (in) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + e) = q;
-      if (in && c % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(row, c / 16, tile_cols)) = word;
-    } else if (in) {
-      if (a.y_dtype == MOE_BF16)
-        store_chunk<__nv_bfloat16, ODD>(static_cast<__nv_bfloat16*>(a.y), e, lo, hi, y);
-      else
-        store_chunk<float, ODD>(static_cast<float*>(a.y), e, lo, hi, y);
+      if (a.y_dtype == MOE_MX8) {
+        uint32_t byte;
+        const uint2 q = quantize8(y, byte);
+        if (!in) byte = 0u;  // groups past the last column
+        const uint32_t word = gather_scales(byte);
+        if (in) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + e) = q;
+        if (in && c % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(row, c / 16, tile_cols)) = word;
+      } else if (in) {
+        if (a.y_dtype == MOE_BF16)
+          store_chunk<__nv_bfloat16, ODD>(static_cast<__nv_bfloat16*>(a.y), e, lo, hi, y);
+        else
+          store_chunk<float, ODD>(static_cast<float*>(a.y), e, lo, hi, y);
+      }
     }
   }
 }
 
-// Gradients.  A block walks rows blockIdx.x, + gridDim.x, ...; every thread
-// keeps the weight gradient of its own columns in registers over all of them
-// and leaves it in row blockIdx.x of `partial`, which norm_grad_sum_kernel adds
-// up in a fixed order (no atomics: the result does not depend on timing).  The
-// columns of a thread must be the same for every row, so rows of odd width are
-// read one column at a time (neighbouring threads, neighbouring columns).
+// Gradients.  A block (R == 32: a warp) walks rows as above; every thread keeps
+// the weight gradient of its own columns in registers over all of them and
+// leaves it in a row of `partial`, which norm_grad_sum_kernel adds up in a fixed
+// order (no atomics: the result does not depend on timing).  The columns of a
+// thread must be the same for every row, so rows of odd width are read one
+// column at a time (neighbouring threads, neighbouring columns).
 template <typename ST, int R, int C, bool ODD>
-__global__ void __launch_bounds__(R) norm_grad_kernel(NormGradArgs a) {
-  __shared__ float red[2][32];
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradArgs a) {
+  __shared__ float red[2][2][32];
+  constexpr int kRows = R == 32 ? 4 : 1;
+  const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int first = blockIdx.x * kRows + (R == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows;
   const ST* s_in = static_cast<const ST*>(a.s);
   const ST* dy_in = static_cast<const ST*>(a.dy);
   const ST* ds_in = static_cast<const ST*>(a.ds);
   ST* dx = static_cast<ST*>(a.dx);
   // column of value i of chunk j: 8 (tid + j R) + i, or tid + (8 j + i) R
   auto column = [&](int j, int i) { return ODD ? tid + (8 * j + i) * R : (tid + j * R) * 8 + i; };
-  F8 acc[C];
+  F8 acc[C], w[C];
 #pragma unroll
   for (int j = 0; j < C; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[j].v[i] = 0.f;
-  auto load_weight = [&](int j) {
-    F8 w;
-    if (!ODD && column(j, 0) < a.d) {
-      w = a.w_dtype == MOE_BF16 ? load8(static_cast<const __nv_bfloat16*>(a.w) + column(j, 0))
-                                : load8(static_cast<const float*>(a.w) + column(j, 0));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = column(j, i);
-        w.v[i] = k >= a.d ? 0.f
-                          : (a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
-                                                   : static_cast<const float*>(a.w)[k]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int k = column(j, i);
+      acc[j].v[i] = 0.f;
+      w[j].v[i] = k >= a.d ? 0.f
+                           : (a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
+                                                    : static_cast<const float*>(a.w)[k]);
     }
-    return w;
-  };
-  auto load_row = [&](const ST* p, size_t lo, F8(&f)[C]) {
+  auto load_row = [&](const ST* p, int row, Raw<ST>(&f)[C]) {
+    const size_t lo = (size_t)row * a.d;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       if (ODD) {
+        __align__(16) ST t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[j].v[i] = column(j, i) < a.d ? to_f(p[lo + column(j, i)]) : 0.f;
+        for (int i = 0; i < 8; ++i) t[i] = column(j, i) < a.d ? p[lo + column(j, i)] : ST(0.f);
+        f[j].load(t);
       } else if (column(j, 0) < a.d) {
-        f[j] = load8(p + lo + column(j, 0));
+        f[j].load(p + lo + column(j, 0));
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[j].v[i] = 0.f;
+        f[j].zero();
       }
     }
   };
-  for (int row = blockIdx.x, it = 0; row < a.T; row += gridDim.x, ++it) {
+  Raw<ST> rs[C], rdy[C], rds[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) rds[j].zero();
+  auto load_all = [&](int row) {
+    load_row(s_in, row, rs);
+    load_row(dy_in, row, rdy);
+    if (ds_in) load_row(ds_in, row, rds);
+  };
+  if (first < a.T) load_all(first);
+  for (int row = first, it = 0; row < a.T; row += stride, it ^= 1) {
     const size_t lo = (size_t)row * a.d;
-    F8 s[C], dy[C];
-    load_row(s_in, lo, s);
-    load_row(dy_in, lo, dy);
-    float ss = 0.f, sg = 0.f;
+    Raw<ST> cs[C], cdy[C], cds[C];
+    float sum[2] = {0.f, 0.f};  // s^2 and s dy w
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const F8 w = load_weight(j);
+      cs[j] = rs[j];
+      cdy[j] = rdy[j];
+      cds[j] = rds[j];
+      const F8 s = cs[j].get(), dy = cdy[j].get();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ss += s[j].v[i] * s[j].v[i];
-        sg += s[j].v[i] * dy[j].v[i] * w.v[i];
+        sum[0] += s.v[i] * s.v[i];
+        sum[1] += s.v[i] * dy.v[i] * w[j].v[i];
       }
     }
-    ss = warp_sum(ss);
-    sg = warp_sum(sg);
-    if (R > 32) {
-      const int warp = tid >> 5, lane = tid & 31;
-      __syncthreads();  // the previous row's sums have been read
-      if (lane == 0) {
-        red[0][warp] = ss;
-        red[1][warp] = sg;
+    if (row + stride < a.T) load_all(row + stride);  // in flight while this row is finished
+    row_sums<R>(sum, &red[it]);
+    const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
+    const float k = sum[1] * rstd / (float)a.d;  // mean(g n)
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const F8 s = cs[j].get(), dy = cdy[j].get();
+      F8 o = cds[j].get();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = s.v[i] * rstd;
+        o.v[i] += rstd * (dy.v[i] * w[j].v[i] - n * k);
+        acc[j].v[i] += dy.v[i] * n;
       }
-      __syncthreads();
-      ss = warp_sum(lane < R / 32 ? red[0][lane] : 0.f);
-      sg = warp_sum(lane < R / 32 ? red[1][lane] : 0.f);
-    }
-    const float rstd = rsqrtf(ss / (float)a.d + a.eps);
-    const float k = sg * rstd / (float)a.d;  // mean(g n)
-    if (dx) {
-      F8 o[C];
-      if (ds_in) {
-        load_row(ds_in, lo, o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[j].v[i] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const F8 w = load_weight(j);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[j].v[i] += rstd * (dy[j].v[i] * w.v[i] - s[j].v[i] * rstd * k);
+      if (dx) {
         if (ODD) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (column(j, i) < a.d) put(dx + lo + column(j, i), o[j].v[i]);
+            if (column(j, i) < a.d) put(dx + lo + column(j, i), o.v[i]);
         } else if (column(j, 0) < a.d) {
-          store8(dx + lo + column(j, 0), o[j]);
+          store8(dx + lo + column(j, 0), o);
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[j].v[i] += dy[j].v[i] * (s[j].v[i] * rstd);
   }
-  if (a.dw) {
+  if (a.dw && first < a.T) {
 #pragma unroll
     for (int j = 0; j < C; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (column(j, i) < a.d) a.partial[(size_t)blockIdx.x * a.d + column(j, i)] = acc[j].v[i];
+        if (column(j, i) < a.d) a.partial[(size_t)first * a.d + column(j, i)] = acc[j].v[i];
   }
 }
 
-// dw[c] = the sum of the blocks' partial gradients: 32 columns per block, 8
-// threads per column over every 8th partial row, then the eight in order.
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float* partial, int rows, int d, void* dw,
-                                                            int w_dtype) {
-  __shared__ float part[8][32];
+// dw[c] = the sum of the partial gradients: 32 columns per block, 32 threads
+// per column over every 32nd partial row, then the 32 in order.
+__global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partial, int rows, int d, void* dw,
+                                                             int w_dtype) {
+  __shared__ float part[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (c < d)
-    for (int r = threadIdx.y; r < rows; r += 8) v += partial[(size_t)r * d + c];
+  if (c < d) {
+#pragma unroll 4
+    for (int r = threadIdx.y; r < rows; r += 32) v += partial[(size_t)r * d + c];
+  }
   part[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && c < d) {
-    for (int i = 1; i < 8; ++i) v += part[i][threadIdx.x];
+  const float t = warp_sum(part[threadIdx.x][threadIdx.y]);  // column threadIdx.y of the block
+  const int k = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && k < d) {
     if (w_dtype == MOE_BF16)
-      static_cast<__nv_bfloat16*>(dw)[c] = __float2bfloat16_rn(v);
+      static_cast<__nv_bfloat16*>(dw)[k] = __float2bfloat16_rn(t);
     else
-      static_cast<float*>(dw)[c] = v;
+      static_cast<float*>(dw)[k] = t;
   }
 }
 
@@ -372,64 +402,92 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const T* v, int rows, 
   if (c % 16 == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(row, c / 16, tile_cols)) = word;
 }
 
-// Threads per row: the fewest (a power of two, 32 at least) that hold the row
-// in at most 4 chunks of 8 columns each.
-int row_threads(int chunks) {
-  int r = 32;
-  while (r < 1024 && r * 4 < chunks) r *= 2;
-  return r;
+// Blocks that walk the rows: as many as are resident on the device's SMs.
+template <typename K>
+int resident_blocks(K kernel, int block, size_t smem) {
+  int dev = 0, sms = 1, per = 1;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, smem) != cudaSuccess || per < 1) per = 1;
+  return sms * per;
 }
 
-template <typename XT, typename ST, int R, int C>
-cudaError_t norm_odd(const NormArgs& a, cudaStream_t st) {
+template <typename XT, typename ST, int R, int C, bool ODD>
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
+  constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
+  const auto kernel = norm_kernel<XT, ST, R, C, ODD>;
+  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+  }
   const int rows = a.y_dtype == MOE_MX8 ? (a.T + 127) / 128 * 128 : a.T;
-  const int grid = R == 32 ? (rows + 3) / 4 : rows;
-  const int block = R == 32 ? 128 : R;
-  if (a.d % 8 == 0)
-    norm_kernel<XT, ST, R, C, false><<<grid, block, 0, st>>>(a);
-  else
-    norm_kernel<XT, ST, R, C, true><<<grid, block, 0, st>>>(a);
+  int grid = (rows + kRows - 1) / kRows;
+  // (a grid of fewer blocks than SMs needs no look at what is resident; without the weight in shared memory the answer
+  // is one number per kernel)
+  if (grid > 128) {
+    int most;
+    if constexpr (ODD) {
+      most = resident_blocks(kernel, kBlock, smem);
+    } else {
+      static const int resident = resident_blocks(kernel, kBlock, 0);
+      most = resident;
+    }
+    if (grid > most) grid = most;
+  }
+  kernel<<<grid, kBlock, smem, st>>>(a);
   return cudaGetLastError();
+}
+// Threads per row: one or two chunks of 8 columns each.
+template <typename XT, typename ST, bool ODD>
+cudaError_t norm_width(const NormArgs& a, cudaStream_t st) {
+  const int chunks = ODD ? (a.d + 7) / 8 + 1 : a.d / 8;  // an unaligned row may touch one window more
+  if (chunks <= 32) return norm_launch<XT, ST, 32, 1, ODD>(a, st);
+  if (chunks <= 64) return norm_launch<XT, ST, 32, 2, ODD>(a, st);
+  if (chunks <= 128) return norm_launch<XT, ST, 128, 1, ODD>(a, st);
+  if (chunks <= 256) return norm_launch<XT, ST, 128, 2, ODD>(a, st);
+  if (chunks <= 512) return norm_launch<XT, ST, 256, 2, ODD>(a, st);
+  if (chunks <= 1024) return norm_launch<XT, ST, 512, 2, ODD>(a, st);
+  if (chunks <= 2048) return norm_launch<XT, ST, 1024, 2, ODD>(a, st);
+  if constexpr (ODD) return norm_launch<XT, ST, 1024, 3, true>(a, st);  // the widest odd rows
+  return cudaErrorInvalidValue;
 }
 template <typename XT, typename ST>
 cudaError_t norm_typed(const NormArgs& a, cudaStream_t st) {
-  const int chunks = a.d % 8 == 0 ? a.d / 8 : (a.d + 7) / 8 + 1;  // an unaligned row may touch one window more
-  switch (row_threads(chunks)) {
-    case 32:
-      if (chunks <= 32) return norm_odd<XT, ST, 32, 1>(a, st);
-      return norm_odd<XT, ST, 32, 4>(a, st);
-    case 64: return norm_odd<XT, ST, 64, 4>(a, st);
-    case 128: return norm_odd<XT, ST, 128, 4>(a, st);
-    case 256: return norm_odd<XT, ST, 256, 4>(a, st);
-    case 512: return norm_odd<XT, ST, 512, 4>(a, st);
-    default: return norm_odd<XT, ST, 1024, 4>(a, st);  // the widest odd rows
-  }
+  return a.d % 8 == 0 ? norm_width<XT, ST, false>(a, st) : norm_width<XT, ST, true>(a, st);
 }
 
-template <typename ST, int R, int C>
-cudaError_t grad_odd(const NormGradArgs& a, cudaStream_t st) {
-  const int grid = a.T < kNormPartials ? a.T : kNormPartials;
-  if (a.d % 8 == 0)
-    norm_grad_kernel<ST, R, C, false><<<grid, R, 0, st>>>(a);
-  else
-    norm_grad_kernel<ST, R, C, true><<<grid, R, 0, st>>>(a);
+template <typename ST, int R, int C, bool ODD>
+cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
+  constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
+  const auto kernel = norm_grad_kernel<ST, R, C, ODD>;
+  int grid = (a.T + kRows - 1) / kRows;
+  if (grid > 128) {
+    static const int resident = resident_blocks(kernel, kBlock, 0);
+    const int most = resident < kNormPartials / kRows ? resident : kNormPartials / kRows;
+    if (grid > most) grid = most;
+  }
+  kernel<<<grid, kBlock, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dw) return e;
-  norm_grad_sum_kernel<<<(a.d + 31) / 32, dim3(32, 8), 0, st>>>(a.partial, grid, a.d, a.dw, a.w_dtype);
+  const int partials = a.T < grid * kRows ? a.T : grid * kRows;
+  norm_grad_sum_kernel<<<(a.d + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, partials, a.d, a.dw, a.w_dtype);
   return cudaGetLastError();
+}
+template <typename ST, bool ODD>
+cudaError_t grad_width(const NormGradArgs& a, cudaStream_t st) {
+  const int chunks = (a.d + 7) / 8;
+  if (chunks <= 32) return grad_launch<ST, 32, 1, ODD>(a, st);
+  if (chunks <= 64) return grad_launch<ST, 32, 2, ODD>(a, st);
+  if (chunks <= 128) return grad_launch<ST, 128, 1, ODD>(a, st);
+  if (chunks <= 256) return grad_launch<ST, 128, 2, ODD>(a, st);
+  if (chunks <= 512) return grad_launch<ST, 256, 2, ODD>(a, st);
+  if (chunks <= 1024) return grad_launch<ST, 512, 2, ODD>(a, st);
+  return grad_launch<ST, 1024, 2, ODD>(a, st);
 }
 template <typename ST>
 cudaError_t grad_typed(const NormGradArgs& a, cudaStream_t st) {
-  const int chunks = (a.d + 7) / 8;
-  switch (row_threads(chunks)) {
-    case 32:
-      if (chunks <= 32) return grad_odd<ST, 32, 1>(a, st);
-      return grad_odd<ST, 32, 4>(a, st);
-    case 64: return grad_odd<ST, 64, 4>(a, st);
-    case 128: return grad_odd<ST, 128, 4>(a, st);
-    case 256: return grad_odd<ST, 256, 4>(a, st);
-    default: return grad_odd<ST, 512, 4>(a, st);
-  }
+  return a.d % 8 == 0 ? grad_width<ST, false>(a, st) : grad_width<ST, true>(a, st);
 }
 
 }  // namespace
