@@ -63,7 +63,10 @@ constexpr int threads_of(bool mx) { return (mx ? kScaleWarp + 1 : kBWarp + 1) * 
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
-constexpr int kTileCost = 10, kSplitCost = 6; // of a tile besides its k blocks, in k blocks (~0.27 us), see run()
+// What a tile costs besides its k blocks, in k blocks (~0.27 us), see run(): its start and end; its epilogue by kind
+// (a split divides that too); the exchange of a split.
+constexpr int kTileCost = 6, kSplitCost = 7;
+constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 1 ? 9 : 16; }
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
 enum { kEpiStore, kEpiGateUp, kEpiGrad };
@@ -700,8 +703,10 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
   const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int blocks = (p.K + (MX ? 127 : 63)) / (MX ? 128 : 64);
-  // Pairs that a tile's reduction is split over: time of a pair ~ rounds of tiles x (k blocks + what a tile costs
-  // besides them, in k blocks); a split adds the exchange.
+  // Pairs that a tile's reduction is split over: the least of rounds of tiles x time of a tile.  Measured (us for the
+  // two products of a forward call, all with 1, 2 or 4, against this choice for each): T = 128, d = 2048, I = 8192:
+  // 58.1, 50.4, 68.6 -> 34.8; T = 1024, d = 2048, I = 2048: 29.9, 36.2, 79.5 -> 27.1; T = 2048, d = 2048, I = 8192:
+  // 120.4, 223.5, 427.3 -> 120.7.
   constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
   int split = 1;
   double best = 1e30;
@@ -709,7 +714,7 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b,
     const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : e.pairs4;  // clusters that run at a time
     if (fit < 1) break;
     const double rounds = (double)((tiles + fit - 1) / fit);
-    const double cost = rounds * ((blocks + s - 1) / s + kTileCost + (s > 1 ? kSplitCost : 0));
+    const double cost = rounds * ((blocks + s - 1) / s + kTileCost + (double)epilogue_cost(EPI) / s + (s > 1 ? kSplitCost : 0));
     if (cost < best) best = cost, split = s;
   }
   if (!ok) return cudaErrorInvalidValue;
