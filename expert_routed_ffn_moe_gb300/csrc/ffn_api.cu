@@ -236,20 +236,13 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
   const FfnShape s{T, c.d, c.inter, c.activation};
   auto in = [](const void* p) { return static_cast<const uint16_t*>(p); };
   auto out = [](void* p) { return static_cast<uint16_t*>(p); };
-  const FfnScratch& sc = ctx->sc;
-  cudaError_t err = launch_ffn_grad_h(ctx->eng, s, in(dy), in(down), in(pre), sc.dpre, sc.h, st);
+  const FfnBackwardArgs a{in(x), in(pre), in(gate_up), in(down), in(dy), out(dx), out(dgate_up), out(ddown)};
+  cudaError_t err = launch_ffn_grad_h(ctx->eng, s, a, ctx->sc, st);
   ++ctx->launches;
-  if (err == cudaSuccess && dx) {
-    err = launch_ffn_dx(ctx->eng, s, sc.dpre, in(gate_up), out(dx), st);
-    ++ctx->launches;
-  }
-  if (err == cudaSuccess && dgate_up) {
-    err = launch_ffn_weight_grad(ctx->eng, sc.dpre, 2 * s.I, in(x), s.d, T, out(dgate_up), st);
-    ++ctx->launches;
-  }
-  if (err == cudaSuccess && ddown) {
-    err = launch_ffn_weight_grad(ctx->eng, in(dy), s.d, sc.h, s.I, T, out(ddown), st);
-    ++ctx->launches;
+  if (err == cudaSuccess) {
+    int n = 0;
+    err = launch_ffn_grads(ctx->eng, s, a, ctx->sc, &n, st);
+    ctx->launches += n;
   }
   return cuda_code(err);
 }

@@ -65,23 +65,32 @@ constexpr int kSharedCols = 32;             // mx8: accumulator columns that bot
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
 // What a tile costs besides its k blocks, in k blocks (~0.27 us), see run(): its start and end; its epilogue by kind
 // (a split divides that too); the exchange of a split.
-constexpr int kTileCost = 6, kSplitCost = 7;
+constexpr int kTileCost = 6, kSplitCost = 7, kLaunchCost = 8;  // (and of another launch)
 constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 1 ? 9 : 16; }
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
 enum { kEpiStore, kEpiGateUp, kEpiGrad };
 
+// One product: result [M, N] = a b^T over K.
+struct Product {
+  CUtensorMap a, b;
+  uint16_t* y;                     // bf16 result: y / dx / dW, or h
+  int M, N, K;                     // N: columns of the result (gate/up: neurons)
+  int a_mn;                        // MULTI: a is MN-major
+  int wide;                        // rows of the results are 32-byte aligned: N is a multiple of 16
+  int mt, nt, tiles, blocks;       // m-tiles, n-tiles, their product, k blocks
+};
 struct GemmParams {
-  CUtensorMap a, b;                // operands
+  Product q[3];                    // MULTI: up to three, those with the longer reduction first; else one
+  int count;                       // MULTI: products
+  int heavy_count, heavy_tiles;    // MULTI: the first products, of the longer reduction, and their tiles
+  int early;                       // MULTI: light tiles that take as long as a heavy one
   CUtensorMap as, bs0, bs1;        // mx8 scales: of A, and of the two 128-row halves of B
   uint8_t *hq, *hs;                // mx8 gate/up: codes and scales of h
-  uint16_t* y;                     // bf16 result [M, N]: y / dx / dW, or h
   uint16_t* pre_out;               // gate/up: pre [M, 2N], or NULL
   const uint16_t* pre;             // grad: pre [M, 2N]
   uint16_t* dpre;                  // grad: [M, 2N]
-  int M, N, K;                     // N: columns of the result (gate/up: neurons)
   int act;
-  int wide;                        // rows of the results are 32-byte aligned: N is a multiple of 16
   DevCtl ctl;
 };
 
@@ -208,15 +217,50 @@ MOE_DEV void copy_to_cta(uint32_t dst, const void* src, uint32_t bytes, uint32_t
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
 MOE_DEV void set_abort(Bars* b) { *reinterpret_cast<volatile int*>(&b->abort_flag) = 1; }
 
-// Tile t of the sweep: kGroupM m-tiles at a time, all n for each group.
-MOE_DEV void tile_of(int t, int mt, int nt, int& m, int& n) {
-  const int per = kGroupM * nt, g = t / per, r = t - g * per;
+// The j-th tile of a pair: its product, m-tile and n-tile; false past the last.
+// A product's tiles are swept kGroupM m-tiles at a time, all n for each group,
+// so that the pairs of one moment share operands in L2.
+//
+// MULTI: independent products in one launch, so that only one of them ends with
+// idle pairs.  The heavy tiles (longer reduction) are dealt out first, round
+// robin; the light tiles follow in the order in which pairs come free: the pairs
+// that got one heavy tile less deal among themselves for the `early` rounds that
+// a heavy tile lasts, then all deal.
+struct Tile {
+  int q, m, n;
+};
+template <bool MULTI>
+MOE_DEV bool tile_of(const GemmParams& p, int pair, int pairs, int j, Tile& t) {
+  int i;
+  t.q = 0;
+  if (!MULTI) {
+    i = pair + j * pairs;
+    if (i >= p.q[0].tiles) return false;
+  } else {
+    const int rem = p.heavy_tiles % pairs, mine = p.heavy_tiles / pairs + (pair < rem ? 1 : 0);
+    int last;
+    if (j < mine) {
+      i = pair + j * pairs;
+      last = p.heavy_count;
+    } else {
+      const int f = j - mine, fewer = rem ? pairs - rem : 0, skip = rem ? p.early : 0;  // pairs with a heavy tile less
+      i = rem && pair >= rem && f < skip ? f * fewer + pair - rem
+                                         : skip * fewer + (rem && pair >= rem ? f - skip : f) * pairs + pair;
+      t.q = p.heavy_count;
+      last = p.count;
+    }
+    while (t.q < last && i >= p.q[t.q].tiles) i -= p.q[t.q++].tiles;
+    if (t.q >= last) return false;
+  }
+  const int mt = p.q[t.q].mt, nt = p.q[t.q].nt;
+  const int per = kGroupM * nt, g = i / per, r = i - g * per;
   const int gm = min(kGroupM, mt - g * kGroupM);
-  m = g * kGroupM + r % gm;
-  n = r / gm;
+  t.m = g * kGroupM + r % gm;
+  t.n = r / gm;
+  return true;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT, bool MULTI>
 __global__ void __launch_bounds__(threads_of(MX), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = kStages;
@@ -233,9 +277,8 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;  // rank in the pair, its first CTA
   const int slot = SPLIT > 1 ? (int)crank >> 1 : 0;                             // the pair's part of the reduction
   const int pair = blockIdx.x / (2 * SPLIT), pairs = gridDim.x / (2 * SPLIT);   // (SPLIT: a cluster has one tile)
-  const int mt = (p.M + 2 * kBM - 1) / (2 * kBM), nt = (p.N + TN - 1) / TN, tiles = mt * nt;
-  const int blocks = (p.K + kDepth - 1) / kDepth;
-  const int kb0 = slot * blocks / SPLIT, kb1 = (slot + 1) * blocks / SPLIT;
+  static_assert(!MULTI || (EPI == kEpiStore && B_MN && !MX && SPLIT == 1), "MULTI: dx and the weights' gradients");
+  Tile t;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) {
@@ -270,15 +313,16 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   if (warp == 0 || warp >= kBWarp) {
     if (lane == 0) {
       const int role = warp == 0 ? 0 : warp - kBWarp + 1;  // A, B, scales
-      tma_prefetch_desc(role == 0 ? &p.a : role == 1 ? &p.b : &p.as);
+      tma_prefetch_desc(role == 0 ? &p.q[0].a : role == 1 ? &p.q[0].b : &p.as);
       bool ok = true;
       int issued = 0;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        int m, n;
-        tile_of(t, mt, nt, m, n);
+      for (int i = 0; ok && tile_of<MULTI>(p, pair, pairs, i, t); ++i) {
+        const Product& q = p.q[MULTI ? t.q : 0];
+        const bool a_mn = MULTI ? q.a_mn != 0 : A_MN;
+        const int m = t.m, n = t.n, kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
         const int arow = (2 * m + (int)rank) * kBM;
         // B's half: gate rows in the first CTA, up rows in the second
-        const int brow = EPI == kEpiGateUp ? n * TN + (int)rank * p.N : n * TN + (int)rank * 128;
+        const int brow = EPI == kEpiGateUp ? n * TN + (int)rank * q.N : n * TN + (int)rank * 128;
         for (int kb = kb0; kb < kb1; ++kb) {
           const int st = issued % S;
           if (!mbar_wait(&bar->empty[st], ((issued / S) & 1) ^ 1, p.ctl) || aborted(bar)) {
@@ -292,18 +336,18 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           const int k = kb * kDepth;
           if (role == 0) {
             if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kTx);  // everything, both CTAs'
-            if (A_MN) {
-              tma_load_pair(a, &p.a, arow, k, fb);
-              tma_load_pair(a + kOpBytes / 2, &p.a, arow + 64, k, fb);
+            if (a_mn) {
+              tma_load_pair(a, &q.a, arow, k, fb);
+              tma_load_pair(a + kOpBytes / 2, &q.a, arow + 64, k, fb);
             } else {
-              tma_load_pair(a, &p.a, k, arow, fb);
+              tma_load_pair(a, &q.a, k, arow, fb);
             }
           } else if (role == 1) {
             if (B_MN) {
-              tma_load_pair(b, &p.b, brow, k, fb);
-              tma_load_pair(b + kOpBytes / 2, &p.b, brow + 64, k, fb);
+              tma_load_pair(b, &q.b, brow, k, fb);
+              tma_load_pair(b + kOpBytes / 2, &q.b, brow + 64, k, fb);
             } else {
-              tma_load_pair(b, &p.b, k, brow, fb);
+              tma_load_pair(b, &q.b, k, brow, fb);
             }
           } else if (MX) {
             uint8_t* sc = scales + st * kScaleBytes;
@@ -318,7 +362,6 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       const uint16_t both = (uint16_t)(3u << lead);  // the pair's CTAs in the cluster
       int it = 0, lt = 0;
       bool ok = true, ready = false;
@@ -326,7 +369,11 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         set_abort(bar);
         ok = false;
       }
-      for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
+      for (; ok && tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
+        const Product& q = p.q[MULTI ? t.q : 0];
+        const bool a_mn = MULTI ? q.a_mn != 0 : A_MN;
+        const uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (a_mn ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const int kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
         const int acc = lt & 1;
         // bf16: the accumulator was read two tiles ago; mx8: the tile before has left the shared columns (which its
         // epilogue warps reach only after the tile before that)
@@ -349,9 +396,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           ready = mbar_test(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
           tc_fence_after();
           const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
-          const uint64_t da = A_MN ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
+          const uint64_t da = a_mn ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
           // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
-          constexpr uint64_t sa = A_MN ? 128 : 2, sb = B_MN ? 128 : 2;
+          const uint64_t sa = a_mn ? 128 : 2, sb = B_MN ? 128 : 2;
           if (MX) {
             const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + (it & 1) * 16;
 #pragma unroll
@@ -376,42 +423,42 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   } else {
     const int ew = warp - 2, part = warp & 3, half = ew >> 2;
     const uint32_t lanes = (uint32_t)(part * 32) << 16;
-    // 16 columns of a row as bf16; N is a multiple of 8, and of 16 where p.wide says so
-    auto store16 = [&](uint16_t* to, int pitch, int row, int col, const float(&v)[16]) {
-      if (row >= p.M) return;
+    // 16 columns of a row as bf16; N is a multiple of 8, and of 16 where q.wide says so
+    auto store16 = [&](const Product& q, uint16_t* to, int pitch, int row, int col, const float(&v)[16]) {
+      if (row >= q.M) return;
       uint32_t w[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+      for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
       uint16_t* at = to + (size_t)row * pitch + col;
-      if (p.wide) {
-        if (col < p.N) store32(at, w);
+      if (q.wide) {
+        if (col < q.N) store32(at, w);
       } else {
-        if (col < p.N) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (col + 8 < p.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        if (col < q.N) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (col + 8 < q.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     };
     // One row's results: 16 columns of a product or of dh, or gate and up values of 16 neurons
-    auto finish = [&](int row, int col, float(&v)[16], const float(&u)[16]) {
+    auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16]) {
       if (EPI == kEpiStore) {
-        store16(p.y, p.N, row, col, v);
+        store16(q, q.y, q.N, row, col, v);
       } else if (EPI == kEpiGateUp) {
         if (p.pre_out) {  // (the up half lies N columns further)
-          store16(p.pre_out, 2 * p.N, row, col, v);
-          store16(p.pre_out + p.N, 2 * p.N, row, col, u);
+          store16(q, p.pre_out, 2 * q.N, row, col, v);
+          store16(q, p.pre_out + q.N, 2 * q.N, row, col, u);
         }
         with_act(p.act, [&](auto act) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = act_value<decltype(act)::value>(v[q]) * u[q];
+          for (int e = 0; e < 16; ++e) v[e] = act_value<decltype(act)::value>(v[e]) * u[e];
         });
-        store16(p.y, p.N, row, col, v);
+        store16(q, q.y, q.N, row, col, v);
       } else {
         float dg[16], du[16], h[16];
 #pragma unroll
-        for (int q = 0; q < 16; q += 8) {
-          const bool in = row < p.M && col + q < p.N;
-          const uint16_t* gp = p.pre + (size_t)row * 2 * p.N + col + q;
+        for (int c = 0; c < 16; c += 8) {
+          const bool in = row < q.M && col + c < q.N;
+          const uint16_t* gp = p.pre + (size_t)row * 2 * q.N + col + c;
           const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
-          const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + p.N) : make_uint4(0, 0, 0, 0);
+          const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + q.N) : make_uint4(0, 0, 0, 0);
           const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
           with_act(p.act, [&](auto act) {
 #pragma unroll
@@ -420,19 +467,19 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
               const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
               float a, da;
               act_and_grad<decltype(act)::value>(gv, a, da);
-              dg[q + e] = v[q + e] * uv * da;
-              du[q + e] = v[q + e] * a;
-              h[q + e] = a * uv;
+              dg[c + e] = v[c + e] * uv * da;
+              du[c + e] = v[c + e] * a;
+              h[c + e] = a * uv;
             }
           });
         }
-        store16(p.dpre, 2 * p.N, row, col, dg);
-        store16(p.dpre + p.N, 2 * p.N, row, col, du);
-        store16(p.y, p.N, row, col, h);
+        store16(q, p.dpre, 2 * q.N, row, col, dg);
+        store16(q, p.dpre + q.N, 2 * q.N, row, col, du);
+        store16(q, q.y, q.N, row, col, h);
       }
     };
     // mx8 gate/up: one row's 32 neurons, a group
-    auto finish_mx = [&](int row, int col, float(&h)[32], const float(&u)[32]) {
+    auto finish_mx = [&](const Product& q, int row, int col, float(&h)[32], const float(&u)[32]) {
       uint32_t top = 0;
       with_act(p.act, [&](auto act) {
 #pragma unroll
@@ -443,20 +490,19 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       });
       const uint32_t byte = mx_scale_byte(__uint_as_float(top));
       const float k = mx_inverse_scale(byte);
-      if (row >= p.M || col >= p.N) return;
+      if (row >= q.M || col >= q.N) return;
       uint32_t w[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) w[q] = e4m3x4(h[4 * q] * k, h[4 * q + 1] * k, h[4 * q + 2] * k, h[4 * q + 3] * k);
-      store32(p.hq + (size_t)row * p.N + col, w);
-      p.hs[mx_scale_word(row, col / 128, mx_tile_cols(p.N)) + col / 32 % 4] = (uint8_t)byte;
+      for (int e = 0; e < 8; ++e) w[e] = e4m3x4(h[4 * e] * k, h[4 * e + 1] * k, h[4 * e + 2] * k, h[4 * e + 3] * k);
+      store32(p.hq + (size_t)row * q.N + col, w);
+      p.hs[mx_scale_word(row, col / 128, mx_tile_cols(q.N)) + col / 32 % 4] = (uint8_t)byte;
     };
 
     if constexpr (SPLIT == 1) {
       int lt = 0;
-      for (int t = pair; t < tiles; t += pairs, ++lt) {
-        int m, n;
-        tile_of(t, mt, nt, m, n);
-        const int acc = lt & 1;
+      for (; tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
+        const Product& q = p.q[MULTI ? t.q : 0];
+        const int m = t.m, n = t.n, acc = lt & 1;
         const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
         if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
           set_abort(bar);
@@ -488,7 +534,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             tmem_ld16_async(src + 128 + c + 16, u + 16);
             tmem_ld_wait();
             if (i == 0) release();
-            finish_mx(row, n * TN + c, g, u);
+            finish_mx(q, row, n * TN + c, g, u);
           }
         } else {
           // 16 columns (neurons) at a time in a compact loop: straight-line code for the whole tile takes longer to
@@ -507,10 +553,10 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             tmem_ld_wait();
             float x[16], y[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) x[q] = v[q], y[q] = u[q];
+            for (int e = 0; e < 16; ++e) x[e] = v[e], y[e] = u[e];
             if (i == kShared - 1) release();
             if (i + 1 < kChunks) load(i + 1);
-            finish(row, n * TN + (half * kChunks + (back ? kChunks - 1 - i : i)) * 16, x, y);
+            finish(q, row, n * TN + (half * kChunks + (back ? kChunks - 1 - i : i)) * 16, x, y);
           }
         }
       }
@@ -569,9 +615,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       }
       if (!ok) {
         set_abort(bar);
-      } else if (pair < tiles) {
-        int m, n;
-        tile_of(pair, mt, nt, m, n);
+      } else if (tile_of<MULTI>(p, pair, pairs, 0, t)) {
+        const Product& q = p.q[0];
+        const int m = t.m, n = t.n;
         const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
         // 16 columns' sums over the pairs in the order of k; place c in the exchange, TMEM column col
         auto sum16 = [&](int c, int col, float* v) {
@@ -601,21 +647,21 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           sum16(16, a0 + 16, g + 16);
           sum16(32, b0, u);
           sum16(48, b0 + 16, u + 16);
-          finish_mx(row, n * TN + a0, g, u);
+          finish_mx(q, row, n * TN + a0, g, u);
         } else if (EPI == kEpiGateUp) {
 #pragma unroll 1
           for (int c = 0; c < W; c += 16) {
             float g[16], u[16];
             sum16(c, a0 + c, g);
             sum16(W + c, b0 + c, u);
-            finish(row, n * TN + a0 + c, g, u);
+            finish(q, row, n * TN + a0 + c, g, u);
           }
         } else {
 #pragma unroll 1
           for (int c = 0; c < 2 * W; c += 16) {
             float v[16];
             sum16(c, a0 + c, v);
-            finish(row, n * TN + a0 + c, v, v);
+            finish(q, row, n * TN + a0 + c, v, v);
           }
         }
       }
@@ -678,57 +724,74 @@ cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute (&at)[2]) {
   return cfg;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT, bool MULTI = false>
 cudaError_t launch(const GemmParams& p, int clusters, cudaStream_t st) {
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(clusters, at);
   cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT, MULTI>, p);
+}
+
+// A product's operands and sizes.  b_rows: rows of b (columns where it is MN-major).  Without y the sizes alone.
+template <int EPI, bool A_MN, bool B_MN, bool MX>
+bool set_product(const FfnEngine& e, Product& q, const void* a, const void* b, int M, int N, int K, uint64_t b_rows,
+                 void* y) {
+  constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
+  q.M = M;
+  q.N = N;
+  q.K = K;
+  q.a_mn = A_MN;
+  q.wide = N % 16 == 0;
+  q.y = static_cast<uint16_t*>(y);
+  q.mt = (M + 2 * kBM - 1) / (2 * kBM);
+  q.nt = (N + TN - 1) / TN;
+  if ((long long)q.mt * q.nt > (1 << 28)) return false;
+  q.tiles = q.mt * q.nt;
+  q.blocks = (K + (MX ? 127 : 63)) / (MX ? 128 : 64);
+  if (!y && EPI == kEpiStore) return true;
+  if (MX) return make_code_map(e.encode, &q.a, a, K, M, 128) && make_code_map(e.encode, &q.b, b, K, b_rows, 128);
+  // a K-major operand is [rows, K], an MN-major one [K, rows]
+  return (A_MN ? make_bf16_map(e.encode, &q.a, a, M, K, M, 64, kBK) : make_bf16_map(e.encode, &q.a, a, K, M, K, kBK, kBM)) &&
+         (B_MN ? make_bf16_map(e.encode, &q.b, b, b_rows, K, b_rows, 64, kBK)
+               : make_bf16_map(e.encode, &q.b, b, K, b_rows, K, kBK, 128));
+}
+
+// Pairs that a tile's reduction is split over, and the time of the product, in
+// k blocks: the least of rounds of tiles x time of a tile.  Measured (us for
+// the two products of a forward call, all with 1, 2 or 4, against this choice
+// for each): T = 128, d = 2048, I = 8192: 58.1, 50.4, 68.6 -> 34.8; T = 1024, d
+// = 2048, I = 2048: 29.9, 36.2, 79.5 -> 27.1; T = 2048, d = 2048, I = 8192:
+// 120.4, 223.5, 427.3 -> 120.7.
+template <int EPI, bool MX>
+int split_of(const FfnEngine& e, const Product& q, double* cost) {
+  constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
+  int split = 1;
+  *cost = 1e30;
+  for (int s = 1; s <= kMost && s <= q.blocks; s *= 2) {
+    const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : e.pairs4;  // clusters that run at a time
+    if (fit < 1) break;
+    const double rounds = (double)((q.tiles + fit - 1) / fit);
+    const double c =
+        rounds * ((q.blocks + s - 1) / s + kTileCost + (double)epilogue_cost(EPI) / s + (s > 1 ? kSplitCost : 0));
+    if (c < *cost) *cost = c, split = s;
+  }
+  return split;
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool MX>
-cudaError_t run(const FfnEngine& e, GemmParams& p, const void* a, const void* b, uint64_t b_rows, void* out,
-                cudaStream_t st) {
-  bool ok;
-  if (MX) {
-    ok = make_code_map(e.encode, &p.a, a, p.K, p.M, 128) && make_code_map(e.encode, &p.b, b, p.K, b_rows, 128);
-  } else {  // a K-major operand is [rows, K], an MN-major one [K, rows]
-    ok = A_MN ? make_bf16_map(e.encode, &p.a, a, p.M, p.K, p.M, 64, kBK)
-              : make_bf16_map(e.encode, &p.a, a, p.K, p.M, p.K, kBK, kBM);
-    ok = ok && (B_MN ? make_bf16_map(e.encode, &p.b, b, b_rows, p.K, b_rows, 64, kBK)
-                     : make_bf16_map(e.encode, &p.b, b, p.K, b_rows, p.K, kBK, 128));
-  }
+cudaError_t run(const FfnEngine& e, GemmParams& p, cudaStream_t st) {
   p.ctl = e.ctl;
-  constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;
-  const long long tiles = (long long)((p.M + 2 * kBM - 1) / (2 * kBM)) * ((p.N + TN - 1) / TN);
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int blocks = (p.K + (MX ? 127 : 63)) / (MX ? 128 : 64);
-  // Pairs that a tile's reduction is split over: the least of rounds of tiles x time of a tile.  Measured (us for the
-  // two products of a forward call, all with 1, 2 or 4, against this choice for each): T = 128, d = 2048, I = 8192:
-  // 58.1, 50.4, 68.6 -> 34.8; T = 1024, d = 2048, I = 2048: 29.9, 36.2, 79.5 -> 27.1; T = 2048, d = 2048, I = 8192:
-  // 120.4, 223.5, 427.3 -> 120.7.
-  constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
-  int split = 1;
-  double best = 1e30;
-  for (int s = 1; s <= kMost && s <= blocks; s *= 2) {
-    const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : e.pairs4;  // clusters that run at a time
-    if (fit < 1) break;
-    const double rounds = (double)((tiles + fit - 1) / fit);
-    const double cost = rounds * ((blocks + s - 1) / s + kTileCost + (double)epilogue_cost(EPI) / s + (s > 1 ? kSplitCost : 0));
-    if (cost < best) best = cost, split = s;
-  }
-  if (!ok) return cudaErrorInvalidValue;
-  p.y = static_cast<uint16_t*>(out);
-  p.wide = p.N % 16 == 0;
-  if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? (int)tiles : e.pairs, st);
-  if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, (int)tiles, st);
-  if constexpr (kMost == 4) return launch<EPI, A_MN, B_MN, MX, 4>(p, (int)tiles, st);
+  double cost;
+  const int split = split_of<EPI, MX>(e, p.q[0], &cost), tiles = p.q[0].tiles;
+  if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? tiles : e.pairs, st);
+  if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, tiles, st);
+  if constexpr (!(MX && EPI == kEpiGateUp)) return launch<EPI, A_MN, B_MN, MX, 4>(p, tiles, st);
   return cudaErrorInvalidValue;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
+template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT, bool MULTI = false>
 cudaError_t prepare(int* clusters) {
-  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT>;
+  auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT, MULTI>;
   cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(MX));
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute at[2];
@@ -770,6 +833,7 @@ cudaError_t prepare_ffn_gemm(FfnEngine* e) {
   if (err == cudaSuccess) err = prepare_splits<kEpiGrad, false, true, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, true, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, true, true, false>(e);
+  if (err == cudaSuccess) err = prepare<kEpiStore, true, true, false, 1, true>(&e->pairs);
   if (err == cudaSuccess) err = prepare_splits<kEpiGateUp, false, false, true>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, false, true>(e);
   return err == cudaSuccess && e->pairs < 1 ? cudaErrorInvalidConfiguration : err;
@@ -786,81 +850,116 @@ cudaError_t launch_mx_up_scales(const FfnShape& s, const uint8_t* gate_up_s, uin
 cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const FfnForwardArgs& a, const uint8_t* up_s,
                                   uint8_t* hq, uint8_t* hs, cudaStream_t st) {
   GemmParams p{};
-  p.M = s.T;
-  p.N = s.I;
-  p.K = s.d;
   p.act = s.act;
   p.hq = hq;
   p.hs = hs;
   const uint64_t tiles = (s.I + 127) / 128;
-  if (!make_scale_map(e.encode, &p.as, a.xs, s.d, (s.T + 127) / 128) ||
+  if (!set_product<kEpiGateUp, false, false, true>(e, p.q[0], a.x, a.gate_up, s.T, s.I, s.d, 2 * (uint64_t)s.I, nullptr) ||
+      !make_scale_map(e.encode, &p.as, a.xs, s.d, (s.T + 127) / 128) ||
       !make_scale_map(e.encode, &p.bs0, a.gate_up_s, s.d, tiles) || !make_scale_map(e.encode, &p.bs1, up_s, s.d, tiles))
     return cudaErrorInvalidValue;
-  return run<kEpiGateUp, false, false, true>(e, p, a.x, a.gate_up, 2 * (uint64_t)s.I, nullptr, st);
+  return run<kEpiGateUp, false, false, true>(e, p, st);
 }
 
 cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint8_t* hq, const uint8_t* hs,
                                const FfnForwardArgs& a, cudaStream_t st) {
   GemmParams p{};
-  p.M = s.T;
-  p.N = s.d;
-  p.K = s.I;
-  const uint64_t tiles = (s.d + 127) / 128;
-  if (!make_scale_map(e.encode, &p.as, hs, s.I, (s.T + 127) / 128) ||
-      !make_scale_map(e.encode, &p.bs0, a.down_s, s.I, tiles))
+  if (!set_product<kEpiStore, false, false, true>(e, p.q[0], hq, a.down, s.T, s.d, s.I, s.d, a.y) ||
+      !make_scale_map(e.encode, &p.as, hs, s.I, (s.T + 127) / 128) ||
+      !make_scale_map(e.encode, &p.bs0, a.down_s, s.I, (s.d + 127) / 128))
     return cudaErrorInvalidValue;
   p.bs1 = p.bs0;
-  return run<kEpiStore, false, false, true>(e, p, hq, a.down, s.d, a.y, st);
+  return run<kEpiStore, false, false, true>(e, p, st);
 }
 
 cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void* x, const void* gate_up, uint16_t* h,
                                uint16_t* pre, cudaStream_t st) {
   GemmParams p{};
-  p.M = s.T;
-  p.N = s.I;
-  p.K = s.d;
   p.act = s.act;
   p.pre_out = pre;
-  return run<kEpiGateUp, false, false, false>(e, p, x, gate_up, 2 * (uint64_t)s.I, h, st);
+  if (!set_product<kEpiGateUp, false, false, false>(e, p.q[0], x, gate_up, s.T, s.I, s.d, 2 * (uint64_t)s.I, h))
+    return cudaErrorInvalidValue;
+  return run<kEpiGateUp, false, false, false>(e, p, st);
 }
 
 cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
                             cudaStream_t st) {
   GemmParams p{};
-  p.M = s.T;
-  p.N = s.d;
-  p.K = s.I;
-  return run<kEpiStore, false, false, false>(e, p, h, down, s.d, y, st);
+  if (!set_product<kEpiStore, false, false, false>(e, p.q[0], h, down, s.T, s.d, s.I, s.d, y))
+    return cudaErrorInvalidValue;
+  return run<kEpiStore, false, false, false>(e, p, st);
 }
 
-cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint16_t* dy, const uint16_t* down,
-                              const uint16_t* pre, uint16_t* dpre, uint16_t* h, cudaStream_t st) {
+cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
+                              cudaStream_t st) {
   GemmParams p{};
-  p.M = s.T;
-  p.N = s.I;
-  p.K = s.d;
   p.act = s.act;
-  p.pre = pre;
-  p.dpre = dpre;
-  return run<kEpiGrad, false, true, false>(e, p, dy, down, s.I, h, st);
+  p.pre = a.pre;
+  p.dpre = sc.dpre;
+  if (!set_product<kEpiGrad, false, true, false>(e, p.q[0], a.dy, a.down, s.T, s.I, s.d, s.I, sc.h))
+    return cudaErrorInvalidValue;
+  return run<kEpiGrad, false, true, false>(e, p, st);
 }
 
-cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t* dpre, const uint16_t* gate_up,
-                          uint16_t* dx, cudaStream_t st) {
-  GemmParams p{};
-  p.M = s.T;
-  p.N = s.d;
-  p.K = 2 * s.I;
-  return run<kEpiStore, false, true, false>(e, p, dpre, gate_up, s.d, dx, st);
-}
+// dx = dpre gate_up (K = 2I), dgate_up = dpre^T x and ddown = dy^T h (K = T).
+// They do not depend on one another: they go into one launch unless splitting
+// each one's few tiles over clusters is the shorter.  That is decided for all
+// three, so that a gradient does not depend on which others are wanted.
+cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
+                             int* launches, cudaStream_t st) {
+  Product all[3] = {};  // dx, dgate_up, ddown
+  if (!set_product<kEpiStore, false, true, false>(e, all[0], sc.dpre, a.gate_up, s.T, s.d, 2 * s.I, s.d, a.dx) ||
+      !set_product<kEpiStore, true, true, false>(e, all[1], sc.dpre, a.x, 2 * s.I, s.d, s.T, s.d, a.dgate_up) ||
+      !set_product<kEpiStore, true, true, false>(e, all[2], a.dy, sc.h, s.d, s.I, s.T, s.I, a.ddown))
+    return cudaErrorInvalidValue;
+  const bool dx_first = all[0].blocks >= all[1].blocks;  // the longer reduction
 
-cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
-                                   uint16_t* dw, cudaStream_t st) {
+  // time of one launch, in k blocks: at best even, at worst one light tile more, and no less than the heavy tiles'
+  const int each = kTileCost + epilogue_cost(kEpiStore);
+  const long long weight_tiles = (long long)all[1].tiles + all[2].tiles;
+  const long long heavy = dx_first ? all[0].tiles : weight_tiles, light = dx_first ? weight_tiles : all[0].tiles;
+  const int ch = (dx_first ? all[0] : all[1]).blocks + each, cl = (dx_first ? all[1] : all[0]).blocks + each;
+  double together = (double)(heavy * ch + light * cl) / e.pairs + cl;
+  const double least = (double)((heavy + e.pairs - 1) / e.pairs) * ch;
+  if (together < least) together = least;
+  double apart = 2 * kLaunchCost, c;
+  for (const Product& q : all) {
+    split_of<kEpiStore, false>(e, q, &c);
+    apart += c;
+  }
+
   GemmParams p{};
-  p.M = M;
-  p.N = N;
-  p.K = T;
-  return run<kEpiStore, true, true, false>(e, p, a, b, N, dw, st);
+  p.ctl = e.ctl;
+  p.early = ch / cl;
+  auto add = [&](const Product& q) {
+    if (q.y) p.q[p.count++] = q;
+  };
+  if (dx_first) add(all[0]);
+  if (!dx_first) add(all[1]), add(all[2]);
+  p.heavy_count = p.count;
+  if (dx_first) add(all[1]), add(all[2]);
+  if (!dx_first) add(all[0]);
+  long long tiles = 0;
+  for (int i = 0; i < p.count; ++i) {
+    tiles += p.q[i].tiles;
+    if (i < p.heavy_count) p.heavy_tiles = (int)tiles;
+  }
+  if (tiles > (1 << 28)) return cudaErrorInvalidValue;
+  const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
+  *launches = 1;
+  if (together <= apart) {
+    if (p.count > 1) return launch<kEpiStore, true, true, false, 1, true>(p, pairs, st);
+    return p.q[0].a_mn ? launch<kEpiStore, true, true, false, 1>(p, pairs, st)
+                       : launch<kEpiStore, false, true, false, 1>(p, pairs, st);
+  }
+  *launches = p.count;
+  cudaError_t err = cudaSuccess;
+  for (int i = 0; i < p.count && err == cudaSuccess; ++i) {
+    GemmParams one{};
+    one.q[0] = p.q[i];
+    err = one.q[0].a_mn ? run<kEpiStore, true, true, false>(e, one, st) : run<kEpiStore, false, true, false>(e, one, st);
+  }
+  return err;
 }
 
 }  // namespace moe

@@ -178,6 +178,10 @@ struct FfnForwardArgs {
   void* y;
   void* pre;
 };
+struct FfnBackwardArgs {
+  const uint16_t *x, *pre, *gate_up, *down, *dy;
+  uint16_t *dx, *dgate_up, *ddown;
+};
 struct FfnScratch {
   uint16_t* h;       // [max_tokens, I] bf16 act(gate) * up
   uint8_t* hq;       // the same as mx8 codes
@@ -239,13 +243,11 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
                                uint16_t* pre, cudaStream_t st);
 cudaError_t launch_ffn_down(const FfnEngine& e, const FfnShape& s, const uint16_t* h, const void* down, void* y,
                             cudaStream_t st);
-cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const uint16_t* dy, const uint16_t* down,
-                              const uint16_t* pre, uint16_t* dpre, uint16_t* h, cudaStream_t st);
-cudaError_t launch_ffn_dx(const FfnEngine& e, const FfnShape& s, const uint16_t* dpre, const uint16_t* gate_up,
-                          uint16_t* dx, cudaStream_t st);
-// dw [M, N] = a^T b, a [T, M], b [T, N]
-cudaError_t launch_ffn_weight_grad(const FfnEngine& e, const uint16_t* a, int M, const uint16_t* b, int N, int T,
-                                   uint16_t* dw, cudaStream_t st);
+cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
+                              cudaStream_t st);
+// dx, dgate_up and ddown, as far as wanted, from what launch_ffn_grad_h left; *launches: kernels launched
+cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
+                             int* launches, cudaStream_t st);
 
 // mx8.  up_s: the scales of gate_up's rows I .. 2I - 1 as a matrix of their own:
 // where I is a multiple of 128 they are one inside gate_up_s, else

@@ -383,7 +383,8 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
  *   dpre = [dh * u * act'(g) | dh * act(g)],  dx = dpre gate_up,
  *   dgate_up = dpre^T x,  ddown = dy^T (act(g) * u).
  * x, pre and the weights are those of the forward call, dy [T, d].  Any of dx
- * [T, d], dgate_up [2I, d], ddown [d, I] may be NULL to skip it.  Sums are fp32;
+ * [T, d], dgate_up [2I, d], ddown [d, I] may be NULL to skip it, which does not
+ * change the others.  Sums are fp32;
  * dpre and act(g) * u are held in bf16 between the products.  T == 0 sets
  * dgate_up and ddown to 0.  MOE_ERR_UNSUPPORTED without cfg.training. */
 int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const void* gate_up, const void* down,
