@@ -14,8 +14,9 @@
 // SM 32 KB of shared-memory fill for 256 cycles of MMA (a lone CTA's 128 x 256
 // tile takes 48 KB for the same work).  Per CTA 11 warps (12 for mx8):
 //   warps 0, 10, 11  TMA producers (one thread each) of a ring of k blocks,
-//              128-byte swizzle: A, B, and mx8's scales.  One thread alone takes
-//              longer for all of a k block's copies than its MMAs do;
+//              128-byte swizzle: A, B, and mx8's scales.  A thread takes some 100
+//              cycles to issue a copy and up to 300 to see that a stage is free,
+//              against a k block's 512 cycles of MMAs;
 //   warp 1     allocates all 512 TMEM columns: two fp32 accumulators of 256
 //              columns; in the pair's first CTA one thread issues the MMAs;
 //   warps 2-9  epilogue: two warps for each quarter of the TMEM lanes, each
@@ -58,8 +59,9 @@ constexpr int kBK = 64;                     // k block of bf16
 constexpr int kOpBytes = 128 * kRowBytes;   // one operand's half tile: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
 constexpr int kEpiWarps = 8;
-constexpr int kBWarp = 2 + kEpiWarps, kScaleWarp = kBWarp + 1;  // producers of B and of the scales (A: warp 0)
-constexpr int threads_of(bool mx) { return (mx ? kScaleWarp + 1 : kBWarp + 1) * 32; }
+constexpr int kBWarp = 2 + kEpiWarps;       // producers (one thread each): A on warp 0, B on this, mx8's scales on the next
+constexpr int roles_of(bool mx) { return mx ? 3 : 2; }  // A, B; mx8: and the scales
+constexpr int threads_of(bool mx) { return (kBWarp + roles_of(mx) - 1) * 32; }
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
@@ -107,7 +109,7 @@ struct __align__(8) Bars {
   uint64_t recv[kEpiWarps];  // SPLIT: the other pairs' sums of an epilogue warp's columns have come
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t issued[2][3];  // k blocks loaded by each CTA's producers of A, B and scales (first CTA: both's)
+  uint32_t issued[2][3];  // k blocks loaded by each CTA's producers (first CTA: both's)
   uint32_t any_abort;     // some CTA of the cluster has given up
 };
 
@@ -265,7 +267,6 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int S = kStages;
   constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
-  constexpr int kDepth = MX ? kRowBytes : kBK;     // values of k per block
   static_assert(!MX || (!A_MN && !B_MN && EPI != kEpiGrad), "mx8: forward products only");
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;  // result columns per tile
   extern __shared__ uint8_t smem_raw[];
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
 
   if (warp == 0 || warp >= kBWarp) {
     if (lane == 0) {
-      const int role = warp == 0 ? 0 : warp - kBWarp + 1;  // A, B, scales
+      const int role = warp == 0 ? 0 : warp - kBWarp + 1;
       tma_prefetch_desc(role == 0 ? &p.q[0].a : role == 1 ? &p.q[0].b : &p.as);
       bool ok = true;
       int issued = 0;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           const uint32_t fb = map_cta(&bar->full[st], lead);
           uint8_t* a = base + st * kStageBytes;
           uint8_t* b = a + kOpBytes;
-          const int k = kb * kDepth;
+          const int k = kb * (MX ? kRowBytes : kBK);
           if (role == 0) {
             if (rank == 0) mbar_expect_tx(&bar->full[st], 2 * kTx);  // everything, both CTAs'
             if (a_mn) {
@@ -361,65 +362,104 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       bar->issued[rank][role] = issued;
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
-      const uint16_t both = (uint16_t)(3u << lead);  // the pair's CTAs in the cluster
-      int it = 0, lt = 0;
-      bool ok = true, ready = false;
-      if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
-        set_abort(bar);
-        ok = false;
-      }
-      for (; ok && tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
-        const Product& q = p.q[MULTI ? t.q : 0];
-        const bool a_mn = MULTI ? q.a_mn != 0 : A_MN;
-        const uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (a_mn ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-        const int kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
-        const int acc = lt & 1;
-        // bf16: the accumulator was read two tiles ago; mx8: the tile before has left the shared columns (which its
-        // epilogue warps reach only after the tile before that)
-        const bool free = MX ? lt == 0 || mbar_wait(&bar->tempty[0], (lt - 1) & 1, p.ctl)
-                             : mbar_wait(&bar->tempty[acc], ((lt >> 1) & 1) ^ 1, p.ctl);
-        if (!free || aborted(bar)) {
-          set_abort(bar);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * (MX ? kBN - kSharedCols : kBN);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % S;
-          if (!ready && (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar))) {
-            set_abort(bar);
+    // Seeing that a block has landed takes a load from shared memory, which queues behind the operand reads of the MMAs
+    // issued before it (some 300 cycles of a block's 512).
+    const uint16_t both = (uint16_t)(3u << lead);  // the pair's CTAs in the cluster
+    int it = 0, lt = 0;
+    bool ok = true;
+    if (p.ctl.stall && rank == 0) {  // test hook: nothing arrives there before the end
+      if (lane == 0) ok = mbar_wait(&bar->mma_done, 0, p.ctl);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+    if constexpr (!MX) {
+      if (rank == 0 && lane == 0) {
+        bool ready = false;
+        for (; ok && tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
+          const Product& q = p.q[MULTI ? t.q : 0];
+          const bool a_mn = MULTI ? q.a_mn != 0 : A_MN;
+          const uint32_t idesc = umma_idesc_bf16(2 * kBM, kBN) | (a_mn ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+          const int kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
+          const int acc = lt & 1;
+          // the accumulator was read two tiles ago
+          if (!mbar_wait(&bar->tempty[acc], ((lt >> 1) & 1) ^ 1, p.ctl) || aborted(bar)) {
             ok = false;
             break;
           }
-          // asked for before this block's MMAs: a load from shared memory queues behind their operand reads
-          ready = mbar_test(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
           tc_fence_after();
-          const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
-          const uint64_t da = a_mn ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
-          // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
-          const uint64_t sa = a_mn ? 128 : 2, sb = B_MN ? 128 : 2;
-          if (MX) {
-            const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + (it & 1) * 16;
-#pragma unroll
-            for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_pair_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(2 * kBM, kBN, j), ts, ts + 4, kb != kb0 || j != 0);
-          } else {
+          const uint32_t d = tmem + acc * kBN;
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const int st = it % S;
+            if (!ready && (!mbar_wait(&bar->full[st], (it / S) & 1, p.ctl) || aborted(bar))) {
+              ok = false;
+              break;
+            }
+            // asked for before this block's MMAs
+            ready = mbar_test(&bar->full[(it + 1) % S], ((it + 1) / S) & 1);
+            tc_fence_after();
+            const uint32_t a = smem_u32(base + st * kStageBytes), b = a + kOpBytes;
+            const uint64_t da = a_mn ? desc_mn(a) : umma_desc_sw128(a), db = B_MN ? desc_mn(b) : umma_desc_sw128(b);
+            // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+            const uint64_t sa = a_mn ? 128 : 2, sb = B_MN ? 128 : 2;
 #pragma unroll
             for (int j = 0; j < kBK / 16; ++j) mma_pair(d, da + j * sa, db + j * sb, idesc, kb != kb0 || j != 0);
+            commit_pair(&bar->empty[st], both);
           }
-          commit_pair(&bar->empty[st], both);
+          if (ok) commit_pair(&bar->tfull[acc], both);
         }
-        if (ok) commit_pair(&bar->tfull[acc], both);
       }
+    } else if (rank == 0) {
+      // The scales' copies need more of a lead: the warp's lanes look at all stages at once, and lane 0 issues every
+      // block in a row that has landed (T = 4096, d = 4096, I = 8192, a forward call: 309 -> 295 us).
+      for (; ok && tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
+        const Product& q = p.q[0];
+        const int kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
+        const int acc = lt & 1;
+        // the tile before has left the shared columns (which its epilogue warps reach only after the tile before that)
+        if (lane == 0) ok = (lt == 0 || mbar_wait(&bar->tempty[0], (lt - 1) & 1, p.ctl)) && !aborted(bar);
+        const uint32_t d = tmem + acc * (kBN - kSharedCols);
+        for (int kb = kb0; kb < kb1;) {
+          const bool here = lane < S && mbar_test(&bar->full[(it + lane) % S], ((it + lane) / S) & 1);
+          int n = __ffs(~__ballot_sync(0xffffffffu, here)) - 1;
+          if (n == 0) {
+            if (lane == 0) ok = ok && mbar_wait(&bar->full[it % S], (it / S) & 1, p.ctl) && !aborted(bar);
+            n = 1;
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          n = min(n, kb1 - kb);
+          if (lane == 0) {
+            tc_fence_after();
+            for (int i = it; i < it + n; ++i) {
+              const int st = i % S;
+              const uint32_t a = smem_u32(base + st * kStageBytes);
+              const uint64_t da = umma_desc_sw128(a), db = umma_desc_sw128(a + kOpBytes);
+              // tcgen05 runs a thread's copies and MMAs in the order of issue; two sets of columns for the scales
+              const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + (i & 1) * 16;
+#pragma unroll
+              for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_pair_mx(d, da + j * 2, db + j * 2, umma_idesc_mx(2 * kBM, kBN, j), ts, ts + 4,
+                            kb + i != kb0 + it || j != 0);
+              commit_pair(&bar->empty[st], both);
+            }
+          }
+          __syncwarp();
+          kb += n;
+          it += n;
+        }
+        if (ok && lane == 0) commit_pair(&bar->tfull[acc], both);
+      }
+    }
+    if (rank == 0 && lane == 0) {
+      if (!ok) set_abort(bar);
       // the MMAs issued so far are done before TMEM is freed and shared memory left
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                        smem_u32(&bar->mma_done))
                    : "memory");
       mbar_wait(&bar->mma_done, 0, p.ctl);
     }
+    __syncwarp();
   } else {
     const int ew = warp - 2, part = warp & 3, half = ew >> 2;
     const uint32_t lanes = (uint32_t)(part * 32) << 16;
@@ -437,8 +477,20 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         if (col + 8 < q.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     };
+    // grad: pre's values that belong to 16 columns of dh, asked for ahead of them
+    auto load_pre = [&](const Product& q, int row, int col, uint4(&in)[4]) {
+      if (EPI != kEpiGrad) return;
+      const uint16_t* gp = p.pre + (size_t)row * 2 * q.N + col;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bool ok = row < q.M && col + c * 8 < q.N;
+        in[c] = ok ? *reinterpret_cast<const uint4*>(gp + c * 8) : make_uint4(0, 0, 0, 0);
+        in[2 + c] = ok ? *reinterpret_cast<const uint4*>(gp + q.N + c * 8) : make_uint4(0, 0, 0, 0);
+      }
+    };
     // One row's results: 16 columns of a product or of dh, or gate and up values of 16 neurons
-    auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16]) {
+    // (grad: pre's 16 gate and up values of the row in `in`)
+    auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16], const uint4(&in)[4]) {
       if (EPI == kEpiStore) {
         store16(q, q.y, q.N, row, col, v);
       } else if (EPI == kEpiGateUp) {
@@ -453,26 +505,20 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         store16(q, q.y, q.N, row, col, v);
       } else {
         float dg[16], du[16], h[16];
+        const uint32_t gw[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+        const uint32_t uw[8] = {in[2].x, in[2].y, in[2].z, in[2].w, in[3].x, in[3].y, in[3].z, in[3].w};
+        with_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int c = 0; c < 16; c += 8) {
-          const bool in = row < q.M && col + c < q.N;
-          const uint16_t* gp = p.pre + (size_t)row * 2 * q.N + col + c;
-          const uint4 g4 = in ? *reinterpret_cast<const uint4*>(gp) : make_uint4(0, 0, 0, 0);
-          const uint4 u4 = in ? *reinterpret_cast<const uint4*>(gp + q.N) : make_uint4(0, 0, 0, 0);
-          const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
-          with_act(p.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
-              const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
-              float a, da;
-              act_and_grad<decltype(act)::value>(gv, a, da);
-              dg[c + e] = v[c + e] * uv * da;
-              du[c + e] = v[c + e] * a;
-              h[c + e] = a * uv;
-            }
-          });
-        }
+          for (int e = 0; e < 16; ++e) {
+            const float gv = e & 1 ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
+            const float uv = e & 1 ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
+            float a, da;
+            act_and_grad<decltype(act)::value>(gv, a, da);
+            dg[e] = v[e] * uv * da;
+            du[e] = v[e] * a;
+            h[e] = a * uv;
+          }
+        });
         store16(q, p.dpre, 2 * q.N, row, col, dg);
         store16(q, p.dpre + q.N, 2 * q.N, row, col, du);
         store16(q, q.y, q.N, row, col, h);
@@ -504,6 +550,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         const Product& q = p.q[MULTI ? t.q : 0];
         const int m = t.m, n = t.n, acc = lt & 1;
         const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
+        constexpr int kChunks = EPI == kEpiGateUp ? 4 : 8;  // of 16 columns (neurons), see below
+        uint4 in[4];
+        load_pre(q, row, n * TN + half * kChunks * 16, in);  // in flight while the product is waited for
         if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
           set_abort(bar);
           break;
@@ -539,7 +588,6 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         } else {
           // 16 columns (neurons) at a time in a compact loop: straight-line code for the whole tile takes longer to
           // fetch than to run where a CTA has one tile or two
-          constexpr int kChunks = EPI == kEpiGateUp ? 4 : 8;
           constexpr int kShared = MX ? kSharedCols / 16 : kChunks;  // chunks after which the accumulator is released
           float v[16], u[16];
           auto load = [&](int i) {
@@ -554,9 +602,13 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             float x[16], y[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = v[e], y[e] = u[e];
+            const uint4 now[4] = {in[0], in[1], in[2], in[3]};
             if (i == kShared - 1) release();
-            if (i + 1 < kChunks) load(i + 1);
-            finish(q, row, n * TN + (half * kChunks + (back ? kChunks - 1 - i : i)) * 16, x, y);
+            if (i + 1 < kChunks) {
+              load(i + 1);
+              load_pre(q, row, n * TN + (half * kChunks + i + 1) * 16, in);
+            }
+            finish(q, row, n * TN + (half * kChunks + (back ? kChunks - 1 - i : i)) * 16, x, y, now);
           }
         }
       }
@@ -649,19 +701,22 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           sum16(48, b0 + 16, u + 16);
           finish_mx(q, row, n * TN + a0, g, u);
         } else if (EPI == kEpiGateUp) {
+          const uint4 none[4] = {};
 #pragma unroll 1
           for (int c = 0; c < W; c += 16) {
             float g[16], u[16];
             sum16(c, a0 + c, g);
             sum16(W + c, b0 + c, u);
-            finish(q, row, n * TN + a0 + c, g, u);
+            finish(q, row, n * TN + a0 + c, g, u, none);
           }
         } else {
 #pragma unroll 1
           for (int c = 0; c < 2 * W; c += 16) {
             float v[16];
+            uint4 in[4];
+            load_pre(q, row, n * TN + a0 + c, in);
             sum16(c, a0 + c, v);
-            finish(q, row, n * TN + a0 + c, v, v);
+            finish(q, row, n * TN + a0 + c, v, v, in);
           }
         }
       }
@@ -675,7 +730,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   // told, copies may be in flight: a pair's second CTA reports what its
   // producers have issued, and the first waits for both CTAs' copies block by
   // block, crediting a barrier with what never was.
-  constexpr int kRoles = MX ? 3 : 2;
+  constexpr int kRoles = roles_of(MX);
   if (threadIdx.x == 0 && bar->abort_flag)
     for (uint32_t r = 0; r < 2 * SPLIT; ++r) store_cluster(map_cta(&bar->any_abort, r), 1u);
   cluster_sync();
