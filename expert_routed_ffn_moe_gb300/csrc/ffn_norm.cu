@@ -29,6 +29,28 @@ struct F8 {
   float v[8];
 };
 
+// The norm's kernels are launched while the kernel before may still run
+// (programmatic stream serialization): their blocks come up during its end, and
+// read and write nothing before it has finished.
+MOE_DEV void follow() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // A chunk as it lies in memory.
 template <typename T>
 struct Raw;
@@ -135,6 +157,7 @@ template <typename XT, typename ST, int R, int C, bool ODD>
 __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
   __shared__ float red[2][1][32];
   extern __shared__ float wsm[];  // ODD: the weight, [8][(d + 7) / 8]
+  follow();
   constexpr int kRows = R == 32 ? 4 : 1;
   const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x;
   const size_t tile_cols = mx_tile_cols(a.d);
@@ -258,6 +281,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
 template <typename ST, int R, int C, bool ODD>
 __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2][2][32];
+  follow();
   constexpr int kRows = R == 32 ? 4 : 1;
   const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int first = blockIdx.x * kRows + (R == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows;
@@ -358,6 +382,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
 __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* partial, int rows, int d, void* dw,
                                                              int w_dtype) {
   __shared__ float part[32][33];
+  follow();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < d) {
@@ -435,8 +460,7 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
     }
     if (grid > most) grid = most;
   }
-  kernel<<<grid, kBlock, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(kernel, grid, dim3(kBlock), smem, st, a);
 }
 // Threads per row: one or two chunks of 8 columns each.
 template <typename XT, typename ST, bool ODD>
@@ -467,12 +491,11 @@ cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
     const int most = resident < kNormPartials / kRows ? resident : kNormPartials / kRows;
     if (grid > most) grid = most;
   }
-  kernel<<<grid, kBlock, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), 0, st, a);
   if (e != cudaSuccess || !a.dw) return e;
   const int partials = a.T < grid * kRows ? a.T : grid * kRows;
-  norm_grad_sum_kernel<<<(a.d + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, partials, a.d, a.dw, a.w_dtype);
-  return cudaGetLastError();
+  return launch_after(norm_grad_sum_kernel, (a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial, partials, a.d,
+                      a.dw, a.w_dtype);
 }
 template <typename ST, bool ODD>
 cudaError_t grad_width(const NormGradArgs& a, cudaStream_t st) {
