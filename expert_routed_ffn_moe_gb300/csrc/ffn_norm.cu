@@ -133,6 +133,15 @@ MOE_DEV void row_sums(float (&v)[N], float (*red)[N][32]) {
   for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < R / 32 ? (*red)[i][lane] : 0.f);
 }
 
+// Rows of odd width: where value i of window c of a row that begins r = (its
+// first value) mod 8 into the first window has its column in an array [8][pitch]
+// by (column mod 8, column / 8): at off(i) + c, off() the same in all threads.
+struct OddRow {
+  int r, pitch, d;
+  MOE_DEV int off(int i) const { return i >= r ? (i - r) * pitch : (i - r + 8) * pitch - 1; }
+  MOE_DEV bool in(int c, int i) const { return (unsigned)(8 * c + i - r) < (unsigned)d; }
+};
+
 // The scale and the codes of this thread's 8 columns of a group of 32 (4
 // neighbouring lanes hold the group; every lane of the warp takes part).
 MOE_DEV uint2 quantize8(const F8& f, uint32_t& byte) {
@@ -214,18 +223,17 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
     }
     const size_t lo = (size_t)row * a.d, hi = lo + a.d, c0 = lo / 8;
     const int chunks = (int)((hi + 7) / 8 - c0);
+    const OddRow odd{(int)(lo & 7), wpitch, a.d};
     F8 s[C];
     float sum[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       s[j] = x[j].get();
       const F8 r = res[j].get();
-      const size_t e = (c0 + tid + j * R) * 8;
-      const bool edge = ODD && (e < lo || e + 8 > hi);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s[j].v[i] += r.v[i];
-        if (edge && (e + i < lo || e + i >= hi)) s[j].v[i] = 0.f;
+        if (ODD && !odd.in(tid + j * R, i)) s[j].v[i] = 0.f;
         sum[0] += s[j].v[i] * s[j].v[i];
       }
     }
@@ -244,13 +252,8 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
       const size_t e = (c0 + c) * 8;
       F8 y;
       if (ODD) {
-        // column e + i - lo of the weight: the same residue mod 8 in every thread
-        const int k0 = (int)((ptrdiff_t)e - (ptrdiff_t)lo);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = k0 + i;
-          y.v[i] = in && k >= 0 && k < a.d ? s[j].v[i] * rstd * wsm[(k & 7) * wpitch + (k >> 3)] : 0.f;
-        }
+        for (int i = 0; i < 8; ++i) y.v[i] = odd.in(c, i) ? s[j].v[i] * rstd * wsm[odd.off(i) + c] : 0.f;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y.v[i] = in ? s[j].v[i] * rstd * w[j].v[i] : 0.f;
@@ -272,63 +275,76 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
   }
 }
 
-// Gradients.  A block (R == 32: a warp) walks rows as above; every thread keeps
-// the weight gradient of its own columns in registers over all of them and
-// leaves it in a row of `partial`, which norm_grad_sum_kernel adds up in a fixed
-// order (no atomics: the result does not depend on timing).  The columns of a
-// thread must be the same for every row, so rows of odd width are read one
-// column at a time (neighbouring threads, neighbouring columns).
+// Gradients.  A block walks rows as above and leaves the
+// weight gradient of all of them in a row of `partial`; norm_grad_sum_kernel
+// adds those up in a fixed order (no atomics: the result does not depend on
+// timing).  A thread has the same columns in every row and keeps their gradient
+// in registers; where the width is not a multiple of 8 (ODD) the windows move
+// from row to row, and the gradient lies in shared memory like the weight: a
+// column has one thread per row, and the barrier of the row's sums stands
+// between one row's additions and the next's.
 template <typename ST, int R, int C, bool ODD>
 __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2][2][32];
+  // ODD: the weight, [8][(d + 7) / 8], then the gradient likewise (R == 32: of each warp); else R == 32: the warps'
+  // gradients at the end, [4][d]
+  extern __shared__ float wsm[];
   follow();
   constexpr int kRows = R == 32 ? 4 : 1;
-  const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x;
-  const int first = blockIdx.x * kRows + (R == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows;
+  const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x, group = R == 32 ? threadIdx.x >> 5 : 0;
+  const int first = blockIdx.x * kRows + group, stride = gridDim.x * kRows;
   const ST* s_in = static_cast<const ST*>(a.s);
   const ST* dy_in = static_cast<const ST*>(a.dy);
   const ST* ds_in = static_cast<const ST*>(a.ds);
   ST* dx = static_cast<ST*>(a.dx);
-  // column of value i of chunk j: 8 (tid + j R) + i, or tid + (8 j + i) R
-  auto column = [&](int j, int i) { return ODD ? tid + (8 * j + i) * R : (tid + j * R) * 8 + i; };
-  F8 acc[C], w[C];
-#pragma unroll
-  for (int j = 0; j < C; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = column(j, i);
-      acc[j].v[i] = 0.f;
-      w[j].v[i] = k >= a.d ? 0.f
-                           : (a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
-                                                    : static_cast<const float*>(a.w)[k]);
-    }
-  auto load_row = [&](const ST* p, int row, Raw<ST>(&f)[C]) {
-    const size_t lo = (size_t)row * a.d;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (ODD) {
-        __align__(16) ST t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = column(j, i) < a.d ? p[lo + column(j, i)] : ST(0.f);
-        f[j].load(t);
-      } else if (column(j, 0) < a.d) {
-        f[j].load(p + lo + column(j, 0));
-      } else {
-        f[j].zero();
-      }
-    }
+  const size_t n = (size_t)a.T * a.d;
+  const int wpitch = (a.d + 7) / 8;
+  float* acc_sm = wsm + 8 * wpitch * (1 + group);
+  auto place = [&](int k) { return (k & 7) * wpitch + (k >> 3); };
+  auto weight = [&](int k) {
+    return a.w_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[k])
+                                 : static_cast<const float*>(a.w)[k];
   };
+
   Raw<ST> rs[C], rdy[C], rds[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) rds[j].zero();
   auto load_all = [&](int row) {
-    load_row(s_in, row, rs);
-    load_row(dy_in, row, rdy);
-    if (ds_in) load_row(ds_in, row, rds);
+    const size_t lo = (size_t)row * a.d, c0 = lo / 8;
+    const int chunks = (int)((lo + a.d + 7) / 8 - c0);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = tid + j * R;
+      if (c < chunks) {
+        load_raw<ODD>(rs[j], s_in, (c0 + c) * 8, n);
+        load_raw<ODD>(rdy[j], dy_in, (c0 + c) * 8, n);
+        if (ds_in) load_raw<ODD>(rds[j], ds_in, (c0 + c) * 8, n);
+      } else {
+        rs[j].zero();
+        rdy[j].zero();
+      }
+    }
   };
   if (first < a.T) load_all(first);
+  F8 acc[C], w[C];
+  if (ODD) {
+    for (int k = threadIdx.x; k < a.d; k += blockDim.x) wsm[place(k)] = weight(k);
+    for (int k = tid; k < 8 * wpitch; k += R) acc_sm[k] = 0.f;
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = (tid + j * R) * 8 + i;
+        acc[j].v[i] = 0.f;
+        w[j].v[i] = k < a.d ? weight(k) : 0.f;
+      }
+  }
   for (int row = first, it = 0; row < a.T; row += stride, it ^= 1) {
-    const size_t lo = (size_t)row * a.d;
+    const size_t lo = (size_t)row * a.d, hi = lo + a.d, c0 = lo / 8;
+    const int chunks = (int)((hi + 7) / 8 - c0);
+    const OddRow odd{(int)(lo & 7), wpitch, a.d};
     Raw<ST> cs[C], cdy[C], cds[C];
     float sum[2] = {0.f, 0.f};  // s^2 and s dy w
 #pragma unroll
@@ -337,43 +353,71 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
       cdy[j] = rdy[j];
       cds[j] = rds[j];
       const F8 s = cs[j].get(), dy = cdy[j].get();
+      const int c = tid + j * R;
+      if (ODD) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[j].v[i] = odd.in(c, i) ? wsm[odd.off(i) + c] : 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[0] += s.v[i] * s.v[i];
-        sum[1] += s.v[i] * dy.v[i] * w[j].v[i];
+        const bool in = !ODD || odd.in(c, i);  // (a masked neighbour may be anything)
+        sum[0] += in ? s.v[i] * s.v[i] : 0.f;
+        sum[1] += in ? s.v[i] * dy.v[i] * w[j].v[i] : 0.f;
       }
     }
     if (row + stride < a.T) load_all(row + stride);  // in flight while this row is finished
     row_sums<R>(sum, &red[it]);
     const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
-    const float k = sum[1] * rstd / (float)a.d;  // mean(g n)
+    const float k_mean = sum[1] * rstd / (float)a.d;  // mean(g n)
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const F8 s = cs[j].get(), dy = cdy[j].get();
+      const int c = tid + j * R;
       F8 o = cds[j].get();
+      if (ODD) {  // all loads before the stores: they lie in the same memory
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j].v[i] = odd.in(c, i) ? acc_sm[odd.off(i) + c] : 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float n = s.v[i] * rstd;
-        o.v[i] += rstd * (dy.v[i] * w[j].v[i] - n * k);
-        acc[j].v[i] += dy.v[i] * n;
+        const float nrm = s.v[i] * rstd;
+        o.v[i] += rstd * (dy.v[i] * w[j].v[i] - nrm * k_mean);
+        acc[j].v[i] += dy.v[i] * nrm;
       }
-      if (dx) {
-        if (ODD) {
+      if (ODD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (column(j, i) < a.d) put(dx + lo + column(j, i), o.v[i]);
-        } else if (column(j, 0) < a.d) {
-          store8(dx + lo + column(j, 0), o);
-        }
+        for (int i = 0; i < 8; ++i)
+          if (odd.in(c, i)) acc_sm[odd.off(i) + c] = acc[j].v[i];
       }
+      if (dx && c < chunks) store_chunk<ST, ODD>(dx, (c0 + c) * 8, lo, hi, o);
     }
+    if (ODD && R == 32) __syncwarp();
   }
-  if (a.dw && first < a.T) {
+  if (!a.dw) return;
+  float* to = a.partial + (size_t)blockIdx.x * a.d;
+  if (ODD || R == 32) {
+    if (!ODD) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((tid + j * R) * 8 < a.d) wsm[group * a.d + (tid + j * R) * 8 + i] = acc[j].v[i];
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.d; k += blockDim.x) {
+      const float* from = ODD ? wsm + 8 * wpitch + place(k) : wsm + k;
+      float v = from[0];
+      for (int g = 1; g < kRows; ++g) v += from[g * (ODD ? 8 * wpitch : a.d)];
+      to[k] = v;
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < C; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (column(j, i) < a.d) a.partial[(size_t)first * a.d + column(j, i)] = acc[j].v[i];
+      for (int i = 0; i < 8; ++i) {
+        const int k = (tid + j * R) * 8 + i;
+        if (k < a.d) to[k] = acc[j].v[i];
+      }
   }
 }
 
@@ -485,28 +529,40 @@ template <typename ST, int R, int C, bool ODD>
 cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
   constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
   const auto kernel = norm_grad_kernel<ST, R, C, ODD>;
+  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 * (1 + kRows) : R == 32 ? (size_t)a.d * 4 * kRows : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+  }
   int grid = (a.T + kRows - 1) / kRows;
   if (grid > 128) {
-    static const int resident = resident_blocks(kernel, kBlock, 0);
-    const int most = resident < kNormPartials / kRows ? resident : kNormPartials / kRows;
+    int most;
+    if constexpr (ODD) {
+      most = resident_blocks(kernel, kBlock, smem);
+    } else {
+      static const int resident = resident_blocks(kernel, kBlock, R == 32 ? 512 * 4 * kRows : 0);  // (the widest)
+      most = resident;
+    }
+    if (most > kNormPartials) most = kNormPartials;
     if (grid > most) grid = most;
   }
-  const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), 0, st, a);
+  const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), smem, st, a);
   if (e != cudaSuccess || !a.dw) return e;
-  const int partials = a.T < grid * kRows ? a.T : grid * kRows;
-  return launch_after(norm_grad_sum_kernel, (a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial, partials, a.d,
+  return launch_after(norm_grad_sum_kernel, (a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial, grid, a.d,
                       a.dw, a.w_dtype);
 }
 template <typename ST, bool ODD>
 cudaError_t grad_width(const NormGradArgs& a, cudaStream_t st) {
-  const int chunks = (a.d + 7) / 8;
+  const int chunks = ODD ? (a.d + 7) / 8 + 1 : a.d / 8;
   if (chunks <= 32) return grad_launch<ST, 32, 1, ODD>(a, st);
   if (chunks <= 64) return grad_launch<ST, 32, 2, ODD>(a, st);
   if (chunks <= 128) return grad_launch<ST, 128, 1, ODD>(a, st);
   if (chunks <= 256) return grad_launch<ST, 128, 2, ODD>(a, st);
   if (chunks <= 512) return grad_launch<ST, 256, 2, ODD>(a, st);
   if (chunks <= 1024) return grad_launch<ST, 512, 2, ODD>(a, st);
-  return grad_launch<ST, 1024, 2, ODD>(a, st);
+  if (chunks <= 2048) return grad_launch<ST, 1024, 2, ODD>(a, st);
+  if constexpr (ODD) return grad_launch<ST, 1024, 3, true>(a, st);  // the widest odd rows
+  return cudaErrorInvalidValue;
 }
 template <typename ST>
 cudaError_t grad_typed(const NormGradArgs& a, cudaStream_t st) {

@@ -147,6 +147,22 @@ def test_norm_backward_matches_formula(T, d, dt, with_ds):
     near(dw, dw0, rnd * dw0.abs() + (2.0 ** -20 + T * 2.0 ** -24) * (dy.to(fc.D) * n).abs().sum(0) + 1e-30, "dweight")
 
 
+@pytest.mark.parametrize("d", [64, 75, 301, 999])
+def test_norm_backward_nan_stays_in_its_row(d):
+    # (rows of odd width share 16-byte windows with their neighbours)
+    g = gen(13)
+    T = 9
+    s, dy, ds, w = (normal(g, *sh, dtype=F32) for sh in ((T, d), (T, d), (T, d), (d,)))
+    clean, _ = moe.AddNorm(d).backward(s, w, dy, ds)
+    for bad in (float("nan"), float("inf")):
+        s2, dy2 = s.clone(), dy.clone()
+        s2[3, 0], dy2[5, d - 1] = bad, bad
+        dx, dw = moe.AddNorm(d).backward(s2, w, dy2, ds)
+        keep = [0, 1, 2, 4, 6, 7, 8]
+        assert torch.equal(dx[keep], clean[keep])
+        assert not torch.isfinite(dx[3]).all() and not torch.isfinite(dx[5]).all() and not torch.isfinite(dw).all()
+
+
 def test_norm_backward_against_differences_and_repeatable():
     g = gen(11)
     T, d = 50, 104
