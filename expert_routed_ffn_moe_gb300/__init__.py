@@ -87,8 +87,8 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_set_spin_limit.argtypes = [P, ctypes.c_longlong]
         L.moe_ffn_inject_stall.argtypes = [P, I]
         L.moe_ffn_status.argtypes = [P]
-        for f in ("moe_ffn_set_spin_limit", "moe_ffn_inject_stall", "moe_add_norm", "moe_add_norm_backward", "moe_quantize_mx", "moe_ffn_init", "moe_ffn_forward",
-                  "moe_ffn_backward", "moe_ffn_status"):
+        for f in ("moe_ffn_set_spin_limit", "moe_ffn_inject_stall", "moe_add_norm", "moe_add_norm_backward",
+                  "moe_quantize_mx", "moe_ffn_init", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_status"):
             getattr(L, f).restype = I
         L.moe_add_norm_workspace.argtypes = [I]
         L.moe_mx_scale_bytes.argtypes = [I, I]
@@ -504,8 +504,8 @@ class AddNorm:
             py, pys = y[0].data_ptr(), y[1].data_ptr()
         else:
             raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
-        _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T, d, self.eps,
-                                  s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x)), "moe_add_norm")
+        _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T, d,
+                                  self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x)), "moe_add_norm")
         return y, s_out
 
     def backward(self, s, weight, dy, ds=None, stream=None):

@@ -11,7 +11,7 @@
 // One persistent kernel.  A pair of CTAs on neighbouring SMs (a cluster of two)
 // computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA loads its
 // own 128 rows of A and half of B's 256 rows, so a 64-deep k block costs each
-// SM 32 KB of shared-memory fill for 256 cycles of MMA (a lone CTA's 128 x 256
+// SM 32 KB of shared-memory fill for 512 cycles of MMA (a lone CTA's 128 x 256
 // tile takes 48 KB for the same work).  Per CTA 11 warps (12 for mx8):
 //   warps 0, 10, 11  TMA producers (one thread each) of a ring of k blocks,
 //              128-byte swizzle: A, B, and mx8's scales.  A thread takes some 100
@@ -41,12 +41,20 @@
 // the same 128 bytes.  The scale bytes are stored in the order in which
 // tcgen05.cp moves them into tensor memory, so a k block brings 512 bytes of
 // scales per 128 rows and three copies; each CTA needs its own rows' and all of
-// B's.  They take TMEM columns, so the two accumulators there share 32 columns:
+// B's.  They take TMEM columns, so the two accumulators there share 48 columns:
 // the epilogue reads those first and the next tile's MMAs may then start.  h is
 // rounded to mx8 in the epilogue, where a thread holds a whole group of 32.
 //
 // Every wait is bounded; on expiry the kernel drains what it has in flight,
 // frees TMEM and returns (see the end of the kernel).
+//
+// What bounds it: large bf16 products the MMAs (the tensor pipe is active 85-88%
+// of a CTA's time) and, run back to back, the card's power: T = 8192, d = 4096,
+// I = 16384 with pre saved, 1.96-2.05 ms, 1.61-1.68 PFLOP/s; the backward call at
+// T = 4096 2.06-2.13 ms.  mx8 at T = 8191 1.2 ms, 2.7 PFLOP/s: a block's data,
+// its scales' copies and the sight of both have to come in time for 512 cycles of
+// MMAs (TMEM has room for four blocks' scales).  Few tiles: the ~1 us that each
+// of a launch's start, first loads, epilogue and end take.
 #include "ffn_internal.h"
 
 namespace moe {
@@ -59,12 +67,14 @@ constexpr int kBK = 64;                     // k block of bf16
 constexpr int kOpBytes = 128 * kRowBytes;   // one operand's half tile: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
 constexpr int kEpiWarps = 8;
-constexpr int kBWarp = 2 + kEpiWarps;       // producers (one thread each): A on warp 0, B on this, mx8's scales on the next
+constexpr int kBWarp = 2 + kEpiWarps;       // producers: A on warp 0, B on this, mx8's scales on the next
 constexpr int roles_of(bool mx) { return mx ? 3 : 2; }  // A, B; mx8: and the scales
 constexpr int threads_of(bool mx) { return (kBWarp + roles_of(mx) - 1) * 32; }
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
-constexpr int kSharedCols = 32;             // mx8: accumulator columns that both tiles use
-constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;  // mx8: TMEM columns of two k blocks' scales, 16 each
+constexpr int kScaleSets = 4;               // mx8: k blocks whose scales TMEM holds, 12 columns each
+constexpr int kSharedCols = 12 * kScaleSets;  // mx8: accumulator columns that both tiles use
+static_assert(kSharedCols % 16 == 0 && kSharedCols <= 64, "the epilogue reads them in whole chunks, at most two groups");
+constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;
 // What a tile costs besides its k blocks, in k blocks (~0.27 us), see run(): its start and end; its epilogue by kind
 // (a split divides that too); the exchange of a split.
 constexpr int kTileCost = 6, kSplitCost = 7, kLaunchCost = 8;  // (and of another launch)
@@ -128,8 +138,8 @@ MOE_DEV void tma_load_pair(void* dst, const CUtensorMap* m, int x, int y, uint32
       : "memory");
 }
 MOE_DEV void store32(void* to, const uint32_t(&w)[8]) {  // 32-byte aligned
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 // Shared-memory matrix descriptor of an MN-major bf16 operand, 128-byte swizzle:
@@ -408,8 +418,10 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         }
       }
     } else if (rank == 0) {
-      // The scales' copies need more of a lead: the warp's lanes look at all stages at once, and lane 0 issues every
-      // block in a row that has landed (T = 4096, d = 4096, I = 8192, a forward call: 309 -> 295 us).
+      // A block needs its data and a set of scale columns, which the MMAs of the block kScaleSets before it must have
+      // left (tcgen05.cp and a later MMA keep their order, an MMA and a later tcgen05.cp need not).  Lanes 0-5 look at
+      // the stages, lanes 8 on at the blocks before, all at once, and lane 0 issues what can go.  T = 4096, d = 4096, I =
+      // 8192, a forward call: 340 us with two sets, 316 with three, 310 with four.
       for (; ok && tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
         const Product& q = p.q[0];
         const int kb0 = slot * q.blocks / SPLIT, kb1 = (slot + 1) * q.blocks / SPLIT;
@@ -418,10 +430,19 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         if (lane == 0) ok = (lt == 0 || mbar_wait(&bar->tempty[0], (lt - 1) & 1, p.ctl)) && !aborted(bar);
         const uint32_t d = tmem + acc * (kBN - kSharedCols);
         for (int kb = kb0; kb < kb1;) {
-          const bool here = lane < S && mbar_test(&bar->full[(it + lane) % S], ((it + lane) / S) & 1);
-          int n = __ffs(~__ballot_sync(0xffffffffu, here)) - 1;
+          const int before = it + lane - 8 - kScaleSets;  // lanes 8 on: blocks it - kScaleSets ... it - 1
+          bool yes = true;
+          if (lane < S)
+            yes = mbar_test(&bar->full[(it + lane) % S], ((it + lane) / S) & 1);
+          else if (lane >= 8 && lane < 8 + kScaleSets && before >= 0)
+            yes = mbar_test(&bar->empty[before % S], (before / S) & 1);
+          const uint32_t seen = __ballot_sync(0xffffffffu, yes);
+          int n = min(__ffs(~(seen & 0xffu)) - 1, __ffs(~(seen >> 8 & ((1u << kScaleSets) - 1u))) - 1);
           if (n == 0) {
-            if (lane == 0) ok = ok && mbar_wait(&bar->full[it % S], (it / S) & 1, p.ctl) && !aborted(bar);
+            if (lane == 0)
+              ok = ok && mbar_wait(&bar->full[it % S], (it / S) & 1, p.ctl) &&
+                   (it < kScaleSets || mbar_wait(&bar->empty[(it - kScaleSets) % S], ((it - kScaleSets) / S) & 1, p.ctl)) &&
+                   !aborted(bar);
             n = 1;
           }
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -433,8 +454,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
               const int st = i % S;
               const uint32_t a = smem_u32(base + st * kStageBytes);
               const uint64_t da = umma_desc_sw128(a), db = umma_desc_sw128(a + kOpBytes);
-              // tcgen05 runs a thread's copies and MMAs in the order of issue; two sets of columns for the scales
-              const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + (i & 1) * 16;
+              const uint32_t sc = smem_u32(scales + st * kScaleBytes), ts = tmem + kScaleCol + i % kScaleSets * 12;
 #pragma unroll
               for (int j = 0; j < 3; ++j) copy_scales_pair(ts + 4 * j, sc + 512 * j);
 #pragma unroll
@@ -572,18 +592,35 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
                              map_cta(&bar->tempty[MX ? 0 : acc], lead))
                          : "memory");
         };
+        const bool holds = !MX || half == (back ? 1 : 0);  // mx8: this warp reads shared columns
+        if (!holds) release();
         if (EPI == kEpiGateUp && MX) {
+          // Two groups of 32 neurons.  The shared columns are up values (back) or gate values of both groups, so the
+          // second group's are read with the first.
+          auto column = [&](int i) { return half * 64 + (back ? 1 - i : i) * 32; };
+          auto load = [&](float* v, int c) {
+            tmem_ld16_async(src + c, v);
+            tmem_ld16_async(src + c + 16, v + 16);
+          };
+          float g[32], u[32], next[32];
+          load(g, column(0));
+          load(u, 128 + column(0));
+          load(next, (back ? 128 : 0) + column(1));
+          tmem_ld_wait();
+          if (holds) release();
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
-            const int c = half * 64 + (back ? 1 - i : i) * 32;
-            float g[32], u[32];
-            tmem_ld16_async(src + c, g);
-            tmem_ld16_async(src + c + 16, g + 16);
-            tmem_ld16_async(src + 128 + c, u);
-            tmem_ld16_async(src + 128 + c + 16, u + 16);
-            tmem_ld_wait();
-            if (i == 0) release();
-            finish_mx(q, row, n * TN + c, g, u);
+            finish_mx(q, row, n * TN + column(i), g, u);
+            if (i == 0) {
+              float other[32];
+              load(other, (back ? 0 : 128) + column(1));
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                g[e] = back ? other[e] : next[e];
+                u[e] = back ? next[e] : other[e];
+              }
+            }
           }
         } else {
           // 16 columns (neurons) at a time in a compact loop: straight-line code for the whole tile takes longer to
@@ -603,7 +640,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = v[e], y[e] = u[e];
             const uint4 now[4] = {in[0], in[1], in[2], in[3]};
-            if (i == kShared - 1) release();
+            if (holds && i == kShared - 1) release();
             if (i + 1 < kChunks) {
               load(i + 1);
               load_pre(q, row, n * TN + (half * kChunks + i + 1) * 16, in);
@@ -806,7 +843,8 @@ bool set_product(const FfnEngine& e, Product& q, const void* a, const void* b, i
   if (!y && EPI == kEpiStore) return true;
   if (MX) return make_code_map(e.encode, &q.a, a, K, M, 128) && make_code_map(e.encode, &q.b, b, K, b_rows, 128);
   // a K-major operand is [rows, K], an MN-major one [K, rows]
-  return (A_MN ? make_bf16_map(e.encode, &q.a, a, M, K, M, 64, kBK) : make_bf16_map(e.encode, &q.a, a, K, M, K, kBK, kBM)) &&
+  return (A_MN ? make_bf16_map(e.encode, &q.a, a, M, K, M, 64, kBK)
+               : make_bf16_map(e.encode, &q.a, a, K, M, K, kBK, kBM)) &&
          (B_MN ? make_bf16_map(e.encode, &q.b, b, b_rows, K, b_rows, 64, kBK)
                : make_bf16_map(e.encode, &q.b, b, K, b_rows, K, kBK, 128));
 }
@@ -909,7 +947,8 @@ cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const F
   p.hq = hq;
   p.hs = hs;
   const uint64_t tiles = (s.I + 127) / 128;
-  if (!set_product<kEpiGateUp, false, false, true>(e, p.q[0], a.x, a.gate_up, s.T, s.I, s.d, 2 * (uint64_t)s.I, nullptr) ||
+  if (!set_product<kEpiGateUp, false, false, true>(e, p.q[0], a.x, a.gate_up, s.T, s.I, s.d, 2 * (uint64_t)s.I,
+                                                   nullptr) ||
       !make_scale_map(e.encode, &p.as, a.xs, s.d, (s.T + 127) / 128) ||
       !make_scale_map(e.encode, &p.bs0, a.gate_up_s, s.d, tiles) || !make_scale_map(e.encode, &p.bs1, up_s, s.d, tiles))
     return cudaErrorInvalidValue;
@@ -1012,7 +1051,8 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   for (int i = 0; i < p.count && err == cudaSuccess; ++i) {
     GemmParams one{};
     one.q[0] = p.q[i];
-    err = one.q[0].a_mn ? run<kEpiStore, true, true, false>(e, one, st) : run<kEpiStore, false, true, false>(e, one, st);
+    err = one.q[0].a_mn ? run<kEpiStore, true, true, false>(e, one, st)
+                        : run<kEpiStore, false, true, false>(e, one, st);
   }
   return err;
 }

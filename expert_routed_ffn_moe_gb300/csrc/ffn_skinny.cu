@@ -62,8 +62,10 @@ constexpr int exchange_bytes(bool gate, int nt) { return nt * (gate ? 2 : 1) * k
 // in their order (a wait by parity for a phase after the next would return at
 // once).  A gate/up and a down CTA fit an SM together.
 constexpr int stages_of(bool gate, int nt) { return gate && nt <= 16 ? 6 : 4; }
-constexpr uint32_t tmem_cols(bool mx, int nt) {
-  const int need = 2 * nt + (mx ? 16 : 0);
+// Accumulators; mx8: and 8 columns of scales per stage, so that they are overwritten only when the MMAs that read them
+// are done, like the stage itself.
+constexpr uint32_t tmem_cols(bool mx, bool gate, int nt) {
+  const int need = 2 * nt + (mx ? 8 * stages_of(gate, nt) : 0);
   return need <= 32 ? 32 : need <= 64 ? 64 : 128;
 }
 
@@ -123,7 +125,7 @@ template <bool MX, bool GATE, int NT>
 __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_constant__ SkinnyParams p) {
   static_assert(stages_of(GATE, NT) % 2 == 0 && stages_of(GATE, NT) <= kMaxStages, "see stages_of");
   constexpr int S = stages_of(GATE, NT), kStage = stage_bytes(MX, NT);
-  constexpr uint32_t kCols = tmem_cols(MX, NT);
+  constexpr uint32_t kCols = tmem_cols(MX, GATE, NT);
   constexpr int kDepth = MX ? 128 : 64;  // values of k per block
   constexpr int kParts = GATE ? 2 : 1;   // weight blocks per k block
   extern __shared__ uint8_t smem_raw[];
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
         const uint64_t da = umma_desc_sw128(smem_u32(base + st * kBlockBytes));
         const uint64_t db = umma_desc_sw128(smem_u32(xs0 + st * NT * 128));
         if (MX) {
-          const uint32_t ts = tmem + 2 * NT + odd * 8, sc = smem_u32(sc0 + st * 1024);
+          const uint32_t ts = tmem + 2 * NT + st * 8, sc = smem_u32(sc0 + st * 1024);
           copy_scales(ts, sc);
           copy_scales(ts + 4, sc + 512);
 #pragma unroll

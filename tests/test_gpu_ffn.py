@@ -189,7 +189,8 @@ def test_norm_backward_against_differences_and_repeatable():
 
 # ------------------------------------------------------------------ feed-forward block
 SHAPES = [(1, 2048, 512), (1, 4096, 8192), (5, 1000, 5000), (40, 2048, 3000), (64, 8, 4096), (17, 4096, 8),
-          (3, 136, 9000), (62, 640, 640), (63, 2048, 200), (1, 8, 8), (2, 16, 24), (3, 64, 72), (7, 200, 136), (8, 512, 1000), (9, 2048, 2048),
+          (3, 136, 9000), (62, 640, 640), (63, 2048, 200), (1, 8, 8), (2, 16, 24), (3, 64, 72), (7, 200, 136),
+          (8, 512, 1000), (9, 2048, 2048),
           (16, 256, 128), (17, 520, 264), (32, 2048, 512), (33, 72, 2000), (64, 1024, 640), (100, 256, 8),
           (127, 128, 256), (128, 256, 128), (129, 264, 384), (200, 8, 520), (255, 640, 768), (256, 512, 256),
           (257, 1000, 1000), (385, 2048, 136), (511, 136, 1544), (640, 1536, 1024), (1000, 328, 2744), (1537, 512, 512)]
@@ -273,7 +274,8 @@ def test_mx8_forward_matches_definition(T, d, I, name):
 
 def test_saturated_activations_stay_finite():
     # gates far outside the range in which exp() is finite, and the ends of bf16
-    vals = torch.tensor([-3e38, -1e19, -1e4, -200.0, -90.0, -10.0, -1e-30, 0.0, 1e-30, 10.0, 90.0, 200.0, 1e4], device="cuda")
+    vals = torch.tensor([-3e38, -1e19, -1e4, -200.0, -90.0, -10.0, -1e-30, 0.0, 1e-30, 10.0, 90.0, 200.0, 1e4],
+                        device="cuda")
     I = 16
     pre = torch.zeros(len(vals), 2 * I, dtype=BF, device="cuda")
     pre[:, :I] = vals.to(BF).view(-1, 1)
@@ -398,7 +400,8 @@ def test_refusals():
                 lambda: op.forward(z(4, 32), gu, dn), lambda: op.forward(x, z(32, 64), dn),
                 lambda: op.forward(x.cpu(), gu, dn), lambda: op.forward(x, gu, dn, y=z(5, 64)),
                 lambda: moe.AddNorm(64).forward(z(4, 32), None, z(32)), lambda: moe.AddNorm(64).forward(x, None, z(32)),
-                lambda: moe.AddNorm(64).forward(x, x.half(), z(64)), lambda: moe.AddNorm(64).forward(x, None, z(64), y_dtype=7),
+                lambda: moe.AddNorm(64).forward(x, x.half(), z(64)),
+                lambda: moe.AddNorm(64).forward(x, None, z(64), y_dtype=7),
                 lambda: moe.GatedFfn(64, 32, 8, weight_format=moe.MOE_W_MX8).forward(x, gu, dn)):
         with pytest.raises(ValueError):
             bad()
