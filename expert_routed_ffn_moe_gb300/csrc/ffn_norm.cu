@@ -136,9 +136,12 @@ MOE_DEV void row_sums(float (&v)[N], float (*red)[N][32]) {
 // Rows of odd width: where value i of window c of a row that begins r = (its
 // first value) mod 8 into the first window has its column in an array [8][pitch]
 // by (column mod 8, column / 8): at off(i) + c, off() the same in all threads.
+// Only the first and the last window hold values of other rows (not in()); for
+// those off(i) + c is some other place of the array, or the one past its end.
 struct OddRow {
-  int r, pitch, d;
+  int r, pitch, d, chunks;
   MOE_DEV int off(int i) const { return i >= r ? (i - r) * pitch : (i - r + 8) * pitch - 1; }
+  MOE_DEV bool edge(int c) const { return c == 0 || c >= chunks - 1; }
   MOE_DEV bool in(int c, int i) const { return (unsigned)(8 * c + i - r) < (unsigned)d; }
 };
 
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
     }
     const size_t lo = (size_t)row * a.d, hi = lo + a.d, c0 = lo / 8;
     const int chunks = (int)((hi + 7) / 8 - c0);
-    const OddRow odd{(int)(lo & 7), wpitch, a.d};
+    const OddRow odd{(int)(lo & 7), wpitch, a.d, chunks};
     F8 s[C];
     float sum[1] = {0.f};
 #pragma unroll
@@ -231,11 +234,14 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
       s[j] = x[j].get();
       const F8 r = res[j].get();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[j].v[i] += r.v[i];
-        if (ODD && !odd.in(tid + j * R, i)) s[j].v[i] = 0.f;
-        sum[0] += s[j].v[i] * s[j].v[i];
+      for (int i = 0; i < 8; ++i) s[j].v[i] += r.v[i];
+      if (ODD && odd.edge(tid + j * R)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!odd.in(tid + j * R, i)) s[j].v[i] = 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += s[j].v[i] * s[j].v[i];
     }
     if (row + stride < a.T) load_row(row + stride, x, res);  // in flight while this row is finished
     if (s_out) {
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_kernel(NormArgs a) {
       F8 y;
       if (ODD) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y.v[i] = odd.in(c, i) ? s[j].v[i] * rstd * wsm[odd.off(i) + c] : 0.f;
+        for (int i = 0; i < 8; ++i) y.v[i] = in ? s[j].v[i] * rstd * wsm[odd.off(i) + c] : 0.f;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y.v[i] = in ? s[j].v[i] * rstd * w[j].v[i] : 0.f;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
   for (int row = first, it = 0; row < a.T; row += stride, it ^= 1) {
     const size_t lo = (size_t)row * a.d, hi = lo + a.d, c0 = lo / 8;
     const int chunks = (int)((hi + 7) / 8 - c0);
-    const OddRow odd{(int)(lo & 7), wpitch, a.d};
+    const OddRow odd{(int)(lo & 7), wpitch, a.d, chunks};
     Raw<ST> cs[C], cdy[C], cds[C];
     float sum[2] = {0.f, 0.f};  // s^2 and s dy w
 #pragma unroll
@@ -352,17 +358,23 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
       cs[j] = rs[j];
       cdy[j] = rdy[j];
       cds[j] = rds[j];
-      const F8 s = cs[j].get(), dy = cdy[j].get();
+      F8 s = cs[j].get(), dy = cdy[j].get();
       const int c = tid + j * R;
       if (ODD) {
+        if (c < chunks) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[j].v[i] = odd.in(c, i) ? wsm[odd.off(i) + c] : 0.f;
+          for (int i = 0; i < 8; ++i) w[j].v[i] = wsm[odd.off(i) + c];
+        }
+        if (odd.edge(c)) {  // (a neighbour's value may be anything)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!odd.in(c, i)) s.v[i] = dy.v[i] = w[j].v[i] = 0.f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = !ODD || odd.in(c, i);  // (a masked neighbour may be anything)
-        sum[0] += in ? s.v[i] * s.v[i] : 0.f;
-        sum[1] += in ? s.v[i] * dy.v[i] * w[j].v[i] : 0.f;
+        sum[0] += s.v[i] * s.v[i];
+        sum[1] += s.v[i] * dy.v[i] * w[j].v[i];
       }
     }
     if (row + stride < a.T) load_all(row + stride);  // in flight while this row is finished
@@ -375,8 +387,13 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
       const int c = tid + j * R;
       F8 o = cds[j].get();
       if (ODD) {  // all loads before the stores: they lie in the same memory
+        if (!odd.edge(c)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j].v[i] = odd.in(c, i) ? acc_sm[odd.off(i) + c] : 0.f;
+          for (int i = 0; i < 8; ++i) acc[j].v[i] = acc_sm[odd.off(i) + c];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[j].v[i] = odd.in(c, i) ? acc_sm[odd.off(i) + c] : 0.f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -385,9 +402,14 @@ __global__ void __launch_bounds__(R == 32 ? 128 : R) norm_grad_kernel(NormGradAr
         acc[j].v[i] += dy.v[i] * nrm;
       }
       if (ODD) {
+        if (!odd.edge(c)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (odd.in(c, i)) acc_sm[odd.off(i) + c] = acc[j].v[i];
+          for (int i = 0; i < 8; ++i) acc_sm[odd.off(i) + c] = acc[j].v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (odd.in(c, i)) acc_sm[odd.off(i) + c] = acc[j].v[i];
+        }
       }
       if (dx && c < chunks) store_chunk<ST, ODD>(dx, (c0 + c) * 8, lo, hi, o);
     }
@@ -485,7 +507,7 @@ template <typename XT, typename ST, int R, int C, bool ODD>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
   constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
   const auto kernel = norm_kernel<XT, ST, R, C, ODD>;
-  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 : 0;
+  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 + 4 : 0;  // (see OddRow)
   if (smem > 48 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
@@ -529,7 +551,7 @@ template <typename ST, int R, int C, bool ODD>
 cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
   constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
   const auto kernel = norm_grad_kernel<ST, R, C, ODD>;
-  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 * (1 + kRows) : R == 32 ? (size_t)a.d * 4 * kRows : 0;
+  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 * (1 + kRows) + 4 : R == 32 ? (size_t)a.d * 4 * kRows : 0;
   if (smem > 48 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
