@@ -75,7 +75,7 @@ constexpr int kScaleSets = 4;               // mx8: k blocks whose scales TMEM h
 constexpr int kSharedCols = 12 * kScaleSets;  // mx8: accumulator columns that both tiles use
 static_assert(kSharedCols % 16 == 0 && kSharedCols <= 64, "the epilogue reads them in whole chunks, at most two groups");
 constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;
-// What a tile costs besides its k blocks, in k blocks (~0.27 us), see run(): its start and end; its epilogue by kind
+// What a tile costs besides its k blocks, in k blocks (~0.27 us), see split_of(): its start and end; its epilogue by kind
 // (a split divides that too); the exchange of a split.
 constexpr int kTileCost = 6, kSplitCost = 7, kLaunchCost = 8;  // (and of another launch)
 constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 1 ? 9 : 16; }

@@ -193,7 +193,8 @@ SHAPES = [(1, 2048, 512), (1, 4096, 8192), (5, 1000, 5000), (40, 2048, 3000), (6
           (8, 512, 1000), (9, 2048, 2048),
           (16, 256, 128), (17, 520, 264), (32, 2048, 512), (33, 72, 2000), (64, 1024, 640), (100, 256, 8),
           (127, 128, 256), (128, 256, 128), (129, 264, 384), (200, 8, 520), (255, 640, 768), (256, 512, 256),
-          (257, 1000, 1000), (385, 2048, 136), (511, 136, 1544), (640, 1536, 1024), (1000, 328, 2744), (1537, 512, 512)]
+          (257, 1000, 1000), (385, 2048, 136), (511, 136, 1544), (640, 1536, 1024), (1000, 328, 2744), (1537, 512, 512),
+          (3000, 1024, 1032), (2049, 2048, 264)]
 
 
 @pytest.mark.parametrize("T,d,I", SHAPES)
@@ -258,7 +259,8 @@ def test_backward_against_differences(name):
 @pytest.mark.parametrize("T,d,I", [(1, 2048, 512), (1, 4096, 8192), (17, 4096, 32), (48, 1024, 3008), (3, 160, 8992),
                                    (1, 32, 32), (2, 64, 96), (9, 1024, 2048), (16, 256, 160),
                                    (33, 96, 2048), (64, 512, 224), (128, 256, 128), (129, 288, 384), (257, 1024, 992),
-                                   (511, 160, 1568), (1000, 352, 2752)])
+                                   (511, 160, 1568), (1000, 352, 2752), (2000, 256, 4128), (2000, 4096, 256),
+                                   (700, 4128, 4096)])
 @pytest.mark.parametrize("name", ["silu", "gelu"])
 def test_mx8_forward_matches_definition(T, d, I, name):
     g = gen(T + 5000 * d + I)
