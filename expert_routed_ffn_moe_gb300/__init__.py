@@ -361,29 +361,28 @@ def _t():
 
 
 def _handle(stream, t):
-    return _t()._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _checked(t, name, shape, dtype=None):
     """t's address, after the checks; None for None.  Without ``dtype`` t is float32 or bfloat16."""
     if t is None:
         return None
+    if t.is_cuda and t.shape == shape and (t.dtype in _DTYPES if dtype is None else t.dtype is dtype) and \
+            t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is None:
-        if t.dtype not in _DTYPES:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    elif t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {'float32 or bfloat16' if dtype is None else dtype}, got {t.dtype}")
 
 
 def _rows(t, name, cols=None):
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must have shape [rows, {'cols' if cols is None else cols}], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} must have shape [rows, {'cols' if cols is None else cols}], got {tuple(shape)}")
+    return shape
 
 
 def _mx_bytes(rows, cols):
@@ -504,8 +503,10 @@ class AddNorm:
             py, pys = y[0].data_ptr(), y[1].data_ptr()
         else:
             raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
-        _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T, d,
-                                  self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x)), "moe_add_norm")
+        code = (_lib or lib()).moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T,
+                                            d, self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x))
+        if code:
+            _check(code, "moe_add_norm")
         return y, s_out
 
     def backward(self, s, weight, dy, ds=None, stream=None):
@@ -580,8 +581,9 @@ class GatedFfn:
         if pre is None and save:
             pre = torch.empty(T, 2 * I, dtype=bf16, device=rows.device)
         pp = _checked(pre, "pre", (T, 2 * I), bf16)
-        _check(lib().moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(stream, rows)),
-               "moe_ffn_forward")
+        code = (_lib or lib()).moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(stream, rows))
+        if code:
+            _check(code, "moe_ffn_forward")
         return (y, pre) if pre is not None else y
 
     def backward(self, x, pre, gate_up, down, dy, dx=None, dgate_up=None, ddown=None, stream=None):
