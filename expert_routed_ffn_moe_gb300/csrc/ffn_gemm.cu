@@ -89,7 +89,7 @@ struct Product {
   uint16_t* y;                     // bf16 result: y / dx / dW, or h
   int M, N, K;                     // N: columns of the result (gate/up: neurons)
   int a_mn;                        // MULTI: a is MN-major
-  int wide;                        // rows of the results are 32-byte aligned: N is a multiple of 16
+  int wide;                        // rows of the results are 32-byte aligned (a tensor's first row need only be 16)
   int mt, nt, tiles, blocks;       // m-tiles, n-tiles, their product, k blocks
 };
 struct GemmParams {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
   } else {
     const int ew = warp - 2, part = warp & 3, half = ew >> 2;
     const uint32_t lanes = (uint32_t)(part * 32) << 16;
-    // 16 columns of a row as bf16; N is a multiple of 8, and of 16 where q.wide says so
+    // 16 columns of a row as bf16; N is a multiple of 8, and of 16 where q.wide is set
     auto store16 = [&](const Product& q, uint16_t* to, int pitch, int row, int col, const float(&v)[16]) {
       if (row >= q.M) return;
       uint32_t w[8];
@@ -824,6 +824,8 @@ cudaError_t launch(const GemmParams& p, int clusters, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT, MULTI>, p);
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // A product's operands and sizes.  b_rows: rows of b (columns where it is MN-major).  Without y the sizes alone.
 template <int EPI, bool A_MN, bool B_MN, bool MX>
 bool set_product(const FfnEngine& e, Product& q, const void* a, const void* b, int M, int N, int K, uint64_t b_rows,
@@ -833,7 +835,7 @@ bool set_product(const FfnEngine& e, Product& q, const void* a, const void* b, i
   q.N = N;
   q.K = K;
   q.a_mn = A_MN;
-  q.wide = N % 16 == 0;
+  q.wide = N % 16 == 0 && aligned32(y);
   q.y = static_cast<uint16_t*>(y);
   q.mt = (M + 2 * kBM - 1) / (2 * kBM);
   q.nt = (N + TN - 1) / TN;
@@ -973,6 +975,7 @@ cudaError_t launch_ffn_gate_up(const FfnEngine& e, const FfnShape& s, const void
   p.pre_out = pre;
   if (!set_product<kEpiGateUp, false, false, false>(e, p.q[0], x, gate_up, s.T, s.I, s.d, 2 * (uint64_t)s.I, h))
     return cudaErrorInvalidValue;
+  if (!aligned32(pre)) p.q[0].wide = 0;
   return run<kEpiGateUp, false, false, false>(e, p, st);
 }
 

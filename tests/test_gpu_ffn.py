@@ -341,6 +341,42 @@ def test_stream_graph_and_reuse():
     assert op.status() == moe.MOE_OK and moe.moe_ffn_launch_count(op.ctx) > 0
 
 
+def shifted(t):
+    """A copy of t that begins 16 bytes past a 32-byte boundary."""
+    n = 16 // t.element_size()
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)[n:].view(t.shape)
+    assert buf.data_ptr() % 32 == 16
+    return buf.copy_(t)
+
+
+@pytest.mark.parametrize("T", [3, 300, 700])
+def test_tensors_at_16_bytes_give_the_same(T):
+    d, I = 256, 544
+    g = gen(T)
+    x, gu, dn = normal(g, T, d), normal(g, 2 * I, d, scale=0.05), normal(g, d, I, scale=0.05)
+    dy, w = normal(g, T, d), normal(g, d)
+    ffn, mx = moe.GatedFfn(d, I, T, training=True), moe.GatedFfn(d, I, T, weight_format=moe.MOE_W_MX8)
+    y0, pre0 = ffn.forward(x, gu, dn, save=True)
+    grads0 = ffn.backward(x, pre0, gu, dn, dy)
+    sx, sgu, sdn, sdy = (shifted(t) for t in (x, gu, dn, dy))
+    y, pre = shifted(torch.zeros_like(y0)), shifted(torch.zeros_like(pre0))
+    for out in ((y, pre), (y, torch.zeros_like(pre0)), (torch.zeros_like(y0), pre)):
+        got = ffn.forward(sx, sgu, sdn, y=out[0], pre=out[1])
+        assert torch.equal(got[0], y0) and torch.equal(got[1], pre0)
+    outs = [shifted(torch.zeros_like(t)) for t in grads0]
+    for a, b in zip(ffn.backward(sx, pre, sgu, sdn, sdy, *outs), grads0):
+        assert torch.equal(a, b)
+    q = [moe.moe_quantize_mx(t) for t in (x, gu, dn)]
+    y0 = mx.forward(*q)
+    sq = [(shifted(c), shifted(s)) for c, s in (moe.moe_quantize_mx(shifted(t)) for t in (x, gu, dn))]
+    assert torch.equal(mx.forward(*sq, y=shifted(torch.zeros_like(y0))), y0)
+    op = moe.AddNorm(d)
+    for a, b in zip(op.forward(sx, sdy, shifted(w)), op.forward(x, dy, w)):
+        assert torch.equal(a, b)
+    for a, b in zip(op.backward(sx, shifted(w), sdy), op.backward(x, w, dy)):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     # pre has 2.3e9 elements, h 1.15e9
     g = gen(10)
