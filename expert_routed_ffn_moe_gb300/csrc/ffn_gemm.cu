@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                        smem_u32(&bar->mma_done))
                    : "memory");
-      mbar_wait(&bar->mma_done, 0, p.ctl);
+      mbar_wait(&bar->mma_done, 0, drain_ctl(p.ctl));
     }
     __syncwarp();
   } else {
@@ -695,11 +695,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           __syncwarp();
         }
         ok = mbar_wait(&bar->recv[ew], 0, p.ctl);
-        if (!ok) {
-          DevCtl drain = p.ctl;
-          drain.spin_limit = 1000000000LL;
-          mbar_wait(&bar->recv[ew], 0, drain);
-        }
+        if (!ok) mbar_wait(&bar->recv[ew], 0, drain_ctl(p.ctl));
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) {
@@ -776,8 +772,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       for (int r = 0; r < kRoles; ++r) store_cluster(map_cta(&bar->issued[1][r], lead), bar->issued[1][r]);
     cluster_sync();
     if (threadIdx.x == 0 && rank == 0) {
-      DevCtl drain = p.ctl;
-      drain.spin_limit = 1000000000LL;
+      const DevCtl drain = drain_ctl(p.ctl);
       constexpr uint32_t bytes[3] = {kOpBytes, kOpBytes, kScaleBytes};
       int most = 0;
       for (int r = 0; r < 2 * kRoles; ++r) most = max(most, (int)bar->issued[r / kRoles][r % kRoles]);

@@ -98,6 +98,14 @@ MOE_DEV void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// For waits that end by themselves, on what the CTA itself has in flight before
+// it leaves: 1 s, however short the caller's limit.
+MOE_DEV DevCtl drain_ctl(const DevCtl& c) {
+  DevCtl d = c;
+  d.spin_limit = 1000000000LL;
+  return d;
+}
+
 // ---------------------------------------------------------------- activations
 // silu(g) = g sigmoid(g); gelu in its tanh form, 0.5 g (1 + tanh z) =
 // g sigmoid(2 z): both from the fast exponential and division of sigmoid

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
       }
       if (ok) umma_commit(&bar->tfull);
       umma_commit(&bar->mma_done);  // the MMAs issued so far are done before TMEM is freed
-      mbar_wait(&bar->mma_done, 0, p.ctl);
+      mbar_wait(&bar->mma_done, 0, drain_ctl(p.ctl));
     }
   }
   __syncwarp();
@@ -346,8 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
   if (threadIdx.x == 0 && bar->abort_flag) {
     // After an abort copies may be in flight (otherwise an MMA has waited for each): the last step of every stage
     // that anyone has issued must land before the CTA leaves.
-    DevCtl drain = p.ctl;
-    drain.spin_limit = 1000000000LL;
+    const DevCtl drain = drain_ctl(p.ctl);
     for (int st = 0; st < S; ++st)
       for (int j = st + (steps - 1) / S * S; j >= 0; j -= S) {
         const bool w = j < bar->issued[0][j & 1], t = j < bar->issued[1][j & 1];
