@@ -382,6 +382,8 @@ def _rows(t, name, cols=None):
     shape = t.shape
     if len(shape) != 2 or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must have shape [rows, {'cols' if cols is None else cols}], got {tuple(shape)}")
+    if shape[0] > 0x7fffffff or shape[1] > 0x7fffffff:
+        raise ValueError(f"{name} of shape {tuple(shape)}: more rows or columns than an int holds")
     return shape
 
 

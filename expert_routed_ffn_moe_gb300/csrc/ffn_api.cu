@@ -20,6 +20,7 @@ struct moe_ffn {
 namespace {
 
 constexpr long long kDefaultSpinNs = 1000000000LL;  // 1 s
+constexpr int kMaxRows = 1 << 30;  // norm, rounding to mx8: a row's number plus a grid of rows stays an int
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool stream_dtype(int t) { return t == MOE_F32 || t == MOE_BF16; }
@@ -41,7 +42,7 @@ long long moe_mx_scale_bytes(int rows, int cols) {
 
 int moe_quantize_mx(const void* v, int dtype, int rows, int cols, void* codes, void* scales, void* stream) {
   if (rows < 0 || cols < 0 || !stream_dtype(dtype)) return MOE_ERR_ARG;
-  if (cols % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (cols % 32 != 0 || rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return MOE_OK;
   if (!v || !codes || !scales) return MOE_ERR_ARG;
   if (!aligned16(v) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_ALIGN;
@@ -54,7 +55,7 @@ int moe_add_norm(const void* x, int x_dtype, const void* residual, int s_dtype, 
                  int d, float eps, void* s_out, void* y, int y_dtype, void* y_scales, void* stream) {
   if (T < 0 || d <= 0 || !stream_dtype(x_dtype) || !stream_dtype(s_dtype) || !stream_dtype(w_dtype)) return MOE_ERR_ARG;
   if ((!stream_dtype(y_dtype) && y_dtype != MOE_MX8) || !(eps >= 0.f)) return MOE_ERR_ARG;
-  if (d > kMaxNormWidth || (y_dtype == MOE_MX8 && d % 32 != 0)) return MOE_ERR_UNSUPPORTED;
+  if (d > kMaxNormWidth || T > kMaxRows || (y_dtype == MOE_MX8 && d % 32 != 0)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !weight || !y || (y_dtype == MOE_MX8) != (y_scales != nullptr)) return MOE_ERR_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(s_out) || !aligned16(y) ||
@@ -71,7 +72,7 @@ long long moe_add_norm_workspace(int d) { return d <= 0 ? 0 : (long long)kNormPa
 int moe_add_norm_backward(const void* s, const void* weight, const void* dy, const void* ds, int dtype, int w_dtype,
                           int T, int d, float eps, void* dx, void* dweight, void* workspace, void* stream) {
   if (T < 0 || d <= 0 || !stream_dtype(dtype) || !stream_dtype(w_dtype) || !(eps >= 0.f)) return MOE_ERR_ARG;
-  if (d > kMaxNormWidth) return MOE_ERR_UNSUPPORTED;
+  if (d > kMaxNormWidth || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (!dx && !dweight) return MOE_ERR_ARG;
   if (T > 0 && (!s || !weight || !dy || (dweight && !workspace))) return MOE_ERR_ARG;
   if (!aligned16(s) || !aligned16(weight) || !aligned16(dy) || !aligned16(ds) || !aligned16(dx) ||

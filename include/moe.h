@@ -321,8 +321,8 @@ int moe_last_routing(moe_ctx* ctx, int32_t* idx, float* w, int32_t* counts, int3
  * in y_scales, which is NULL for the others).  s_out may be residual itself,
  * and y may be x where their dtypes are the same and d is a multiple of 8;
  * no other output may overlap an input.  d is any width up to 16384 (a multiple
- * of 32 for MOE_MX8), MOE_ERR_UNSUPPORTED beyond; MOE_ERR_ARG for a dtype not
- * listed or eps < 0.  No workspace, no context. */
+ * of 32 for MOE_MX8) and T at most 2^30, MOE_ERR_UNSUPPORTED beyond; MOE_ERR_ARG
+ * for a dtype not listed or eps < 0.  No workspace, no context. */
 int moe_add_norm(const void* x, int x_dtype, const void* residual, int s_dtype, const void* weight, int w_dtype, int T,
                  int d, float eps, void* s_out, void* y, int y_dtype, void* y_scales, void* stream);
 
@@ -338,7 +338,8 @@ long long moe_add_norm_workspace(int d);
  * residual alike.  weight and dweight [d] have w_dtype.  dx or dweight may be
  * NULL to skip it; dx may be dy or ds.  workspace: moe_add_norm_workspace(d)
  * bytes, needed for dweight; calls that overlap in time need one each.  The
- * result does not depend on timing.  T == 0 sets dweight to 0. */
+ * result does not depend on timing.  T == 0 sets dweight to 0.  Limits of d and T
+ * as above. */
 int moe_add_norm_backward(const void* s, const void* weight, const void* dy, const void* ds, int dtype, int w_dtype,
                           int T, int d, float eps, void* dx, void* dweight, void* workspace, void* stream);
 
@@ -347,7 +348,7 @@ long long moe_mx_scale_bytes(int rows, int cols);
 
 /* Round v [rows, cols] (dtype MOE_F32 or MOE_BF16) to MOE_MX8: codes [rows,
  * cols] and scales, e.g. for the weights of a block with MOE_W_MX8.  cols is a
- * multiple of 32 (MOE_ERR_UNSUPPORTED otherwise). */
+ * multiple of 32 and rows at most 2^30 (MOE_ERR_UNSUPPORTED otherwise). */
 int moe_quantize_mx(const void* v, int dtype, int rows, int cols, void* codes, void* scales, void* stream);
 
 typedef struct moe_ffn_config {

@@ -95,3 +95,21 @@ def test_mx8_definition():
     assert [int(scales[i]) - 127 for i in (0, 1, 2)] == [0, 1, -127]
     back = fc.dequantize(codes, scales)
     assert back[0, 3] == 448 and back[0, 40] == -448 and back[0, 41] == 1 and not back[0, 64:].any()
+
+
+@pytest.mark.parametrize("rows", [(1 << 30) + 1, (1 << 31) - 128, (1 << 31) - 1])
+def test_more_rows_than_the_kernels_count_are_refused(lib, rows):
+    a, B = ctypes.c_void_p(16), moe.MOE_BF16  # never dereferenced
+    assert lib.moe_add_norm(a, B, None, B, a, B, rows, 1, 1e-6, None, a, B, None, None) == moe.MOE_ERR_UNSUPPORTED
+    assert lib.moe_add_norm_backward(a, a, a, None, B, B, rows, 1, 1e-6, a, a, a, None) == moe.MOE_ERR_UNSUPPORTED
+    assert lib.moe_quantize_mx(a, B, rows, 32, a, a, None) == moe.MOE_ERR_UNSUPPORTED
+
+
+def test_sizes_past_an_int_are_refused_before_the_call():
+    # (the C entries take ints: 2^32 + 1 rows would arrive there as one)
+    t = torch.empty((1 << 32) + 1, 32, dtype=torch.bfloat16, device="meta")
+    w = torch.empty(32, dtype=torch.bfloat16, device="meta")
+    for call in (lambda: moe.moe_quantize_mx(t), lambda: moe.AddNorm(32).forward(t, None, w),
+                 lambda: moe.AddNorm(32).backward(t, w, t)):
+        with pytest.raises(ValueError, match="than an int holds"):
+            call()
