@@ -345,7 +345,9 @@ class MoeLayer:
 # ---------------------------------------------------------------- feed-forward block and its norm
 # These calls take a few microseconds on the device, so the checks are kept
 # cheap: tensors' properties are compared directly, and the stream's handle is
-# read without making a stream object.
+# read without making a stream object.  Calls that make tensors make them as the
+# given stream's: with memory of the present stream a call on another one could
+# write what kernels on the present one still read.
 _torch = None
 _DTYPES = {}  # torch dtype -> MOE_F32 / MOE_BF16
 
@@ -420,13 +422,16 @@ def _mx_empty(rows, cols, device):
 
 def moe_quantize_mx(v, codes=None, scales=None, stream=None):
     """Round a float32 or bfloat16 matrix to mx8: (codes, scales); see moe.h."""
-    _t()
+    torch = _t()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_quantize_mx(v, codes, scales)
     rows, cols = _rows(v, "v")
     pv = _checked(v, "v", v.shape)
     if codes is None or scales is None:
         codes, scales = _mx_empty(rows, cols, v.device)
     pc, ps = _mx_checked((codes, scales), "output", rows, cols)
-    _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(stream, v)), "moe_quantize_mx")
+    _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(None, v)), "moe_quantize_mx")
     return codes, scales
 
 
@@ -485,6 +490,9 @@ class AddNorm:
         """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
         in the residual's dtype (x's without a residual)."""
         torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, residual, weight, y_dtype, s_out)
         shape = _rows(x, "x", self.d)
         T, d = shape
         px, pr, pw = _checked(x, "x", shape), _checked(residual, "residual", shape), _checked(weight, "weight", (d,))
@@ -506,7 +514,7 @@ class AddNorm:
         else:
             raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
         code = (_lib or lib()).moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T,
-                                            d, self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(stream, x))
+                                            d, self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(None, x))
         if code:
             _check(code, "moe_add_norm")
         return y, s_out
@@ -514,11 +522,14 @@ class AddNorm:
     def backward(self, s, weight, dy, ds=None, stream=None):
         """(dx, dweight); dx is the gradient of x and of the residual alike."""
         torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(s, weight, dy, ds)
         _rows(s, "s", self.d)
         if self._workspace is None or self._workspace.device != s.device:
             self._workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
         dx, dweight = torch.empty_like(s), torch.empty_like(weight)
-        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, self._workspace, stream)
+        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, self._workspace)
         return dx, dweight
 
 
@@ -562,6 +573,9 @@ class GatedFfn:
     def forward(self, x, gate_up, down, y=None, pre=None, save=False, stream=None):
         """y, or (y, pre) with ``save`` (pre: the pre-activations that ``backward`` needs)."""
         torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, gate_up, down, y, pre, save)
         d, I, bf16 = self.d, self.inter, torch.bfloat16
         if self.mx:
             rows = x[0] if isinstance(x, (tuple, list)) else x
@@ -583,7 +597,7 @@ class GatedFfn:
         if pre is None and save:
             pre = torch.empty(T, 2 * I, dtype=bf16, device=rows.device)
         pp = _checked(pre, "pre", (T, 2 * I), bf16)
-        code = (_lib or lib()).moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(stream, rows))
+        code = (_lib or lib()).moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(None, rows))
         if code:
             _check(code, "moe_ffn_forward")
         return (y, pre) if pre is not None else y
@@ -591,6 +605,9 @@ class GatedFfn:
     def backward(self, x, pre, gate_up, down, dy, dx=None, dgate_up=None, ddown=None, stream=None):
         """(dx, dgate_up, ddown); pass ``False`` for one of them to leave it out (None comes back)."""
         torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, pre, gate_up, down, dy, dx, dgate_up, ddown)
         d, I, bf16 = self.d, self.inter, torch.bfloat16
         T = _rows(x, "x", d)[0]
         ins = [_checked(x, "x", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16), T,
@@ -601,7 +618,7 @@ class GatedFfn:
             t = None if t is False else torch.empty_like(like) if t is None else t
             outs.append(t)
             ins.append(_checked(t, name, like.shape, bf16))
-        _check(lib().moe_ffn_backward(self.ctx, *ins, _handle(stream, x)), "moe_ffn_backward")
+        _check(lib().moe_ffn_backward(self.ctx, *ins, _handle(None, x)), "moe_ffn_backward")
         return tuple(outs)
 
     def status(self) -> int:

@@ -377,6 +377,42 @@ def test_tensors_at_16_bytes_give_the_same(T):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("what", ["norm", "norm_mx8", "norm_backward", "quantize", "ffn", "ffn_save", "ffn_backward"])
+def test_results_on_another_stream_are_not_in_memory_still_read(what):
+    # A tensor is let go while the present stream has yet to read it: its memory is the present stream's to give out
+    # again, and a call on another stream must not write there now.
+    g = gen(21)
+    T, d, I = 64, 256, 512
+    x, gu, dn, w = normal(g, T, d), normal(g, 2 * I, d, scale=0.06), normal(g, d, I, scale=0.04), normal(g, d)
+    op, ffn = moe.AddNorm(d), moe.GatedFfn(d, I, T, training=True)
+    y, pre = ffn.forward(x, gu, dn, save=True)
+    side = torch.cuda.Stream()
+    call = {"norm": lambda st: op.forward(x, x, w, stream=st),
+            "norm_mx8": lambda st: op.forward(x, None, w, y_dtype=moe.MOE_MX8, stream=st),
+            "norm_backward": lambda st: op.backward(x, w, x, stream=st),
+            "quantize": lambda st: moe.moe_quantize_mx(x, stream=st),
+            "ffn": lambda st: ffn.forward(x, gu, dn, stream=st),
+            "ffn_save": lambda st: ffn.forward(x, gu, dn, save=True, stream=st),
+            "ffn_backward": lambda st: ffn.backward(x, pre, gu, dn, x, stream=st)}[what]
+
+    def flat(r):
+        return [t for q in (r if isinstance(r, tuple) else (r,)) for t in (q if isinstance(q, tuple) else (q,))]
+
+    want = [t.view(torch.uint8).clone() for t in flat(call(None))]
+    old = [torch.full_like(t, 7) for t in want]
+    keep = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # ~50 ms
+    for k, o in zip(keep, old):
+        k.copy_(o)
+    del old, o
+    got = flat(call(side))
+    torch.cuda.synchronize()
+    for k, t, want_t in zip(keep, got, want):
+        assert bool((k == 7).all())
+        assert torch.equal(t.view(torch.uint8), want_t)
+
+
 def test_offsets_past_32_bits():
     # pre has 2.3e9 elements, h 1.15e9
     g = gen(10)
