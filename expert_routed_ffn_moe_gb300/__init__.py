@@ -477,14 +477,12 @@ def moe_add_norm_backward(s, weight, dy, ds, eps, dx, dweight, workspace, stream
 
 
 class AddNorm:
-    """The norm of rows of width ``d`` with the residual's addition; keeps the
-    workspace of the backward pass (two backward calls on one object must not
-    overlap in time)."""
+    """The norm of rows of width ``d`` with the residual's addition.  Holds no
+    device memory: a backward call takes its workspace from its stream's."""
 
     def __init__(self, d, eps=1e-6):
         self.d = d
         self.eps = float(eps)
-        self._workspace = None
 
     def forward(self, x, residual, weight, y_dtype=MOE_BF16, s_out=None, stream=None):
         """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
@@ -526,10 +524,9 @@ class AddNorm:
             with torch.cuda.stream(stream):
                 return self.backward(s, weight, dy, ds)
         _rows(s, "s", self.d)
-        if self._workspace is None or self._workspace.device != s.device:
-            self._workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
+        workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
         dx, dweight = torch.empty_like(s), torch.empty_like(weight)
-        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, self._workspace)
+        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, workspace)
         return dx, dweight
 
 

@@ -413,6 +413,21 @@ def test_results_on_another_stream_are_not_in_memory_still_read(what):
         assert torch.equal(t.view(torch.uint8), want_t)
 
 
+def test_norm_backward_of_one_object_on_two_streams():
+    g = gen(22)
+    T, d = 20000, 1024
+    op, w = moe.AddNorm(d), normal(g, d)
+    s, dy = [normal(g, T, d) for _ in range(2)], normal(g, T, d)
+    want = [op.backward(t, w, dy)[1] for t in s]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):  # the calls overlap
+        got = [op.backward(t, w, dy, stream=st)[1] for t, st in zip(s, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_offsets_past_32_bits():
     # pre has 2.3e9 elements, h 1.15e9
     g = gen(10)
