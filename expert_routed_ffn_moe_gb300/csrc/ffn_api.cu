@@ -238,8 +238,10 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
   auto in = [](const void* p) { return static_cast<const uint16_t*>(p); };
   auto out = [](void* p) { return static_cast<uint16_t*>(p); };
   const FfnBackwardArgs a{in(x), in(pre), in(gate_up), in(down), in(dy), out(dx), out(dgate_up), out(ddown)};
-  cudaError_t err = launch_ffn_grad_h(ctx->eng, s, a, ctx->sc, st);
-  ++ctx->launches;
+  const bool skinny = T <= kSkinnyTokens;
+  cudaError_t err = skinny ? launch_skinny_backward(ctx->eng, s, a, ctx->sc, st)
+                           : launch_ffn_grad_h(ctx->eng, s, a, ctx->sc, st);
+  ctx->launches += skinny && dx ? 2 : 1;
   if (err == cudaSuccess) {
     int n = 0;
     err = launch_ffn_grads(ctx->eng, s, a, ctx->sc, &n, st);

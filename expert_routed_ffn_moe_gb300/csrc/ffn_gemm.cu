@@ -51,7 +51,7 @@
 // What bounds it: large bf16 products the MMAs (the tensor pipe is active 85-88%
 // of a CTA's time) and, run back to back, the card's power: T = 8192, d = 4096,
 // I = 16384 with pre saved, 1.96-2.05 ms, 1.61-1.68 PFLOP/s; the backward call at
-// T = 4096 2.06-2.13 ms.  mx8 at T = 8191 1.2 ms, 2.7 PFLOP/s: a block's data,
+// T = 4096 2.06-2.17 ms.  mx8 at T = 8191 1.2 ms, 2.7 PFLOP/s: a block's data,
 // its scales' copies and the sight of both have to come in time for 512 cycles of
 // MMAs (TMEM has room for four blocks' scales).  Few tiles: the ~1 us that each
 // of a launch's start, first loads, epilogue and end take.
@@ -141,18 +141,6 @@ MOE_DEV void store32(void* to, const uint32_t(&w)[8]) {  // 32-byte aligned
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
-}
-// Shared-memory matrix descriptor of an MN-major bf16 operand, 128-byte swizzle:
-// each k is a 128-byte row of 64 elements along m (or n), 8 k rows make a
-// 1024-byte atom; the next 64 elements along m lie `64 k rows` further.
-MOE_DEV uint64_t desc_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
-  d |= static_cast<uint64_t>((kBK * 128) >> 4) << 16;  // leading: from 64 elements of m to the next 64
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;         // stride: from 8 k rows to the next 8
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
 }
 MOE_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -996,7 +984,8 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBa
 // dx = dpre gate_up (K = 2I), dgate_up = dpre^T x and ddown = dy^T h (K = T).
 // They do not depend on one another: they go into one launch unless splitting
 // each one's few tiles over clusters is the shorter.  That is decided for all
-// three, so that a gradient does not depend on which others are wanted.
+// three, so that a gradient does not depend on which others are wanted.  For few
+// tokens launch_skinny_backward has done dx, and the others have one k block.
 cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
                              int* launches, cudaStream_t st) {
   Product all[3] = {};  // dx, dgate_up, ddown
@@ -1023,6 +1012,8 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   GemmParams p{};
   p.ctl = e.ctl;
   p.early = ch / cl;
+  const bool skinny = s.T <= kSkinnyTokens;
+  if (skinny) all[0].y = nullptr;
   auto add = [&](const Product& q) {
     if (q.y) p.q[p.count++] = q;
   };
@@ -1038,8 +1029,9 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   }
   if (tiles > (1 << 28)) return cudaErrorInvalidValue;
   const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
-  *launches = 1;
-  if (together <= apart) {
+  *launches = p.count ? 1 : 0;
+  if (!p.count) return cudaSuccess;
+  if (skinny || together <= apart) {
     if (p.count > 1) return launch<kEpiStore, true, true, false, 1, true>(p, pairs, st);
     return p.q[0].a_mn ? launch<kEpiStore, true, true, false, 1>(p, pairs, st)
                        : launch<kEpiStore, false, true, false, 1>(p, pairs, st);

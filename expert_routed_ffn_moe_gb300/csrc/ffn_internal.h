@@ -69,6 +69,18 @@ MOE_DEV uint64_t mx_scale_desc(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
          (static_cast<uint64_t>(1) << 46);
 }
+// Shared-memory matrix descriptor of an MN-major bf16 operand, 128-byte swizzle:
+// each of 64 k is a 128-byte row of 64 elements along m (or n), 8 k rows make a
+// 1024-byte atom; the next 64 elements along m lie 64 k rows further.
+MOE_DEV uint64_t desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>((64 * 128) >> 4) << 16;  // leading: from 64 elements of m to the next 64
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;        // stride: from 8 k rows to the next 8
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
 // 16 consecutive fp32 columns of this thread's TMEM lane, valid after tmem_ld_wait().
 MOE_DEV void tmem_ld16_async(uint32_t taddr, float* r) {
   asm volatile(
@@ -266,10 +278,13 @@ cudaError_t launch_ffn_gate_up_mx(const FfnEngine& e, const FfnShape& s, const F
 cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint8_t* hq, const uint8_t* hs,
                                const FfnForwardArgs& a, cudaStream_t st);
 
-// ffn_skinny.cu: the whole forward call for few tokens
+// ffn_skinny.cu: for few tokens the whole forward call, and of the backward call
+// what reads the weights: grad_h and, where it is wanted, dx
 constexpr int kSkinnyTokens = 32;
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);
+cudaError_t launch_skinny_backward(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a,
+                                   const FfnScratch& sc, cudaStream_t st);
 
 }  // namespace moe

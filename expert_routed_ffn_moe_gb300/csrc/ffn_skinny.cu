@@ -1,5 +1,5 @@
-// The gated feed-forward block for few tokens (T <= 32): both products bound by
-// reading the weights once.
+// The gated feed-forward block for few tokens (T <= 32): the products that read
+// the weights, bound by reading them once.
 //
 // The weight rows are the tensor cores' 128 rows and the tokens their N columns
 // (D[row, token] = W x^T, N = T rounded up to 16 or 32), so no MMA work and
@@ -31,6 +31,13 @@
 // weights and only then wait for h.  A gate/up CTA that has asked for its last
 // weights pulls its share of down's into L2, so memory stays busy while the
 // gate/up product is summed up.
+//
+// The backward call's two are the same on the weights transposed, which are read
+// where they lie (64 k rows of 128 neighbouring weight columns, an MN-major A):
+// dh = dy down, whose finish reads pre and leaves dpre and h, and dx = dpre
+// gate_up.  A backward call at T = 16, all three gradients, against these two as
+// products of the pair kernel (us): d = 2048, I = 2048: 27 against 35; d = 1024,
+// I = 2816: 20 against 35; d = 4096, I = 16384: 174 against 225.
 #include "ffn_internal.h"
 
 namespace moe {
@@ -42,30 +49,35 @@ constexpr int kThreads = 320;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 6;
 
+enum { kDown, kGateUp, kGradH, kDx };
+constexpr bool first_of(int kind) { return kind == kGateUp || kind == kGradH; }  // of a call's two kernels
+constexpr bool w_mn(int kind) { return kind >= kGradH; }  // the weights lie [K, rows]
+
 struct SkinnyParams {
-  CUtensorMap w, x;                // weights [rows, K]; x or h [T, K]
-  CUtensorMap next;                // gate/up: the weights of down, [next_rows, next_K]
+  CUtensorMap w, x;                // weights; x, h, dy or dpre [T, K]
+  CUtensorMap next;                // the first kernel: the weights of the second, next_rows x next_K (0: there is none)
   int next_rows, next_K;
   CUtensorMap ws, us, xs;          // mx8 scales: of the rows (gate), of the up rows, of x or h
-  uint16_t *h, *pre, *y;
+  uint16_t *h, *pre, *y;           // y: of down, or dx
+  uint16_t* dpre;
   uint8_t *hq, *hs;
-  int T, N, K;                     // N: neurons (gate/up) or rows of down
+  int T, N, K;                     // N: neurons (gate/up, grad_h) or columns of y
   int act;
   int log_cluster;                 // CTAs per tile: 1 << log_cluster
   DevCtl ctl;
 };
 
 constexpr int stage_bytes(bool mx, int nt) { return kBlockBytes + nt * 128 + (mx ? 1024 : 0); }
-constexpr int exchange_bytes(bool gate, int nt) { return nt * (gate ? 2 : 1) * kRows * 4; }
+constexpr int exchange_bytes(int kind, int nt) { return nt * (kind == kGateUp ? 2 : 1) * kRows * 4; }
 // Stages of the ring.  An even number: the even and the odd steps then have
 // stages of their own, so that each stage's phases are waited for by one thread
 // in their order (a wait by parity for a phase after the next would return at
-// once).  A gate/up and a down CTA fit an SM together.
-constexpr int stages_of(bool gate, int nt) { return gate && nt <= 16 ? 6 : 4; }
+// once).  A CTA of a call's first and one of its second kernel fit an SM together.
+constexpr int stages_of(int kind, int nt) { return first_of(kind) && nt <= 16 ? 6 : 4; }
 // Accumulators; mx8: and 8 columns of scales per stage, so that they are overwritten only when the MMAs that read them
 // are done, like the stage itself.
-constexpr uint32_t tmem_cols(bool mx, bool gate, int nt) {
-  const int need = 2 * nt + (mx ? 8 * stages_of(gate, nt) : 0);
+constexpr uint32_t tmem_cols(bool mx, int kind, int nt) {
+  const int need = 2 * nt + (mx ? 8 * stages_of(kind, nt) : 0);
   return need <= 32 ? 32 : need <= 64 ? 64 : 128;
 }
 
@@ -76,13 +88,15 @@ struct __align__(8) Bars {
   int abort_flag;
   int issued[2][2];  // by the producers of weights and of tokens, of even and odd steps
 };
-constexpr size_t smem_of(bool mx, bool gate, int nt) {
-  return 1024 + (size_t)stages_of(gate, nt) * stage_bytes(mx, nt) + exchange_bytes(gate, nt) + sizeof(Bars);
+constexpr size_t smem_of(bool mx, int kind, int nt) {
+  return 1024 + (size_t)stages_of(kind, nt) * stage_bytes(mx, nt) + exchange_bytes(kind, nt) + sizeof(Bars);
 }
-constexpr bool share_an_sm(bool mx, int nt) {  // 228 KB, 1 KB of it the system's for each CTA
-  return smem_of(mx, true, nt) + smem_of(mx, false, nt) + 2048 <= 228 * 1024;
+constexpr bool share_an_sm(bool mx, int first, int second, int nt) {  // 228 KB, 1 KB of it the system's for each CTA
+  return smem_of(mx, first, nt) + smem_of(mx, second, nt) + 2048 <= 228 * 1024;
 }
-static_assert(share_an_sm(false, 16) && share_an_sm(true, 16) && share_an_sm(false, 32) && share_an_sm(true, 32),
+static_assert(share_an_sm(false, kGateUp, kDown, 16) && share_an_sm(true, kGateUp, kDown, 16) &&
+                  share_an_sm(false, kGateUp, kDown, 32) && share_an_sm(true, kGateUp, kDown, 32) &&
+                  share_an_sm(false, kGradH, kDx, 16) && share_an_sm(false, kGradH, kDx, 32),
               "shared memory");
 
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
@@ -121,11 +135,13 @@ MOE_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const DevCtl& c) 
   return ok;
 }
 
-template <bool MX, bool GATE, int NT>
+template <bool MX, int KIND, int NT>
 __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_constant__ SkinnyParams p) {
-  static_assert(stages_of(GATE, NT) % 2 == 0 && stages_of(GATE, NT) <= kMaxStages, "see stages_of");
-  constexpr int S = stages_of(GATE, NT), kStage = stage_bytes(MX, NT);
-  constexpr uint32_t kCols = tmem_cols(MX, GATE, NT);
+  constexpr bool GATE = KIND == kGateUp, FIRST = first_of(KIND), W_MN = w_mn(KIND);
+  static_assert(stages_of(KIND, NT) % 2 == 0 && stages_of(KIND, NT) <= kMaxStages, "see stages_of");
+  static_assert(!MX || !W_MN, "mx8: forward products only");
+  constexpr int S = stages_of(KIND, NT), kStage = stage_bytes(MX, NT);
+  constexpr uint32_t kCols = tmem_cols(MX, KIND, NT);
   constexpr int kDepth = MX ? 128 : 64;  // values of k per block
   constexpr int kParts = GATE ? 2 : 1;   // weight blocks per k block
   extern __shared__ uint8_t smem_raw[];
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
   uint8_t* xs0 = base + S * kBlockBytes;
   uint8_t* sc0 = xs0 + S * NT * 128;
   float* exchange = reinterpret_cast<float*>(base + S * kStage);
-  Bars* bar = reinterpret_cast<Bars*>(base + S * kStage + exchange_bytes(GATE, NT));
+  Bars* bar = reinterpret_cast<Bars*>(base + S * kStage + exchange_bytes(KIND, NT));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), C = 1 << p.log_cluster;
@@ -175,13 +191,19 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
           if (MX) tma_load_scales(sc0 + st * 1024 + 512, &p.xs, kb, 0, &bar->full[st]);
         } else {
           mbar_expect_tx(&bar->full[st], kBlockBytes + (MX ? 512 : 0));
-          tma_load_2d(base + st * kBlockBytes, &p.w, kb * kDepth, row0 + which * p.N, &bar->full[st], once);
+          uint8_t* w = base + st * kBlockBytes;
+          if (W_MN) {
+            tma_load_2d(w, &p.w, row0, kb * kDepth, &bar->full[st], once);
+            tma_load_2d(w + kBlockBytes / 2, &p.w, row0 + kRows / 2, kb * kDepth, &bar->full[st], once);
+          } else {
+            tma_load_2d(w, &p.w, kb * kDepth, row0 + which * p.N, &bar->full[st], once);
+          }
           if (MX) tma_load_scales(sc0 + st * 1024, which ? &p.us : &p.ws, kb, unit, &bar->full[st]);
         }
       };
-      // gate/up: the kernel before may have written anything; down: only h, so its weights do not wait
-      if (GATE || tokens) asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      // first kernel: the one before may have written anything; second: only its x, so the weights do not wait
+      if (FIRST || tokens) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (FIRST) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       int s = odd;
       for (; s < steps; s += 2) {
         if (s >= S && (!mbar_wait(&bar->empty[s % S], ((s / S) & 1) ^ 1, p.ctl) || aborted(bar))) {
@@ -190,12 +212,19 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
         }
         load(s);
       }
-      if (GATE && !tokens) {
+      if (FIRST && !tokens) {
         const int nkb = (p.next_K + kDepth - 1) / kDepth, blocks = (p.next_rows + kRows - 1) / kRows * nkb;
-        for (int b = 2 * blockIdx.x + odd; b < blocks; b += 2 * gridDim.x)
-          tma_prefetch_2d(&p.next, b % nkb * kDepth, b / nkb * kRows);
+        for (int b = 2 * blockIdx.x + odd; b < blocks; b += 2 * gridDim.x) {
+          const int k = b % nkb * kDepth, row = b / nkb * kRows;
+          if (W_MN) {
+            tma_prefetch_2d(&p.next, row, k);
+            if (row + kRows / 2 < p.next_rows) tma_prefetch_2d(&p.next, row + kRows / 2, k);
+          } else {
+            tma_prefetch_2d(&p.next, k, row);
+          }
+        }
       }
-      if (!GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      if (!FIRST) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       bar->issued[tokens][odd] = s;  // steps odd, odd + 2, ... below s
     }
   } else if (warp == 1 || warp == 9) {
@@ -215,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
           break;
         }
         tc_fence_after();
-        const uint64_t da = umma_desc_sw128(smem_u32(base + st * kBlockBytes));
+        const uint32_t w = smem_u32(base + st * kBlockBytes);
+        const uint64_t da = W_MN ? desc_mn(w) : umma_desc_sw128(w);
         const uint64_t db = umma_desc_sw128(smem_u32(xs0 + st * NT * 128));
         if (MX) {
           const uint32_t ts = tmem + 2 * NT + st * 8, sc = smem_u32(sc0 + st * 1024);
@@ -227,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_bf16(d, da + j * 2, db + j * 2, umma_idesc_bf16(kRows, NT), s > odd || j != 0);
+            umma_bf16(d, da + j * (W_MN ? 128 : 2), db + j * 2, umma_idesc_bf16(kRows, NT) | (W_MN ? 1u << 15 : 0u),
+                      s > odd || j != 0);
         }
         umma_commit(&bar->empty[st]);
       }
@@ -244,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
     const int T = p.T, own = (T + C - 1) >> p.log_cluster;  // tokens per CTA
     const int n = unit * kRows + row;
     const bool in = n < p.N;
-    // The results of n tokens t, t + step, ...: gate (or down) values v, up values u.  No branch between the tokens, so
+    // The results of n tokens t, t + step, ...: values v (gate/up: of the gate), up values u.  No branch between the tokens, so
     // that their activations' latencies overlap.
     auto finish = [&](int t, int step, auto& v, const auto& u) {
       constexpr int n_tok = sizeof(v) / sizeof(float);
@@ -262,7 +293,30 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
           }
         });
       }
-      if (GATE && MX) {
+      if constexpr (KIND == kGradH) {
+        uint16_t g[n_tok], up[n_tok];
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i) {
+          const size_t at = (size_t)(t + i * step) * 2 * p.N + n;
+          const bool is = in && t + i * step < T;
+          g[i] = is ? p.pre[at] : (uint16_t)0;
+          up[i] = is ? p.pre[at + p.N] : (uint16_t)0;
+        }
+        with_act(p.act, [&](auto act) {
+#pragma unroll
+          for (int i = 0; i < n_tok; ++i) {
+            const float uv = __bfloat162float(__ushort_as_bfloat16(up[i]));
+            float a, da;
+            act_and_grad<decltype(act)::value>(__bfloat162float(__ushort_as_bfloat16(g[i])), a, da);
+            const size_t row = t + i * step, at = row * 2 * p.N + n;
+            if (in && row < T) {
+              p.dpre[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i] * uv * da));
+              p.dpre[at + p.N] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i] * a));
+              p.h[row * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(a * uv));
+            }
+          }
+        });
+      } else if (GATE && MX) {
         uint32_t byte[n_tok];  // N is a multiple of 32: the warp's group is all in or all out
 #pragma unroll
         for (int i = 0; i < n_tok; ++i)
@@ -283,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
             out[(size_t)(t + i * step) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
       }
     };
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (long over: the sums contain what the producers waited for)
     bool ok = mbar_wait(&bar->tfull, 0, p.ctl) && !aborted(bar);
     if (!__all_sync(0xffffffffu, ok)) {
       set_abort(bar);
@@ -368,7 +423,7 @@ int cluster_of(int tiles, int KB, int sms) {
   return c;
 }
 
-template <bool MX, bool GATE, int NT>
+template <bool MX, int KIND, int NT>
 cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
   const int depth = MX ? 128 : 64;
   const int tiles = (p.N + kRows - 1) / kRows, C = cluster_of(tiles, (p.K + depth - 1) / depth, e.sms);
@@ -376,7 +431,7 @@ cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * C);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_of(MX, GATE, NT);
+  cfg.dynamicSmemBytes = smem_of(MX, KIND, NT);
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -386,36 +441,36 @@ cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ffn_skinny_kernel<MX, GATE, NT>, p);
+  return cudaLaunchKernelEx(&cfg, ffn_skinny_kernel<MX, KIND, NT>, p);
 }
-template <bool MX, bool GATE>
+template <bool MX, int KIND>
 cudaError_t run_nt(const FfnEngine& e, const SkinnyParams& p, cudaStream_t st) {
-  return p.T <= 16 ? run<MX, GATE, 16>(e, p, st) : run<MX, GATE, 32>(e, p, st);
+  return p.T <= 16 ? run<MX, KIND, 16>(e, p, st) : run<MX, KIND, 32>(e, p, st);
 }
-template <bool MX, bool GATE, int NT>
+template <bool MX, int KIND, int NT>
 cudaError_t prepare() {
-  cudaError_t err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, GATE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem_of(MX, GATE, NT));
+  cudaError_t err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem_of(MX, KIND, NT));
   // the SM keeps all its shared memory open, so that the other kernel's CTA fits beside this one's
   if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, GATE, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    err = cudaFuncSetAttribute(ffn_skinny_kernel<MX, KIND, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
   return err;
 }
-template <bool MX, bool GATE>
+template <bool MX, int KIND>
 cudaError_t prepare_nt() {
-  cudaError_t err = prepare<MX, GATE, 16>();
-  if (err == cudaSuccess) err = prepare<MX, GATE, 32>();
+  cudaError_t err = prepare<MX, KIND, 16>();
+  if (err == cudaSuccess) err = prepare<MX, KIND, 32>();
   return err;
 }
 
 uint32_t token_rows(int T) { return T <= 16 ? 16 : 32; }
 
-SkinnyParams params(const FfnEngine& e, const FfnShape& s, bool gate) {
+SkinnyParams params(const FfnEngine& e, const FfnShape& s, int kind) {
   SkinnyParams p{};
   p.T = s.T;
-  p.N = gate ? s.I : s.d;
-  p.K = gate ? s.d : s.I;
+  p.N = first_of(kind) ? s.I : s.d;
+  p.K = first_of(kind) ? s.d : kind == kDx ? 2 * s.I : s.I;
   p.act = s.act;
   p.ctl = e.ctl;
   return p;
@@ -424,16 +479,18 @@ SkinnyParams params(const FfnEngine& e, const FfnShape& s, bool gate) {
 }  // namespace
 
 cudaError_t prepare_ffn_skinny() {
-  cudaError_t err = prepare_nt<false, false>();
-  if (err == cudaSuccess) err = prepare_nt<false, true>();
-  if (err == cudaSuccess) err = prepare_nt<true, false>();
-  if (err == cudaSuccess) err = prepare_nt<true, true>();
+  cudaError_t err = prepare_nt<false, kDown>();
+  if (err == cudaSuccess) err = prepare_nt<false, kGateUp>();
+  if (err == cudaSuccess) err = prepare_nt<true, kDown>();
+  if (err == cudaSuccess) err = prepare_nt<true, kGateUp>();
+  if (err == cudaSuccess) err = prepare_nt<false, kGradH>();
+  if (err == cudaSuccess) err = prepare_nt<false, kDx>();
   return err;
 }
 
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st) {
-  SkinnyParams g = params(e, s, true), d = params(e, s, false);
+  SkinnyParams g = params(e, s, kGateUp), d = params(e, s, kDown);
   const uint32_t nt = token_rows(s.T);
   bool ok;
   if (mx) {
@@ -459,8 +516,32 @@ cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx
   g.next_rows = s.d;
   g.next_K = s.I;
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t err = mx ? run_nt<true, true>(e, g, st) : run_nt<false, true>(e, g, st);
-  if (err == cudaSuccess) err = mx ? run_nt<true, false>(e, d, st) : run_nt<false, false>(e, d, st);
+  cudaError_t err = mx ? run_nt<true, kGateUp>(e, g, st) : run_nt<false, kGateUp>(e, g, st);
+  if (err == cudaSuccess) err = mx ? run_nt<true, kDown>(e, d, st) : run_nt<false, kDown>(e, d, st);
+  return err;
+}
+
+cudaError_t launch_skinny_backward(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a,
+                                   const FfnScratch& sc, cudaStream_t st) {
+  SkinnyParams g = params(e, s, kGradH), d = params(e, s, kDx);
+  const uint32_t nt = token_rows(s.T);
+  const uint64_t I2 = 2 * (uint64_t)s.I;
+  bool ok = make_bf16_map(e.encode, &g.w, a.down, s.I, s.d, s.I, 64, 64) &&
+            make_bf16_map(e.encode, &g.x, a.dy, s.d, s.T, s.d, 64, nt);
+  if (a.dx) {
+    ok = ok && make_bf16_map(e.encode, &d.w, a.gate_up, s.d, I2, s.d, 64, 64) &&
+         make_bf16_map(e.encode, &d.x, sc.dpre, I2, s.T, I2, 64, nt);
+    g.next = d.w;
+    g.next_rows = d.N;
+    g.next_K = d.K;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  g.pre = const_cast<uint16_t*>(a.pre);  // (read)
+  g.dpre = sc.dpre;
+  g.h = sc.h;
+  d.y = a.dx;
+  cudaError_t err = run_nt<false, kGradH>(e, g, st);
+  if (err == cudaSuccess && a.dx) err = run_nt<false, kDx>(e, d, st);
   return err;
 }
 
