@@ -78,6 +78,7 @@ constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;
 // What a tile costs besides its k blocks, in k blocks (~0.27 us), see split_of(): its start and end; its epilogue by kind
 // (a split divides that too); the exchange of a split.
 constexpr int kTileCost = 6, kSplitCost = 7, kLaunchCost = 8;  // (and of another launch)
+constexpr int kNextTileCost = 6;  // a weight gradient's tile after the pair's first
 constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 1 ? 9 : 16; }
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
@@ -982,10 +983,13 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBa
 }
 
 // dx = dpre gate_up (K = 2I), dgate_up = dpre^T x and ddown = dy^T h (K = T).
-// They do not depend on one another: they go into one launch unless splitting
-// each one's few tiles over clusters is the shorter.  That is decided for all
-// three, so that a gradient does not depend on which others are wanted.  For few
-// tokens launch_skinny_backward has done dx, and the others have one k block.
+// They do not depend on one another: they go into one launch, unless it is
+// shorter to split dx's few tiles over clusters and to launch the other two
+// after it, or to split each.  That is decided for all three, so that a gradient
+// does not depend on which others are wanted.  d = 1024, I = 2816, a call with
+// grad_h: T = 501 in one launch 45.4 us, dx first 39.3; T = 256 each by itself
+// 38.6 us, dx first 33.6.  For few tokens launch_skinny_backward has done dx,
+// and the others have one k block.
 cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
                              int* launches, cudaStream_t st) {
   Product all[3] = {};  // dx, dgate_up, ddown
@@ -995,25 +999,39 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
     return cudaErrorInvalidValue;
   const bool dx_first = all[0].blocks >= all[1].blocks;  // the longer reduction
 
-  // time of one launch, in k blocks: at best even, at worst one light tile more, and no less than the heavy tiles'
-  const int each = kTileCost + epilogue_cost(kEpiStore);
+  // Times in k blocks.  One launch: at best even, at worst one light tile more, and no less than the heavy tiles' (a tile
+  // after a pair's first costs less than kTileCost and its epilogue: they overlap).
+  const int each = kNextTileCost, first = kTileCost + epilogue_cost(kEpiStore) - each;
   const long long weight_tiles = (long long)all[1].tiles + all[2].tiles;
   const long long heavy = dx_first ? all[0].tiles : weight_tiles, light = dx_first ? weight_tiles : all[0].tiles;
   const int ch = (dx_first ? all[0] : all[1]).blocks + each, cl = (dx_first ? all[1] : all[0]).blocks + each;
   double together = (double)(heavy * ch + light * cl) / e.pairs + cl;
   const double least = (double)((heavy + e.pairs - 1) / e.pairs) * ch;
   if (together < least) together = least;
-  double apart = 2 * kLaunchCost, c;
-  for (const Product& q : all) {
-    split_of<kEpiStore, false>(e, q, &c);
-    apart += c;
-  }
+  together += first;
+  double c[3];
+  int split[3];
+  for (int i = 0; i < 3; ++i) split[i] = split_of<kEpiStore, false>(e, all[i], &c[i]);
+  const double weights = (double)((weight_tiles + e.pairs - 1) / e.pairs) * (all[1].blocks + each) + first;
+  // (these estimates are good to about a tenth, and one launch has less to go wrong)
+  const double dx_apart = split[0] == 1 ? 1e30 : 1.12 * (c[0] + kLaunchCost + weights);
+  const double apart = 1.12 * (c[0] + c[1] + c[2] + 2 * kLaunchCost);
+  const bool one = together <= dx_apart && together <= apart, two = !one && dx_apart <= apart;
 
   GemmParams p{};
   p.ctl = e.ctl;
   p.early = ch / cl;
-  const bool skinny = s.T <= kSkinnyTokens;
-  if (skinny) all[0].y = nullptr;
+  *launches = 0;
+  if (s.T <= kSkinnyTokens) {
+    all[0].y = nullptr;
+  } else if (two && all[0].y) {
+    GemmParams dx{};
+    dx.q[0] = all[0];
+    const cudaError_t err = run<kEpiStore, false, true, false>(e, dx, st);
+    if (err != cudaSuccess) return err;
+    *launches = 1;
+    all[0].y = nullptr;
+  }
   auto add = [&](const Product& q) {
     if (q.y) p.q[p.count++] = q;
   };
@@ -1029,14 +1047,14 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   }
   if (tiles > (1 << 28)) return cudaErrorInvalidValue;
   const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
-  *launches = p.count ? 1 : 0;
   if (!p.count) return cudaSuccess;
-  if (skinny || together <= apart) {
+  if (s.T <= kSkinnyTokens || one || two) {
+    ++*launches;
     if (p.count > 1) return launch<kEpiStore, true, true, false, 1, true>(p, pairs, st);
     return p.q[0].a_mn ? launch<kEpiStore, true, true, false, 1>(p, pairs, st)
                        : launch<kEpiStore, false, true, false, 1>(p, pairs, st);
   }
-  *launches = p.count;
+  *launches += p.count;
   cudaError_t err = cudaSuccess;
   for (int i = 0; i < p.count && err == cudaSuccess; ++i) {
     GemmParams one{};
