@@ -204,7 +204,7 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
   }
   if (err != cudaSuccess) return cuda_code(err);
   ctx->launches += 2;
-  if (T <= kSkinnyTokens) {
+  if (few_tokens(s)) {
     err = launch_skinny_forward(ctx->eng, s, mx, a, up_s, sc, st);
   } else if (mx) {
     err = launch_ffn_gate_up_mx(ctx->eng, s, a, up_s, sc.hq, sc.hs, st);
@@ -238,7 +238,7 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
   auto in = [](const void* p) { return static_cast<const uint16_t*>(p); };
   auto out = [](void* p) { return static_cast<uint16_t*>(p); };
   const FfnBackwardArgs a{in(x), in(pre), in(gate_up), in(down), in(dy), out(dx), out(dgate_up), out(ddown)};
-  const bool skinny = T <= kSkinnyTokens;
+  const bool skinny = few_tokens(s);
   cudaError_t err = skinny ? launch_skinny_backward(ctx->eng, s, a, ctx->sc, st)
                            : launch_ffn_grad_h(ctx->eng, s, a, ctx->sc, st);
   ctx->launches += skinny && dx ? 2 : 1;

@@ -1022,7 +1022,8 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   p.ctl = e.ctl;
   p.early = ch / cl;
   *launches = 0;
-  if (s.T <= kSkinnyTokens) {
+  const bool few = few_tokens(s);
+  if (few) {
     all[0].y = nullptr;
   } else if (two && all[0].y) {
     GemmParams dx{};
@@ -1048,7 +1049,7 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   if (tiles > (1 << 28)) return cudaErrorInvalidValue;
   const int pairs = tiles < e.pairs ? (int)tiles : e.pairs;
   if (!p.count) return cudaSuccess;
-  if (s.T <= kSkinnyTokens || one || two) {
+  if (few || one || two) {
     ++*launches;
     if (p.count > 1) return launch<kEpiStore, true, true, false, 1, true>(p, pairs, st);
     return p.q[0].a_mn ? launch<kEpiStore, true, true, false, 1>(p, pairs, st)

@@ -280,7 +280,17 @@ cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint
 
 // ffn_skinny.cu: for few tokens the whole forward call, and of the backward call
 // what reads the weights: grad_h and, where it is wanted, dx
-constexpr int kSkinnyTokens = 32;
+//
+// Up to 32 tokens always; up to 64 where reading the weights is most of the time:
+// with 64 tokens the parts' exchange grows and waits for the ring's memory.
+// Forward call at T = 33 and 64, as a stream against as tiles (us): d = 4096, I =
+// 16384: 84, 87 against 95, 95 (mx8: 52, 56 against 67, 67); d = 4096, I = 4096:
+// 30, 32 against 34, 34; d = 2048, I = 2048: 24, 27 against 21, 21; d = 2048, I =
+// 512: 14, 16 against 17, 17 (backward 20, 22 against 20, 20).
+constexpr int kSkinnyTokens = 64;
+inline bool few_tokens(const FfnShape& s) {
+  return s.T <= 32 || (s.T <= kSkinnyTokens && 3LL * s.d * s.I >= 1LL << 25);
+}
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);

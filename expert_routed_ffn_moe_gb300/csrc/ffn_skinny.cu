@@ -1,8 +1,8 @@
-// The gated feed-forward block for few tokens (T <= 32): the products that read
-// the weights, bound by reading them once.
+// The gated feed-forward block for few tokens (see few_tokens()): the products
+// that read the weights, bound by reading them once.
 //
 // The weight rows are the tensor cores' 128 rows and the tokens their N columns
-// (D[row, token] = W x^T, N = T rounded up to 16 or 32), so no MMA work and
+// (D[row, token] = W x^T, N = T rounded up to 16, 32 or 64), so no MMA work and
 // no shared memory goes to rows that do not exist, and one multiply per weight
 // row block serves every token.  128 x 128-byte weight blocks and the matching x
 // blocks go through a TMA ring.  A thread takes ~0.3 us to wait for a stage and
@@ -78,26 +78,33 @@ constexpr int stages_of(int kind, int nt) { return first_of(kind) && nt <= 16 ? 
 // are done, like the stage itself.
 constexpr uint32_t tmem_cols(bool mx, int kind, int nt) {
   const int need = 2 * nt + (mx ? 8 * stages_of(kind, nt) : 0);
-  return need <= 32 ? 32 : need <= 64 ? 64 : 128;
+  return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
 }
+// With 64 tokens the exchange lies in the ring's memory, so that two CTAs still
+// fit an SM: the cluster's CTAs tell one another when their MMAs are done with it
+// (1 - 1.5 us).
+constexpr bool in_ring(int nt) { return nt > 32; }
 
 struct __align__(8) Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull, mma_done;
   uint64_t parts;  // all parts of this CTA's tokens have been pushed here
+  uint64_t ready;  // in_ring: all of the cluster's CTAs take parts in now
   uint32_t tmem_base;
   int abort_flag;
   int issued[2][2];  // by the producers of weights and of tokens, of even and odd steps
 };
 constexpr size_t smem_of(bool mx, int kind, int nt) {
-  return 1024 + (size_t)stages_of(kind, nt) * stage_bytes(mx, nt) + exchange_bytes(kind, nt) + sizeof(Bars);
+  return 1024 + (size_t)stages_of(kind, nt) * stage_bytes(mx, nt) + (in_ring(nt) ? 0 : exchange_bytes(kind, nt)) +
+         sizeof(Bars);
 }
 constexpr bool share_an_sm(bool mx, int first, int second, int nt) {  // 228 KB, 1 KB of it the system's for each CTA
   return smem_of(mx, first, nt) + smem_of(mx, second, nt) + 2048 <= 228 * 1024;
 }
-static_assert(share_an_sm(false, kGateUp, kDown, 16) && share_an_sm(true, kGateUp, kDown, 16) &&
-                  share_an_sm(false, kGateUp, kDown, 32) && share_an_sm(true, kGateUp, kDown, 32) &&
-                  share_an_sm(false, kGradH, kDx, 16) && share_an_sm(false, kGradH, kDx, 32),
-              "shared memory");
+constexpr bool all_share(int nt) {
+  return share_an_sm(false, kGateUp, kDown, nt) && share_an_sm(true, kGateUp, kDown, nt) &&
+         share_an_sm(false, kGradH, kDx, nt);
+}
+static_assert(all_share(16) && all_share(32) && all_share(64), "shared memory");
 
 MOE_DEV bool aborted(const Bars* b) { return *reinterpret_cast<const volatile int*>(&b->abort_flag) != 0; }
 MOE_DEV void set_abort(Bars* b) { *reinterpret_cast<volatile int*>(&b->abort_flag) = 1; }
@@ -140,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
   constexpr bool GATE = KIND == kGateUp, FIRST = first_of(KIND), W_MN = w_mn(KIND);
   static_assert(stages_of(KIND, NT) % 2 == 0 && stages_of(KIND, NT) <= kMaxStages, "see stages_of");
   static_assert(!MX || !W_MN, "mx8: forward products only");
+  static_assert(!in_ring(NT) || exchange_bytes(KIND, NT) <= stages_of(KIND, NT) * stage_bytes(MX, NT), "the exchange");
   constexpr int S = stages_of(KIND, NT), kStage = stage_bytes(MX, NT);
   constexpr uint32_t kCols = tmem_cols(MX, KIND, NT);
   constexpr int kDepth = MX ? 128 : 64;  // values of k per block
@@ -149,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
   // weight blocks, then x blocks, then scales (1024-byte aligned tiles first), then the exchange
   uint8_t* xs0 = base + S * kBlockBytes;
   uint8_t* sc0 = xs0 + S * NT * 128;
-  float* exchange = reinterpret_cast<float*>(base + S * kStage);
-  Bars* bar = reinterpret_cast<Bars*>(base + S * kStage + exchange_bytes(KIND, NT));
+  float* exchange = reinterpret_cast<float*>(base + (in_ring(NT) ? 0 : S * kStage));
+  Bars* bar = reinterpret_cast<Bars*>(base + S * kStage + (in_ring(NT) ? 0 : exchange_bytes(KIND, NT)));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), C = 1 << p.log_cluster;
@@ -167,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
     mbar_init(&bar->tfull, 2);
     mbar_init(&bar->mma_done, 2);
     mbar_init(&bar->parts, 4 * C);
+    mbar_init(&bar->ready, C);
     bar->abort_flag = 0;
     fence_mbar_init();
   }
@@ -339,6 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
     };
     asm volatile("griddepcontrol.wait;" ::: "memory");  // (long over: the sums contain what the producers waited for)
     bool ok = mbar_wait(&bar->tfull, 0, p.ctl) && !aborted(bar);
+    if (in_ring(NT) && C > 1) {
+      // (all loads of this CTA have landed and been read; one that gives up does not arrive, and then nobody pushes)
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && warp == 2 && lane < C) arrive_cluster(map_cta(&bar->ready, lane));
+      ok = ok && mbar_wait_cluster(&bar->ready, 0, p.ctl);
+    }
     if (!__all_sync(0xffffffffu, ok)) {
       set_abort(bar);
     } else {
@@ -445,7 +460,9 @@ cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
 }
 template <bool MX, int KIND>
 cudaError_t run_nt(const FfnEngine& e, const SkinnyParams& p, cudaStream_t st) {
-  return p.T <= 16 ? run<MX, KIND, 16>(e, p, st) : run<MX, KIND, 32>(e, p, st);
+  return p.T <= 16   ? run<MX, KIND, 16>(e, p, st)
+         : p.T <= 32 ? run<MX, KIND, 32>(e, p, st)
+                     : run<MX, KIND, 64>(e, p, st);
 }
 template <bool MX, int KIND, int NT>
 cudaError_t prepare() {
@@ -461,10 +478,11 @@ template <bool MX, int KIND>
 cudaError_t prepare_nt() {
   cudaError_t err = prepare<MX, KIND, 16>();
   if (err == cudaSuccess) err = prepare<MX, KIND, 32>();
+  if (err == cudaSuccess) err = prepare<MX, KIND, 64>();
   return err;
 }
 
-uint32_t token_rows(int T) { return T <= 16 ? 16 : 32; }
+uint32_t token_rows(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 SkinnyParams params(const FfnEngine& e, const FfnShape& s, int kind) {
   SkinnyParams p{};

@@ -274,6 +274,11 @@ def test_mx8_forward_matches_definition(T, d, I, name):
     near(y, y0, b, "y")
 
 
+@pytest.mark.parametrize("T,d,I", [(33, 4096, 2752), (64, 1056, 10624), (50, 11264, 1024)])
+def test_mx8_few_tokens_and_large_weights(T, d, I):
+    test_mx8_forward_matches_definition(T, d, I, "silu")
+
+
 def test_saturated_activations_stay_finite():
     # gates far outside the range in which exp() is finite, and the ends of bf16
     vals = torch.tensor([-3e38, -1e19, -1e4, -200.0, -90.0, -10.0, -1e-30, 0.0, 1e-30, 10.0, 90.0, 200.0, 1e4],
@@ -443,6 +448,42 @@ def test_offsets_past_32_bits():
     near(pre[rows], pre0, e_pre, "pre")
     near(y[rows], y0, e_y, "y")
     near(dx[rows], *fc.backward(x[rows], pre[rows], gu, dn, dy[rows], False)["dx"], "dx")
+
+
+@pytest.mark.parametrize("d,I", [(1032, 10856), (11200, 1000), (4096, 2752)])
+@pytest.mark.parametrize("T", [33, 47, 64])
+def test_few_tokens_and_large_weights(T, d, I):
+    # weights large enough to be streamed up to 64 tokens; clusters of 1 to 8 CTAs
+    g = gen(T * 7 + d)
+    x, gu, dn, dy = normal(g, T, d), normal(g, 2 * I, d, scale=0.02), normal(g, d, I, scale=0.02), normal(g, T, d)
+    op = moe.GatedFfn(d, I, T, training=True)
+    y, pre = op.forward(x, gu, dn, save=True)
+    pre0, e_pre, y0, e_y = fc.forward(x, gu, dn, False)
+    near(pre, pre0, e_pre, "pre")
+    near(y, y0, e_y, "y")
+    got = op.backward(x, pre, gu, dn, dy)
+    want = fc.backward(x, pre, gu, dn, dy, False)
+    for name, t in zip(("dx", "dgate_up", "ddown"), got):
+        near(t, *want[name], name)
+    assert torch.equal(op.backward(x, pre, gu, dn, dy, None, False, False)[0], got[0])
+    assert op.status() == moe.MOE_OK
+
+
+def test_few_tokens_and_large_weights_wait_that_runs_out():
+    g = gen(31)
+    T, d, I = 40, 4096, 2752
+    x, gu, dn = normal(g, T, d), normal(g, 2 * I, d, scale=0.02), normal(g, d, I, scale=0.02)
+    op = moe.GatedFfn(d, I, T, training=True)
+    want, pre = op.forward(x, gu, dn, save=True)
+    moe.moe_ffn_set_spin_limit(op.ctx, 20_000_000)
+    moe.moe_ffn_inject_stall(op.ctx, True)
+    op.forward(x, gu, dn)
+    assert op.status() == moe.MOE_ERR_TIMEOUT
+    op.backward(x, pre, gu, dn, x)
+    assert op.status() == moe.MOE_ERR_TIMEOUT
+    moe.moe_ffn_inject_stall(op.ctx, False)
+    moe.moe_ffn_set_spin_limit(op.ctx, 0)
+    assert torch.equal(op.forward(x, gu, dn), want) and op.status() == moe.MOE_OK
 
 
 @pytest.mark.parametrize("T", [9, 700])
