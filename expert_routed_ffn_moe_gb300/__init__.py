@@ -483,6 +483,7 @@ class AddNorm:
     def __init__(self, d, eps=1e-6):
         self.d = d
         self.eps = float(eps)
+        self._workspace_bytes = lib().moe_add_norm_workspace(d)
 
     def forward(self, x, residual, weight, y_dtype=MOE_BF16, s_out=None, stream=None):
         """(y, s): y in ``y_dtype`` (MOE_MX8: the pair (codes, scales)), s = x + residual
@@ -523,10 +524,18 @@ class AddNorm:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.backward(s, weight, dy, ds)
-        _rows(s, "s", self.d)
-        workspace = torch.empty(lib().moe_add_norm_workspace(self.d), dtype=torch.uint8, device=s.device)
+        shape = _rows(s, "s", self.d)
+        T, d = shape
+        dtype = s.dtype
+        ps, pw, pdy = _checked(s, "s", shape), _checked(weight, "weight", (d,)), _checked(dy, "dy", shape, dtype)
+        pds = _checked(ds, "ds", shape, dtype)
         dx, dweight = torch.empty_like(s), torch.empty_like(weight)
-        moe_add_norm_backward(s, weight, dy, ds, self.eps, dx, dweight, workspace)
+        workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=s.device)
+        code = (_lib or lib()).moe_add_norm_backward(ps, pw, pdy, pds, _DTYPES[dtype], _DTYPES[weight.dtype], T, d,
+                                                     self.eps, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
+                                                     _handle(None, s))
+        if code:
+            _check(code, "moe_add_norm_backward")
         return dx, dweight
 
 
