@@ -616,16 +616,23 @@ class GatedFfn:
                 return self.backward(x, pre, gate_up, down, dy, dx, dgate_up, ddown)
         d, I, bf16 = self.d, self.inter, torch.bfloat16
         T = _rows(x, "x", d)[0]
-        ins = [_checked(x, "x", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16), T,
-               _checked(gate_up, "gate_up", (2 * I, d), bf16), _checked(down, "down", (d, I), bf16),
-               _checked(dy, "dy", (T, d), bf16)]
-        outs = []
-        for name, t, like in (("dx", dx, x), ("dgate_up", dgate_up, gate_up), ("ddown", ddown, down)):
-            t = None if t is False else torch.empty_like(like) if t is None else t
-            outs.append(t)
-            ins.append(_checked(t, name, like.shape, bf16))
-        _check(lib().moe_ffn_backward(self.ctx, *ins, _handle(None, x)), "moe_ffn_backward")
-        return tuple(outs)
+        px, ppre, pdy = _checked(x, "x", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16), \
+            _checked(dy, "dy", (T, d), bf16)
+        pg, pd = _checked(gate_up, "gate_up", (2 * I, d), bf16), _checked(down, "down", (d, I), bf16)
+
+        def output(t, name, like):
+            if t is None:
+                t = torch.empty_like(like)
+                return t, t.data_ptr()
+            return (None, None) if t is False else (t, _checked(t, name, like.shape, bf16))
+
+        dx, pdx = output(dx, "dx", x)
+        dgate_up, pdg = output(dgate_up, "dgate_up", gate_up)
+        ddown, pdd = output(ddown, "ddown", down)
+        code = (_lib or lib()).moe_ffn_backward(self.ctx, px, ppre, T, pg, pd, pdy, pdx, pdg, pdd, _handle(None, x))
+        if code:
+            _check(code, "moe_ffn_backward")
+        return dx, dgate_up, ddown
 
     def status(self) -> int:
         return moe_ffn_status(self.ctx)
