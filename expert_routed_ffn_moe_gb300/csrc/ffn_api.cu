@@ -73,8 +73,8 @@ int moe_add_norm_backward(const void* s, const void* weight, const void* dy, con
                           int T, int d, float eps, void* dx, void* dweight, void* workspace, void* stream) {
   if (T < 0 || d <= 0 || !stream_dtype(dtype) || !stream_dtype(w_dtype) || !(eps >= 0.f)) return MOE_ERR_ARG;
   if (d > kMaxNormWidth || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
-  if (!dx && !dweight) return MOE_ERR_ARG;
-  if (T > 0 && (!s || !weight || !dy || (dweight && !workspace))) return MOE_ERR_ARG;
+  // (without rows dx is a tensor of no values, which may have no address)
+  if (T > 0 && ((!dx && !dweight) || !s || !weight || !dy || (dweight && !workspace))) return MOE_ERR_ARG;
   if (!aligned16(s) || !aligned16(weight) || !aligned16(dy) || !aligned16(ds) || !aligned16(dx) ||
       !aligned16(dweight) || !aligned16(workspace))
     return MOE_ERR_ALIGN;
@@ -221,8 +221,8 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
   if (!ctx || T < 0 || T > ctx->cfg.max_tokens) return MOE_ERR_ARG;
   const moe_ffn_config& c = ctx->cfg;
   if (!c.training) return MOE_ERR_UNSUPPORTED;
-  if (!dx && !dgate_up && !ddown) return MOE_ERR_ARG;
-  if (T > 0 && (!pre || !down || !dy || (dx && !gate_up) || (dgate_up && !x))) return MOE_ERR_ARG;
+  if (T > 0 && ((!dx && !dgate_up && !ddown) || !pre || !down || !dy || (dx && !gate_up) || (dgate_up && !x)))
+    return MOE_ERR_ARG;
   for (const void* p : {x, pre, gate_up, down, dy, (const void*)dx, (const void*)dgate_up, (const void*)ddown})
     if (!aligned16(p)) return MOE_ERR_ALIGN;
   const NvtxRange range("moe_ffn_backward");

@@ -336,7 +336,7 @@ long long moe_add_norm_workspace(int d);
  * s, dy, ds [T, d] and dx [T, d] have `dtype`; ds is the gradient that reaches s
  * by the residual path (NULL: none), and dx is the gradient of x and of the
  * residual alike.  weight and dweight [d] have w_dtype.  dx or dweight may be
- * NULL to skip it; dx may be dy or ds.  workspace: moe_add_norm_workspace(d)
+ * NULL to skip it (with T > 0 not both); dx may be dy or ds.  workspace: moe_add_norm_workspace(d)
  * bytes, needed for dweight; calls that overlap in time need one each.  The
  * result does not depend on timing.  T == 0 sets dweight to 0.  Limits of d and T
  * as above. */
@@ -385,7 +385,7 @@ int moe_ffn_forward(moe_ffn* ctx, const void* x, const void* x_scales, int T, co
  *   dgate_up = dpre^T x,  ddown = dy^T (act(g) * u).
  * x, pre and the weights are those of the forward call, dy [T, d].  Any of dx
  * [T, d], dgate_up [2I, d], ddown [d, I] may be NULL to skip it, which does not
- * change the others.  Sums are fp32;
+ * change the others (with T > 0 not all three).  Sums are fp32;
  * dpre and act(g) * u are held in bf16 between the products.  T == 0 sets
  * dgate_up and ddown to 0.  MOE_ERR_UNSUPPORTED without cfg.training. */
 int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const void* gate_up, const void* down,
