@@ -348,6 +348,10 @@ class MoeLayer:
 # read without making a stream object.  Calls that make tensors make them as the
 # given stream's: with memory of the present stream a call on another one could
 # write what kernels on the present one still read.
+#
+# A call is launched on the current device.  Its tensors, its stream and its
+# context must be of that device: anything else would hand a kernel addresses of
+# another device's memory.
 _torch = None
 _DTYPES = {}  # torch dtype -> MOE_F32 / MOE_BF16
 
@@ -362,19 +366,37 @@ def _t():
     return _torch
 
 
-def _handle(stream, t):
-    return _torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _device(t, name, home=None):
+    """The index of the current device, after the check that t and the context (made on ``home``) are of it."""
+    device = t.get_device()
+    if device < 0:  # (the host's)
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device != _torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on device {device}, but the current device is {_torch._C._cuda_getDevice()}")
+    if home is not None and home != device:
+        raise ValueError(f"the context was made on device {home}, but the current device is {device}")
+    return device
 
 
-def _checked(t, name, shape, dtype=None):
+def _handle(stream, device):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is of device {stream.device_index}, but the current device is {device}")
+    return stream.cuda_stream
+
+
+def _checked(t, name, shape, device, dtype=None):
     """t's address, after the checks; None for None.  Without ``dtype`` t is float32 or bfloat16."""
     if t is None:
         return None
-    if t.is_cuda and t.shape == shape and (t.dtype in _DTYPES if dtype is None else t.dtype is dtype) and \
-            t.is_contiguous():
+    if t.get_device() == device and t.shape == shape and (t.dtype in _DTYPES if dtype is None else t.dtype is dtype) \
+            and t.is_contiguous():  # (a tensor of the host has device -1)
         return t.data_ptr()
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, but the current device is {device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be {'float32 or bfloat16' if dtype is None else dtype}, got {t.dtype}")
@@ -398,13 +420,16 @@ def moe_mx_scale_bytes(rows: int, cols: int) -> int:
     return lib().moe_mx_scale_bytes(rows, cols)
 
 
-def _mx_checked(pair, name, rows, cols):
+def _mx_checked(pair, name, rows, cols, device):
     """Addresses of the codes and scales of an mx8 matrix, after the checks."""
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise ValueError(f"{name} must be a pair (codes, scales)")
     codes, scales = pair
     if not (codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name} codes and scales must be contiguous CUDA tensors")
+    if codes.get_device() != device or scales.get_device() != device:
+        raise ValueError(f"{name} codes and scales are on devices {codes.get_device()} and {scales.get_device()}, but "
+                         f"the current device is {device}")
     if codes.dtype != _t().float8_e4m3fn and codes.dtype != _torch.uint8:
         raise ValueError(f"{name} codes must be float8_e4m3fn or uint8, got {codes.dtype}")
     if codes.shape != (rows, cols):
@@ -427,11 +452,12 @@ def moe_quantize_mx(v, codes=None, scales=None, stream=None):
         with torch.cuda.stream(stream):
             return moe_quantize_mx(v, codes, scales)
     rows, cols = _rows(v, "v")
-    pv = _checked(v, "v", v.shape)
+    device = _device(v, "v")
+    pv = _checked(v, "v", v.shape, device)
     if codes is None or scales is None:
         codes, scales = _mx_empty(rows, cols, v.device)
-    pc, ps = _mx_checked((codes, scales), "output", rows, cols)
-    _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(None, v)), "moe_quantize_mx")
+    pc, ps = _mx_checked((codes, scales), "output", rows, cols, device)
+    _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(None, device)), "moe_quantize_mx")
     return codes, scales
 
 
@@ -440,20 +466,21 @@ def moe_add_norm(x, residual, weight, eps, s_out, y, y_scales=None, stream=None)
     torch = _t()
     shape = _rows(x, "x")
     T, d = shape
-    px, pr = _checked(x, "x", shape), _checked(residual, "residual", shape)
-    ps = _checked(s_out, "s_out", shape, None if residual is None else residual.dtype)
-    pw = _checked(weight, "weight", (d,))
+    device = _device(x, "x")
+    px, pr = _checked(x, "x", shape, device), _checked(residual, "residual", shape, device)
+    ps = _checked(s_out, "s_out", shape, device, None if residual is None else residual.dtype)
+    pw = _checked(weight, "weight", (d,), device)
     if y.dtype == torch.float8_e4m3fn:
         if y_scales is None:
             raise ValueError("y_scales are needed for float8_e4m3fn codes")
-        py, pys = _mx_checked((y, y_scales), "y", T, d)
+        py, pys = _mx_checked((y, y_scales), "y", T, d, device)
         y_dtype = MOE_MX8
     else:
-        py, pys = _checked(y, "y", shape), None if y_scales is None else y_scales.data_ptr()
+        py, pys = _checked(y, "y", shape, device), None if y_scales is None else y_scales.data_ptr()
         y_dtype = _DTYPES[y.dtype]
     s_like = residual if residual is not None else s_out
     _check(lib().moe_add_norm(px, _DTYPES[x.dtype], pr, MOE_F32 if s_like is None else _DTYPES[s_like.dtype], pw,
-                              _DTYPES[weight.dtype], T, d, eps, ps, py, y_dtype, pys, _handle(stream, x)),
+                              _DTYPES[weight.dtype], T, d, eps, ps, py, y_dtype, pys, _handle(stream, device)),
            "moe_add_norm")
 
 
@@ -462,18 +489,21 @@ def moe_add_norm_backward(s, weight, dy, ds, eps, dx, dweight, workspace, stream
     _t()
     shape = _rows(s, "s")
     T, d = shape
-    ps, pw = _checked(s, "s", shape), _checked(weight, "weight", (d,))
-    pdy, pds, pdx = (_checked(t, n, shape, s.dtype) for n, t in (("dy", dy), ("ds", ds), ("dx", dx)))
-    pdw = _checked(dweight, "dweight", (d,), weight.dtype)
+    device = _device(s, "s")
+    ps, pw = _checked(s, "s", shape, device), _checked(weight, "weight", (d,), device)
+    pdy, pds, pdx = (_checked(t, n, shape, device, s.dtype) for n, t in (("dy", dy), ("ds", ds), ("dx", dx)))
+    pdw = _checked(dweight, "dweight", (d,), device, weight.dtype)
     pws = None
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.get_device() != device:
+            raise ValueError(f"workspace is on device {workspace.get_device()}, but the current device is {device}")
         if workspace.numel() * workspace.element_size() < lib().moe_add_norm_workspace(d):
             raise ValueError("workspace is smaller than moe_add_norm_workspace(d) bytes")
         pws = workspace.data_ptr()
     _check(lib().moe_add_norm_backward(ps, pw, pdy, pds, _DTYPES[s.dtype], _DTYPES[weight.dtype], T, d, eps, pdx, pdw,
-                                       pws, _handle(stream, s)), "moe_add_norm_backward")
+                                       pws, _handle(stream, device)), "moe_add_norm_backward")
 
 
 class AddNorm:
@@ -494,12 +524,14 @@ class AddNorm:
                 return self.forward(x, residual, weight, y_dtype, s_out)
         shape = _rows(x, "x", self.d)
         T, d = shape
-        px, pr, pw = _checked(x, "x", shape), _checked(residual, "residual", shape), _checked(weight, "weight", (d,))
+        device = _device(x, "x")
+        px, pr, pw = _checked(x, "x", shape, device), _checked(residual, "residual", shape, device), \
+            _checked(weight, "weight", (d,), device)
         like = x if residual is None else residual
         if s_out is None:
             s_out = torch.empty_like(like)
         else:
-            _checked(s_out, "s_out", shape, like.dtype)
+            _checked(s_out, "s_out", shape, device, like.dtype)
         pys = None
         if y_dtype == MOE_BF16:
             y = torch.empty_like(x, dtype=torch.bfloat16)
@@ -513,7 +545,7 @@ class AddNorm:
         else:
             raise ValueError("y_dtype must be MOE_F32, MOE_BF16 or MOE_MX8")
         code = (_lib or lib()).moe_add_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, _DTYPES[weight.dtype], T,
-                                            d, self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(None, x))
+                                            d, self.eps, s_out.data_ptr(), py, y_dtype, pys, _handle(None, device))
         if code:
             _check(code, "moe_add_norm")
         return y, s_out
@@ -527,13 +559,15 @@ class AddNorm:
         shape = _rows(s, "s", self.d)
         T, d = shape
         dtype = s.dtype
-        ps, pw, pdy = _checked(s, "s", shape), _checked(weight, "weight", (d,)), _checked(dy, "dy", shape, dtype)
-        pds = _checked(ds, "ds", shape, dtype)
+        device = _device(s, "s")
+        ps, pw, pdy = _checked(s, "s", shape, device), _checked(weight, "weight", (d,), device), \
+            _checked(dy, "dy", shape, device, dtype)
+        pds = _checked(ds, "ds", shape, device, dtype)
         dx, dweight = torch.empty_like(s), torch.empty_like(weight)
         workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=s.device)
         code = (_lib or lib()).moe_add_norm_backward(ps, pw, pdy, pds, _DTYPES[dtype], _DTYPES[weight.dtype], T, d,
                                                      self.eps, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
-                                                     _handle(None, s))
+                                                     _handle(None, device))
         if code:
             _check(code, "moe_add_norm_backward")
         return dx, dweight
@@ -575,6 +609,7 @@ class GatedFfn:
         self.ctx = None
         self.d, self.inter, self.mx = d, inter, weight_format == MOE_W_MX8
         self.ctx = moe_ffn_init(d, inter, max_tokens, activation, weight_format, training)
+        self.device = _t().cuda.current_device()
 
     def forward(self, x, gate_up, down, y=None, pre=None, save=False, stream=None):
         """y, or (y, pre) with ``save`` (pre: the pre-activations that ``backward`` needs)."""
@@ -586,24 +621,26 @@ class GatedFfn:
         if self.mx:
             rows = x[0] if isinstance(x, (tuple, list)) else x
             T = _rows(rows, "x", d)[0]
-            px, pxs = _mx_checked(x, "x", T, d)
-            pg, pgs = _mx_checked(gate_up, "gate_up", 2 * I, d)
-            pd, pds = _mx_checked(down, "down", d, I)
+            device = _device(rows, "x", self.device)
+            px, pxs = _mx_checked(x, "x", T, d, device)
+            pg, pgs = _mx_checked(gate_up, "gate_up", 2 * I, d, device)
+            pd, pds = _mx_checked(down, "down", d, I, device)
         else:
             rows = x
             T = _rows(x, "x", d)[0]
-            px, pg, pd = _checked(x, "x", (T, d), bf16), _checked(gate_up, "gate_up", (2 * I, d), bf16), \
-                _checked(down, "down", (d, I), bf16)
+            device = _device(x, "x", self.device)
+            px, pg, pd = _checked(x, "x", (T, d), device, bf16), \
+                _checked(gate_up, "gate_up", (2 * I, d), device, bf16), _checked(down, "down", (d, I), device, bf16)
             pxs = pgs = pds = None
         if y is None:
             y = torch.empty_like(rows, dtype=bf16) if self.mx else torch.empty_like(x)
             py = y.data_ptr()
         else:
-            py = _checked(y, "y", (T, d), bf16)
+            py = _checked(y, "y", (T, d), device, bf16)
         if pre is None and save:
             pre = torch.empty(T, 2 * I, dtype=bf16, device=rows.device)
-        pp = _checked(pre, "pre", (T, 2 * I), bf16)
-        code = (_lib or lib()).moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(None, rows))
+        pp = _checked(pre, "pre", (T, 2 * I), device, bf16)
+        code = (_lib or lib()).moe_ffn_forward(self.ctx, px, pxs, T, pg, pgs, pd, pds, py, pp, _handle(None, device))
         if code:
             _check(code, "moe_ffn_forward")
         return (y, pre) if pre is not None else y
@@ -616,20 +653,22 @@ class GatedFfn:
                 return self.backward(x, pre, gate_up, down, dy, dx, dgate_up, ddown)
         d, I, bf16 = self.d, self.inter, torch.bfloat16
         T = _rows(x, "x", d)[0]
-        px, ppre, pdy = _checked(x, "x", (T, d), bf16), _checked(pre, "pre", (T, 2 * I), bf16), \
-            _checked(dy, "dy", (T, d), bf16)
-        pg, pd = _checked(gate_up, "gate_up", (2 * I, d), bf16), _checked(down, "down", (d, I), bf16)
+        device = _device(x, "x", self.device)
+        px, ppre, pdy = _checked(x, "x", (T, d), device, bf16), _checked(pre, "pre", (T, 2 * I), device, bf16), \
+            _checked(dy, "dy", (T, d), device, bf16)
+        pg, pd = _checked(gate_up, "gate_up", (2 * I, d), device, bf16), _checked(down, "down", (d, I), device, bf16)
 
         def output(t, name, like):
             if t is None:
                 t = torch.empty_like(like)
                 return t, t.data_ptr()
-            return (None, None) if t is False else (t, _checked(t, name, like.shape, bf16))
+            return (None, None) if t is False else (t, _checked(t, name, like.shape, device, bf16))
 
         dx, pdx = output(dx, "dx", x)
         dgate_up, pdg = output(dgate_up, "dgate_up", gate_up)
         ddown, pdd = output(ddown, "ddown", down)
-        code = (_lib or lib()).moe_ffn_backward(self.ctx, px, ppre, T, pg, pd, pdy, pdx, pdg, pdd, _handle(None, x))
+        code = (_lib or lib()).moe_ffn_backward(self.ctx, px, ppre, T, pg, pd, pdy, pdx, pdg, pdd,
+                                                _handle(None, device))
         if code:
             _check(code, "moe_ffn_backward")
         return dx, dgate_up, ddown
