@@ -503,15 +503,26 @@ int resident_blocks(K kernel, int block, size_t smem) {
   return sms * per;
 }
 
+// Shared memory of the kernels for rows of width d (the weight, and the gradient's `copies`; see OddRow), and of the
+// widest rows that R threads of C chunks take.
+constexpr size_t odd_bytes(int d, int copies) { return (size_t)(d + 7) / 8 * 8 * 4 * copies + 4; }
+constexpr int widest(int R, int C) { return R * C * 8 < kMaxNormWidth ? R * C * 8 : kMaxNormWidth; }
+// A kernel's limit on shared memory belongs to all its launches, which threads of the host may issue side by side: it
+// is set for the widest rows, never lower for narrower ones.
+template <typename K>
+cudaError_t allow(K kernel, size_t smem, size_t most) {
+  return smem <= 48 * 1024
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 template <typename XT, typename ST, int R, int C, bool ODD>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
   constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
   const auto kernel = norm_kernel<XT, ST, R, C, ODD>;
-  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 + 4 : 0;  // (see OddRow)
-  if (smem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-  }
+  const size_t smem = ODD ? odd_bytes(a.d, 1) : 0;
+  const cudaError_t err = allow(kernel, smem, odd_bytes(widest(R, C), 1));
+  if (err != cudaSuccess) return err;
   const int rows = a.y_dtype == MOE_MX8 ? (a.T + 127) / 128 * 128 : a.T;
   int grid = (rows + kRows - 1) / kRows;
   // (a grid of fewer blocks than SMs needs no look at what is resident; without the weight in shared memory the answer
@@ -551,11 +562,9 @@ template <typename ST, int R, int C, bool ODD>
 cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
   constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
   const auto kernel = norm_grad_kernel<ST, R, C, ODD>;
-  const size_t smem = ODD ? (size_t)(a.d + 7) / 8 * 8 * 4 * (1 + kRows) + 4 : R == 32 ? (size_t)a.d * 4 * kRows : 0;
-  if (smem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-  }
+  const size_t smem = ODD ? odd_bytes(a.d, 1 + kRows) : R == 32 ? (size_t)a.d * 4 * kRows : 0;
+  const cudaError_t err = allow(kernel, smem, odd_bytes(widest(R, C), 1 + kRows));
+  if (err != cudaSuccess) return err;
   int grid = (a.T + kRows - 1) / kRows;
   if (grid > 128) {
     int most;

@@ -1,4 +1,6 @@
 """Calls of the feed-forward block and the norm in unusual order or company."""
+import threading
+
 import pytest
 import torch
 
@@ -36,3 +38,33 @@ def test_functions_take_a_stream():
     torch.cuda.synchronize()
     for a, b in zip((y, s, dx, dw), (y0, s0, dx0, dw0)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("what,widths", [("forward", (12301, 16301)), ("backward", (6201, 8001))])
+def test_widths_of_one_kernel_from_several_threads(what, widths):
+    # both widths of a pair run on the same kernel and need different amounts of shared memory, above 48 KB
+    g = gen(41)
+    failed, rounds = [], 1500
+
+    def work(d):
+        try:
+            op, st = moe.AddNorm(d), torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                x, w = normal(g, 3, d), normal(g, d)
+                call = (lambda: op.forward(x, x, w)) if what == "forward" else (lambda: op.backward(x, w, x))
+                want = [t.clone() for t in call()]
+                start.wait()
+                for _ in range(rounds):
+                    got = call()
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+        except Exception as e:
+            failed.append(repr(e))
+            start.abort()
+
+    start = threading.Barrier(len(widths))
+    threads = [threading.Thread(target=work, args=(d,)) for d in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
