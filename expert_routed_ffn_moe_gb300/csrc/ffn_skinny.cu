@@ -215,6 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
       if (FIRST) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       int s = odd;
       for (; s < steps; s += 2) {
+        // (the second kernel's weights: the ring is full until h is there, and a wait's limit is not for the first kernel)
+        if (!FIRST && s == S + odd) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (s >= S && (!mbar_wait(&bar->empty[s % S], ((s / S) & 1) ^ 1, p.ctl) || aborted(bar))) {
           set_abort(bar);
           break;
@@ -240,6 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
     if (lane == 0) {
       const int odd = warp == 9 ? 1 : 0;
       bool ok = true;
+      // Waits' limits are for what this kernel does: they begin when the kernel before has ended.
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       if (p.ctl.stall && !mbar_wait(&bar->mma_done, 0, p.ctl)) {  // test hook: nothing arrives there before the end
         set_abort(bar);
         ok = false;

@@ -396,7 +396,8 @@ long long moe_ffn_launch_count(moe_ffn* ctx);
 
 /* As moe_set_spin_limit and moe_inject_stall, for a moe_ffn context (the thread
  * that issues a product's matrix instructions waits for what never happens; calls
- * whose products run without tensor cores do not wait). */
+ * whose products run without tensor cores do not wait).  A limit does not count
+ * the time that a kernel waits for the one before it on the stream. */
 int moe_ffn_set_spin_limit(moe_ffn* ctx, long long limit);
 int moe_ffn_inject_stall(moe_ffn* ctx, int on);
 

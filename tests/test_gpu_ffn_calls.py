@@ -68,3 +68,43 @@ def test_widths_of_one_kernel_from_several_threads(what, widths):
     for t in threads:
         t.join()
     assert not failed
+
+
+@pytest.mark.parametrize("T", [1, 24])
+def test_wait_limit_does_not_count_the_kernel_before(T):
+    # The block before ends with one long tile on a few SMs (8 columns, 2^20 neurons: ~1 ms) and lets what follows
+    # start beside it; the limit is far above what the small block itself takes and below that.
+    g = gen(43)
+    long_d, long_I, d, I = 8, 1 << 20, 256, 512
+    slow = moe.GatedFfn(long_d, long_I, 100, training=True)
+    a = normal(g, 100, long_d), normal(g, 2 * long_I, long_d), normal(g, long_d, long_I, scale=2.0 ** -10)
+    ffn = moe.GatedFfn(d, I, T, training=True)
+    x, dy = normal(g, T, d), normal(g, T, d)
+    gu, dn = normal(g, 2 * I, d, scale=0.06), normal(g, d, I, scale=0.04)
+    want, pre = ffn.forward(x, gu, dn, save=True)
+    grads = ffn.backward(x, pre, gu, dn, dy)
+    y = torch.empty_like(want)
+    outs = [torch.empty_like(t) for t in grads]
+    slow_y = torch.empty_like(a[0])
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    slow.forward(*a, y=slow_y)
+    torch.cuda.synchronize()
+    begin.record()
+    slow.forward(*a, y=slow_y)
+    end.record()
+    torch.cuda.synchronize()
+    took = begin.elapsed_time(end)
+    assert took > 0.6, f"the block before took {took} ms"
+    moe.moe_ffn_set_spin_limit(ffn.ctx, 200_000)
+    for _ in range(3):
+        y.zero_()
+        torch.cuda.synchronize()
+        slow.forward(*a, y=slow_y)
+        ffn.forward(x, gu, dn, y=y)
+        assert ffn.status() == moe.MOE_OK
+        assert torch.equal(y, want)
+        slow.forward(*a, y=slow_y)
+        ffn.backward(x, pre, gu, dn, dy, *outs)
+        assert ffn.status() == moe.MOE_OK
+        assert all(torch.equal(p, q) for p, q in zip(outs, grads))
+    assert slow.status() == moe.MOE_OK
