@@ -446,7 +446,7 @@ def _mx_empty(rows, cols, device):
 
 
 def moe_quantize_mx(v, codes=None, scales=None, stream=None):
-    """Round a float32 or bfloat16 matrix to mx8: (codes, scales); see moe.h."""
+    """Round a float32 or bfloat16 matrix to mx8: (codes, scales), into the given ones; see moe.h."""
     torch = _t()
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -454,8 +454,10 @@ def moe_quantize_mx(v, codes=None, scales=None, stream=None):
     rows, cols = _rows(v, "v")
     device = _device(v, "v")
     pv = _checked(v, "v", v.shape, device)
-    if codes is None or scales is None:
-        codes, scales = _mx_empty(rows, cols, v.device)
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=v.device)
+    if scales is None:
+        scales = torch.empty(_mx_bytes(rows, cols), dtype=torch.uint8, device=v.device)
     pc, ps = _mx_checked((codes, scales), "output", rows, cols, device)
     _check(lib().moe_quantize_mx(pv, _DTYPES[v.dtype], rows, cols, pc, ps, _handle(None, device)), "moe_quantize_mx")
     return codes, scales

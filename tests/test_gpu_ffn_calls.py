@@ -70,6 +70,17 @@ def test_widths_of_one_kernel_from_several_threads(what, widths):
     assert not failed
 
 
+@pytest.mark.parametrize("rows,cols", [(5, 64), (130, 160)])
+def test_quantize_into_one_given_output(rows, cols):
+    v = normal(gen(42), rows, cols)
+    codes, scales = moe.moe_quantize_mx(v)
+    c, s = torch.zeros_like(codes), torch.zeros_like(scales)
+    got = moe.moe_quantize_mx(v, codes=c)
+    assert got[0] is c and torch.equal(c.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(got[1], scales)
+    got = moe.moe_quantize_mx(v, scales=s)
+    assert got[1] is s and torch.equal(s, scales) and torch.equal(got[0].view(torch.uint8), codes.view(torch.uint8))
+
+
 @pytest.mark.parametrize("T", [1, 24])
 def test_wait_limit_does_not_count_the_kernel_before(T):
     # The block before ends with one long tile on a few SMs (8 columns, 2^20 neurons: ~1 ms) and lets what follows
