@@ -46,8 +46,9 @@ def train(d, inter, tokens, steps, lr=2.0, seed=0):
         for k, g in (("norm", dnorm), ("gate_up", dgate_up), ("down", ddown)):
             master[k] -= lr / d * g.float()
             w[k] = master[k].to(torch.bfloat16)
-    if ffn.status() != moe.MOE_OK:
-        raise RuntimeError(moe.moe_strerror(ffn.status()))
+    status = ffn.status()  # (read once: that clears it)
+    if status != moe.MOE_OK:
+        raise RuntimeError(moe.moe_strerror(status))
     return [float(v) for v in losses], w
 
 

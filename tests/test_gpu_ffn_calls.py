@@ -1,4 +1,6 @@
 """Calls of the feed-forward block and the norm in unusual order or company."""
+import importlib.util
+import os
 import threading
 
 import pytest
@@ -79,6 +81,17 @@ def test_quantize_into_one_given_output(rows, cols):
     assert got[0] is c and torch.equal(c.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(got[1], scales)
     got = moe.moe_quantize_mx(v, scales=s)
     assert got[1] is s and torch.equal(s, scales) and torch.equal(got[0].view(torch.uint8), codes.view(torch.uint8))
+
+
+def test_example_names_a_wait_that_ran_out(monkeypatch):
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "dense_block.py")
+    spec = importlib.util.spec_from_file_location("dense_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    left = [moe.MOE_ERR_TIMEOUT]  # (reading the status clears it)
+    monkeypatch.setattr(moe.GatedFfn, "status", lambda self: left.pop() if left else moe.MOE_OK)
+    with pytest.raises(RuntimeError, match=moe.moe_strerror(moe.MOE_ERR_TIMEOUT)):
+        ex.train(64, 64, 8, 1)
 
 
 @pytest.mark.parametrize("T", [1, 24])
