@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import expert_routed_ffn_moe_gb300 as moe
-from test_gpu_ffn import BF, gen, normal
+import ffn_case as fc
+from test_gpu_ffn import BF, gen, near, norm_bound, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +133,125 @@ def test_wait_limit_does_not_count_the_kernel_before(T):
         assert ffn.status() == moe.MOE_OK
         assert all(torch.equal(p, q) for p, q in zip(outs, grads))
     assert slow.status() == moe.MOE_OK
+
+
+# ------------------------------------------------------------------ few tokens: norm -> block -> norm ...
+def chain_of(T, d, I, mx, seed, layers=3):
+    """A chain of `layers` norms and blocks on fixed inputs, and its definition in steps."""
+    g = gen(seed)
+    x, res = normal(g, T, d), normal(g, T, d)
+    w = [normal(g, d) for _ in range(layers + 1)]
+    gu = [normal(g, 2 * I, d, scale=d ** -0.5) for _ in range(layers)]
+    dn = [normal(g, d, I, scale=I ** -0.5) for _ in range(layers)]
+    if mx:
+        gu, dn = [moe.moe_quantize_mx(t) for t in gu], [moe.moe_quantize_mx(t) for t in dn]
+    op = moe.AddNorm(d)
+    ffn = moe.GatedFfn(d, I, max(T, 8), weight_format=moe.MOE_W_MX8 if mx else moe.MOE_W_BF16)
+    form = moe.MOE_MX8 if mx else moe.MOE_BF16
+
+    def run():
+        steps, s, out = [], res, x
+        for i in range(layers):
+            rows, s = op.forward(out, s, w[i], y_dtype=form)
+            out = ffn.forward(rows, gu[i], dn[i])
+            steps.append((rows, s, out))
+        steps.append(op.forward(out, s, w[layers]))
+        return steps
+
+    def check(steps):  # each step from the inputs that it had
+        s, out = res, x
+        for i in range(layers):
+            rows, s1, out1 = steps[i]
+            s0, y0 = fc.norm(out, s, w[i], 1e-6)
+            near(s1, s0, fc.HALF * s0.abs(), f"s {i}")
+            if mx:
+                y, b = fc.forward_mx(rows, gu[i], dn[i], False)
+            else:
+                near(rows, y0, norm_bound(y0, fc.HALF), f"norm {i}")
+                _, _, y, b = fc.forward(rows, gu[i], dn[i], False)
+            near(out1, y, b, f"block {i}")
+            s, out = s1, out1
+        y0 = fc.norm(out, s, w[layers], 1e-6)[1]
+        near(steps[layers][0], y0, norm_bound(y0, fc.HALF), "last norm")
+
+    return run, check, (x, res), ffn
+
+
+def flat(t):
+    return [q for p in t for q in flat(p)] if isinstance(t, (list, tuple)) else [t]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,d,I", [(1, 2048, 8192), (1, 1024, 2816), (9, 512, 1024), (17, 2048, 512), (40, 4096, 2752)])
+def test_few_tokens_in_a_graph_between_norms(T, d, I, mx):
+    run, check, inputs, ffn = chain_of(T, d, I, mx, 44)
+    eager = run()
+    check(eager)
+    eager = [t.view(torch.uint8).clone() for t in flat(eager)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    got = [t.view(torch.uint8) for t in flat(got)]
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        graph.replay()  # (back to back: the first of a replay follows the last of the one before)
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b)
+    # other inputs through the same graph
+    for t in inputs:
+        t.copy_(normal(gen(45), *t.shape))
+    graph.replay()
+    for a, b in zip(got, flat(run())):
+        assert torch.equal(a, b.view(torch.uint8))
+    assert ffn.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [1, 16, 33])
+def test_few_tokens_read_weights_that_the_kernel_before_wrote(T):
+    # (the second product asks for its weights before the first has ended)
+    g = gen(46)
+    d, I = (4096, 2752) if T > 32 else (1024, 2048)
+    op, ffn = moe.AddNorm(d), moe.GatedFfn(d, I, T, training=True)
+    sets = [(normal(g, T, d), normal(g, 2 * I, d, scale=d ** -0.5), normal(g, d, I, scale=I ** -0.5), normal(g, d))
+            for _ in range(2)]
+    res = normal(g, T, d)
+    want = []
+    for x, gu, dn, w in sets:
+        y, s = op.forward(x, res, w)
+        out, pre = ffn.forward(y, gu, dn, save=True)
+        want.append([t.clone() for t in (out, pre) + ffn.backward(y, pre, gu, dn, x)])
+        torch.cuda.synchronize()
+    x, gu, dn, w = (torch.empty_like(t) for t in sets[0])
+    got = []
+    for i in range(20):
+        for to, t in zip((x, gu, dn, w), sets[i % 2]):
+            to.copy_(t)
+        y, s = op.forward(x, res, w)
+        out, pre = ffn.forward(y, gu, dn, save=True)
+        got.append((out, pre) + ffn.backward(y, pre, gu, dn, x))
+    for i, r in enumerate(got):
+        for a, b in zip(r, want[i % 2]):
+            assert torch.equal(a, b)
+    assert ffn.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_few_tokens_beside_other_work(mx):
+    # two chains on two streams, each with a context of its own
+    chains = [chain_of(T, 1024, 2816, mx, 47 + T) for T in (1, 12)]
+    want = [[t.view(torch.uint8).clone() for t in flat(run())] for run, *_ in chains]
+    streams = [torch.cuda.Stream() for _ in chains]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (run, *_) in enumerate(chains):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for a, b in zip(flat(r), want[i]):
+                assert torch.equal(a.view(torch.uint8), b)
+        assert chains[i][3].status() == moe.MOE_OK
