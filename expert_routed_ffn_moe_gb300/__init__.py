@@ -553,7 +553,7 @@ class AddNorm:
         return y, s_out
 
     def backward(self, s, weight, dy, ds=None, stream=None):
-        """(dx, dweight); dx is the gradient of x and of the residual alike."""
+        """(dx, dweight); dx is the gradient of x and of the residual alike.  dy and ds have s's dtype."""
         torch = _t()
         if stream is not None:
             with torch.cuda.stream(stream):

@@ -48,10 +48,11 @@
 // Every wait is bounded; on expiry the kernel drains what it has in flight,
 // frees TMEM and returns (see the end of the kernel).
 //
-// What bounds it: large bf16 products the MMAs (the tensor pipe is active 85-88%
-// of a CTA's time) and, run back to back, the card's power: T = 8192, d = 4096,
-// I = 16384 with pre saved, 1.96-2.05 ms, 1.61-1.68 PFLOP/s; the backward call at
-// T = 4096 2.06-2.17 ms.  mx8 at T = 8191 1.2 ms, 2.7 PFLOP/s: a block's data,
+// What bounds it: large bf16 products the MMAs (the tensor pipe is active 82-85%
+// of the time, in grad_h 65%) and, run back to back, the card's power: T = 8192, d
+// = 4096, I = 16384 with pre saved, 1.96-2.11 ms, 1.57-1.68 PFLOP/s; the backward
+// call at T = 4096 2.06-2.17 ms.  mx8 at T = 8191 1.16-1.27 ms, 2.6-2.8 PFLOP/s,
+// the tensor pipe active 61% (T = 4096, I = 8192): a block's data,
 // its scales' copies and the sight of both have to come in time for 512 cycles of
 // MMAs (TMEM has room for four blocks' scales).  Few tiles: the ~1 us that each
 // of a launch's start, first loads, epilogue and end take.

@@ -35,7 +35,7 @@ MOE_DEV uint32_t mx_scale_byte(float amax) {
   return (uint32_t)max(e, 0);
 }
 // 2^-e, what the values are multiplied by before they are rounded to e4m3.
-// Exact for every byte 0..246 that a finite amax can have (2^127 .. 2^-119); byte 255 gives NaN.
+// Exact for every byte 0..247 that a finite amax can have (2^127 .. 2^-120); byte 255 gives NaN.
 MOE_DEV float mx_inverse_scale(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - byte) << 23);
 }
@@ -285,8 +285,9 @@ cudaError_t launch_ffn_down_mx(const FfnEngine& e, const FfnShape& s, const uint
 // with 64 tokens the parts' exchange grows and waits for the ring's memory.
 // Forward call at T = 33 and 64, as a stream against as tiles (us): d = 4096, I =
 // 16384: 84, 87 against 95, 95 (mx8: 52, 56 against 67, 67); d = 4096, I = 4096:
-// 30, 32 against 34, 34; d = 2048, I = 2048: 24, 27 against 21, 21; d = 2048, I =
-// 512: 14, 16 against 17, 17 (backward 20, 22 against 20, 20).
+// 30, 32 against 34, 34; d = 2048, I = 2048: 24, 27 against 21, 21.  One rule serves
+// both directions: the smallest weights would gain 1 to 3 us forward (d = 2048, I =
+// 512: 14, 16 against 17, 17) but not backward (20, 22 against 20, 20).
 constexpr int kSkinnyTokens = 64;
 inline bool few_tokens(const FfnShape& s) {
   return s.T <= 32 || (s.T <= kSkinnyTokens && 3LL * s.d * s.I >= 1LL << 25);

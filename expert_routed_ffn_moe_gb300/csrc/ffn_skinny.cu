@@ -15,9 +15,11 @@
 // of the memory rate.  Warps 2-5 read the accumulators (one weight row per
 // thread).
 //
-// A tile of 128 weight rows belongs to a cluster of up to 8 CTAs, each of which
-// streams a contiguous part of the row's length, so that about every SM has a
-// part.  The parts meet in distributed shared memory: token t's are pushed to
+// A tile of 128 weight rows belongs to a cluster of 1, 2, 4 or 8 CTAs, each of
+// which streams a contiguous part of the row's length.  A power of two keeps the
+// places of tokens and parts to shifts, but does not fill the device: where the
+// rows are 2048 or a higher power of two there are 128 CTAs for 152 SMs, 86 for
+// 11008 rows, 80 for 5120, 64 for 1024.  The parts meet in distributed shared memory: token t's are pushed to
 // the cluster's CTA t mod C, which adds them in the order of k and finishes the
 // token.  The result depends on the shape and the number of SMs, never on
 // timing, and nothing goes through memory.

@@ -335,11 +335,12 @@ long long moe_add_norm_workspace(int d);
  *   dweight = sum over the rows of dy * n.
  * s, dy, ds [T, d] and dx [T, d] have `dtype`; ds is the gradient that reaches s
  * by the residual path (NULL: none), and dx is the gradient of x and of the
- * residual alike.  weight and dweight [d] have w_dtype.  dx or dweight may be
- * NULL to skip it (with T > 0 not both); dx may be dy or ds.  workspace: moe_add_norm_workspace(d)
- * bytes, needed for dweight; calls that overlap in time need one each.  The
- * result does not depend on timing.  T == 0 sets dweight to 0.  Limits of d and T
- * as above. */
+ * residual alike (a forward call with an fp32 residual has an fp32 s: dy is then
+ * fp32 too).  weight and dweight [d] have w_dtype.  dx or dweight may be NULL to
+ * skip it (with T > 0 not both); dx may be dy or ds.  workspace:
+ * moe_add_norm_workspace(d) bytes, needed for dweight; calls that overlap in time
+ * need one each.  The result does not depend on timing.  T == 0 sets dweight to 0.
+ * Limits of d and T as above. */
 int moe_add_norm_backward(const void* s, const void* weight, const void* dy, const void* ds, int dtype, int w_dtype,
                           int T, int d, float eps, void* dx, void* dweight, void* workspace, void* stream);
 
@@ -394,10 +395,10 @@ int moe_ffn_backward(moe_ffn* ctx, const void* x, const void* pre, int T, const 
 /* Number of kernels this context has launched (or captured) so far. */
 long long moe_ffn_launch_count(moe_ffn* ctx);
 
-/* As moe_set_spin_limit and moe_inject_stall, for a moe_ffn context (the thread
- * that issues a product's matrix instructions waits for what never happens; calls
- * whose products run without tensor cores do not wait).  A limit does not count
- * the time that a kernel waits for the one before it on the stream. */
+/* As moe_set_spin_limit and moe_inject_stall, for a moe_ffn context (the threads
+ * that issue a product's matrix instructions wait for what never happens).  A
+ * limit does not count the time that a kernel waits for the one before it on the
+ * stream. */
 int moe_ffn_set_spin_limit(moe_ffn* ctx, long long limit);
 int moe_ffn_inject_stall(moe_ffn* ctx, int on);
 
