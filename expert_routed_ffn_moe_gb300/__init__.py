@@ -676,11 +676,13 @@ class GatedFfn:
         return dx, dgate_up, ddown
 
     def status(self) -> int:
-        return moe_ffn_status(self.ctx)
+        with _t().cuda.device(self.device):  # (it waits for the current device)
+            return moe_ffn_status(self.ctx)
 
     def close(self):
         if self.ctx:
-            moe_ffn_destroy(self.ctx)
+            with _t().cuda.device(self.device):
+                moe_ffn_destroy(self.ctx)
             self.ctx = None
 
     def __del__(self):

@@ -1,6 +1,8 @@
 """The feed-forward block's and the norm's calls refuse tensors, contexts and
 streams of a device other than the one on which they would launch.  Host only:
 stand-ins for tensors and for the library, nothing is launched."""
+import ctypes
+
 import pytest
 import torch
 
@@ -169,3 +171,26 @@ def test_a_tensor_of_the_host_is_still_named_as_such(host):
                  lambda: moe.GatedFfn(D, I, T).forward(x, x, x)):
         with pytest.raises(ValueError, match="must be a contiguous CUDA tensor"):
             call()
+
+
+def test_status_and_close_wait_for_the_contexts_device(host, monkeypatch):
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, host.current = host.current, self.index
+
+        def __exit__(self, *args):
+            host.current = self.before
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(moe, "moe_ffn_status", lambda ctx: seen.append(("status", host.current)) or moe.MOE_OK)
+    monkeypatch.setattr(moe, "moe_ffn_destroy", lambda ctx: seen.append(("close", host.current)))
+    ffn = moe.GatedFfn(D, I, T)
+    ffn.ctx = ctypes.c_void_p(16)  # (a handle that only the functions above get)
+    host.current = 1
+    assert ffn.status() == moe.MOE_OK
+    ffn.close()
+    assert seen == [("status", 0), ("close", 0)] and host.current == 1 and ffn.ctx is None
