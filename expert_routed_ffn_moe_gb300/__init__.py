@@ -18,7 +18,7 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_T
     MOE_ERR_NOMEM = range(8)
 MOE_F32, MOE_BF16, MOE_MX8 = 0, 1, 2
 MOE_W_BF16, MOE_W_Q4G64, MOE_W_MX8 = 0, 1, 2
-MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
+MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_NONE = 0, 1, 2
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_GEMM = 0, 1, 2
 MOE_ROUTER_AUTO, MOE_ROUTER_SIMT, MOE_ROUTER_TENSOR = 0, 1, 2
 (MOE_K_ROUTER, MOE_K_SELECT, MOE_K_GROUP, MOE_K_GEMV_GATE_UP, MOE_K_GEMV_DOWN, MOE_K_GEMM_GATE_UP, MOE_K_GEMM_DOWN,
@@ -41,6 +41,10 @@ class moe_config(ctypes.Structure):
 
 class moe_ffn_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("d", "inter", "max_tokens", "activation", "weight_format", "training")]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("in_features", "out_features", "max_tokens", "activation", "training")]
 
 
 _lib = None
@@ -97,6 +101,28 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = ctypes.c_longlong
         L.moe_ffn_destroy.argtypes = [P]
         L.moe_ffn_destroy.restype = None
+        L.moe_layer_norm.argtypes = [P, I, P, I, P, P, I, I, I, F, P, P, I, P]
+        L.moe_layer_norm_backward.argtypes = [P, P, P, P, I, I, I, I, F, P, P, P, P, P]
+        L.moe_sort_tokens.argtypes = [P, I, I, I, P, P, P, P, P]
+        L.moe_dispatch.argtypes = [P, I, P, I, I, I, P, I, I, P]
+        L.moe_combine.argtypes = [P, I, I, P, P, I, I, I, P, P, I, P]
+        L.moe_combine_backward.argtypes = [P, I, P, I, I, P, P, I, I, I, P, P, P]
+        L.moe_linear_init.argtypes = [ctypes.POINTER(moe_linear_config), ctypes.POINTER(P)]
+        L.moe_linear_forward.argtypes = [P, P, I, P, P, I, P, P, I, P, P]
+        L.moe_linear_backward.argtypes = [P, P, P, I, P, P, I, P, P, P, I, P]
+        L.moe_linear_set_spin_limit.argtypes = [P, ctypes.c_longlong]
+        L.moe_linear_inject_stall.argtypes = [P, I]
+        L.moe_linear_status.argtypes = [P]
+        for f in ("moe_layer_norm", "moe_layer_norm_backward", "moe_sort_tokens", "moe_dispatch", "moe_combine",
+                  "moe_combine_backward", "moe_linear_init", "moe_linear_forward", "moe_linear_backward",
+                  "moe_linear_set_spin_limit", "moe_linear_inject_stall", "moe_linear_status"):
+            getattr(L, f).restype = I
+        L.moe_layer_norm_workspace.argtypes = [I]
+        L.moe_linear_launch_count.argtypes = [P]
+        for f in ("moe_layer_norm_workspace", "moe_linear_launch_count"):
+            getattr(L, f).restype = ctypes.c_longlong
+        L.moe_linear_destroy.argtypes = [P]
+        L.moe_linear_destroy.restype = None
         L.moe_status.argtypes = [P]
         L.moe_strerror.argtypes = [I]
         L.moe_strerror.restype = ctypes.c_char_p
@@ -683,6 +709,302 @@ class GatedFfn:
         if self.ctx:
             with _t().cuda.device(self.device):
                 moe_ffn_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- layer norm
+# These follow the conventions of the block above.
+class LayerNorm:
+    """Layer norm of rows of width ``d`` with the residual's addition (see moe.h).
+    Holds no device memory: a backward call takes its workspace from its stream's."""
+
+    def __init__(self, d, eps=1e-5):
+        self.d = d
+        self.eps = float(eps)
+        self._workspace_bytes = lib().moe_layer_norm_workspace(d)
+
+    def forward(self, x, residual, weight, bias=None, y_dtype=MOE_BF16, s_out=None, stream=None):
+        """(y, s): y in ``y_dtype`` (MOE_F32 or MOE_BF16), s = x + residual in the residual's
+        dtype (without a residual s is x itself, unless ``s_out`` is given).  ``weight`` and
+        ``bias`` have one dtype; either may be None."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, residual, weight, bias, y_dtype, s_out)
+        shape = _rows(x, "x", self.d)
+        T, d = shape
+        device = _device(x, "x")
+        px, pr = _checked(x, "x", shape, device), _checked(residual, "residual", shape, device)
+        pw = _checked(weight, "weight", (d,), device)
+        pb = _checked(bias, "bias", (d,), device, None if weight is None else weight.dtype)
+        param = weight if weight is not None else bias
+        like = x if residual is None else residual
+        if s_out is None:
+            s_out = x if residual is None else torch.empty_like(residual)
+            ps = None if residual is None else s_out.data_ptr()
+        else:
+            ps = _checked(s_out, "s_out", shape, device, like.dtype)
+        if y_dtype != MOE_BF16 and y_dtype != MOE_F32:
+            raise ValueError("y_dtype must be MOE_F32 or MOE_BF16")
+        y = torch.empty_like(x, dtype=torch.bfloat16 if y_dtype == MOE_BF16 else torch.float32)
+        code = (_lib or lib()).moe_layer_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, pb,
+                                              MOE_F32 if param is None else _DTYPES[param.dtype], T, d, self.eps, ps,
+                                              y.data_ptr(), y_dtype, _handle(None, device))
+        if code:
+            _check(code, "moe_layer_norm")
+        return y, s_out
+
+    def backward(self, s, weight, dy, ds=None, stream=None):
+        """(dx, dweight, dbias); dx is the gradient of x and of the residual alike.  dy and ds have
+        s's dtype, dweight and dbias the weight's (float32 without one)."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(s, weight, dy, ds)
+        shape = _rows(s, "s", self.d)
+        T, d = shape
+        dtype = s.dtype
+        device = _device(s, "s")
+        ps, pw, pdy = _checked(s, "s", shape, device), _checked(weight, "weight", (d,), device), \
+            _checked(dy, "dy", shape, device, dtype)
+        pds = _checked(ds, "ds", shape, device, dtype)
+        dx = torch.empty_like(s)
+        w_dtype = torch.float32 if weight is None else weight.dtype
+        dweight = torch.empty(d, dtype=w_dtype, device=s.device)
+        dbias = torch.empty_like(dweight)
+        workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=s.device)
+        code = (_lib or lib()).moe_layer_norm_backward(ps, pw, pdy, pds, _DTYPES[dtype], _DTYPES[w_dtype], T, d,
+                                                       self.eps, dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
+                                                       workspace.data_ptr(), _handle(None, device))
+        if code:
+            _check(code, "moe_layer_norm_backward")
+        return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------- tokens sorted by expert
+class TokenDispatch:
+    """Tokens sorted by the experts that they picked, and back (see moe.h): a program's own experts between
+    ``dispatch`` and ``combine``, with the gradients of both.  Holds no device memory."""
+
+    def __init__(self, n_experts, top_k):
+        if not 1 <= top_k <= 32 or not 1 <= n_experts <= 1024:
+            raise ValueError(f"n_experts must be 1 to 1024 and top_k 1 to 32, got {n_experts} and {top_k}")
+        self.n_experts, self.top_k = n_experts, top_k
+
+    def _picks(self, t, name, device, dtype):
+        """t's address and its number of tokens, after the checks."""
+        T = _rows(t, name, self.top_k)[0]
+        return _checked(t, name, (T, self.top_k), device, dtype), T
+
+    def sort(self, idx, counts=None, offsets=None, perm=None, slot=None, stream=None):
+        """(counts, offsets, perm, slot) of the picks idx [T, top_k] int32, into the given tensors; ids outside
+        0 .. n_experts - 1 are dropped picks.  Entries of perm past the last sorted row are not written."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.sort(idx, counts, offsets, perm, slot)
+        device, int32 = _device(idx, "idx"), torch.int32
+        pi, T = self._picks(idx, "idx", device, int32)
+        E = self.n_experts
+
+        def output(t, name, shape):
+            if t is None:
+                t = torch.empty(shape, dtype=int32, device=idx.device)
+                return t, t.data_ptr()
+            return t, _checked(t, name, shape, device, int32)
+
+        counts, pc = output(counts, "counts", (E,))
+        offsets, po = output(offsets, "offsets", (E + 1,))
+        perm, pp = output(perm, "perm", (T * self.top_k,))
+        slot, psl = output(slot, "slot", (T, self.top_k))
+        code = (_lib or lib()).moe_sort_tokens(pi, T, self.top_k, E, pc, po, pp, psl, _handle(None, device))
+        if code:
+            _check(code, "moe_sort_tokens")
+        return counts, offsets, perm, slot
+
+    def dispatch(self, x, slot, rows=None, rows_dtype=None, stream=None):
+        """rows [n, d], row slot[t, j] being x[t]: into ``rows``, or [T top_k, d] in ``rows_dtype`` (x's dtype by
+        default).  Rows that no pick has are not written."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.dispatch(x, slot, rows, rows_dtype)
+        T, d = _rows(x, "x")
+        device = _device(x, "x")
+        px, psl = _checked(x, "x", (T, d), device), _checked(slot, "slot", (T, self.top_k), device, torch.int32)
+        if rows is None:
+            rows = torch.empty(T * self.top_k, d, dtype=rows_dtype or x.dtype, device=x.device)
+        n = _rows(rows, "rows", d)[0]
+        pr = _checked(rows, "rows", (n, d), device)
+        code = (_lib or lib()).moe_dispatch(px, _DTYPES[x.dtype], psl, T, self.top_k, d, pr, _DTYPES[rows.dtype], n,
+                                            _handle(None, device))
+        if code:
+            _check(code, "moe_dispatch")
+        return rows
+
+    def combine(self, rows, slot, w=None, add=None, y=None, y_dtype=None, stream=None):
+        """y[t] = sum_j w[t, j] rows[slot[t, j]] + add[t]; y in add's dtype, ``y_dtype``, or the rows'."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.combine(rows, slot, w, add, y, y_dtype)
+        n, d = _rows(rows, "rows")
+        device = _device(rows, "rows")
+        pr = _checked(rows, "rows", (n, d), device)
+        psl, T = self._picks(slot, "slot", device, torch.int32)
+        pw = _checked(w, "w", (T, self.top_k), device, torch.float32)
+        if y is None:
+            y = torch.empty(T, d, dtype=y_dtype or (rows if add is None else add).dtype, device=rows.device)
+        py = _checked(y, "y", (T, d), device)
+        pa = _checked(add, "add", (T, d), device, y.dtype)
+        code = (_lib or lib()).moe_combine(pr, _DTYPES[rows.dtype], n, psl, pw, T, self.top_k, d, pa, py,
+                                           _DTYPES[y.dtype], _handle(None, device))
+        if code:
+            _check(code, "moe_combine")
+        return y
+
+    def dispatch_backward(self, drows, slot, add=None, dx=None, x_dtype=None, stream=None):
+        """dx, the gradient of ``dispatch``'s x; ``add``: the gradient that reaches x by another path."""
+        return self.combine(drows, slot, None, add, dx, x_dtype, stream)
+
+    def combine_backward(self, dy, rows, slot, w, drows=None, dw=None, stream=None):
+        """(drows, dw); pass ``False`` for one of them to leave it out (None comes back).  Rows of drows that no
+        pick has are not written."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.combine_backward(dy, rows, slot, w, drows, dw)
+        n, d = _rows(rows, "rows")
+        device = _device(rows, "rows")
+        pr = _checked(rows, "rows", (n, d), device)
+        psl, T = self._picks(slot, "slot", device, torch.int32)
+        pdy, pw = _checked(dy, "dy", (T, d), device), _checked(w, "w", (T, self.top_k), device, torch.float32)
+
+        def output(t, name, like):
+            if t is None:
+                t = torch.empty_like(like)
+                return t, t.data_ptr()
+            return (None, None) if t is False else (t, _checked(t, name, like.shape, device, like.dtype))
+
+        drows, pdr = output(drows, "drows", rows)
+        dw, pdw = output(dw, "dw", w)
+        code = (_lib or lib()).moe_combine_backward(pdy, _DTYPES[dy.dtype], pr, _DTYPES[rows.dtype], n, psl, pw, T,
+                                                    self.top_k, d, pdr, pdw, _handle(None, device))
+        if code:
+            _check(code, "moe_combine_backward")
+        return drows, dw
+
+
+# ---------------------------------------------------------------- matrix product with its epilogue
+def moe_linear_init(in_features, out_features, max_tokens, activation=MOE_ACT_NONE, training=False) -> ctypes.c_void_p:
+    cfg = moe_linear_config(in_features, out_features, max_tokens, activation, int(training))
+    h = ctypes.c_void_p()
+    _check(lib().moe_linear_init(ctypes.byref(cfg), ctypes.byref(h)), "moe_linear_init")
+    return h
+
+
+def moe_linear_destroy(ctx) -> None:
+    lib().moe_linear_destroy(ctx)
+
+
+def moe_linear_status(ctx) -> int:
+    return lib().moe_linear_status(ctx)
+
+
+def moe_linear_set_spin_limit(ctx, limit_ns: int) -> None:
+    _check(lib().moe_linear_set_spin_limit(ctx, limit_ns), "moe_linear_set_spin_limit")
+
+
+def moe_linear_inject_stall(ctx, on: bool) -> None:
+    _check(lib().moe_linear_inject_stall(ctx, int(on)), "moe_linear_inject_stall")
+
+
+def moe_linear_launch_count(ctx) -> int:
+    return lib().moe_linear_launch_count(ctx)
+
+
+class Linear:
+    """Owns one context of the matrix product with its epilogue, y = act(x weight^T + bias) + residual
+    (moe_linear_*, see moe.h)."""
+
+    def __init__(self, in_features, out_features, max_tokens, *, activation=MOE_ACT_NONE, training=False):
+        self.ctx = None
+        self.in_features, self.out_features = in_features, out_features
+        self.ctx = moe_linear_init(in_features, out_features, max_tokens, activation, training)
+        self.device = _t().cuda.current_device()
+
+    def forward(self, x, weight, bias=None, residual=None, y=None, y_dtype=None, pre=None, save=False, stream=None):
+        """y, or (y, pre) with ``save`` (pre: what ``backward`` needs of a call with an activation).  y has the
+        residual's dtype, or ``y_dtype`` (torch.bfloat16 by default)."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, weight, bias, residual, y, y_dtype, pre, save)
+        k, n, bf16 = self.in_features, self.out_features, torch.bfloat16
+        T = _rows(x, "x", k)[0]
+        device = _device(x, "x", self.device)
+        px, pw = _checked(x, "x", (T, k), device, bf16), _checked(weight, "weight", (n, k), device, bf16)
+        pb = _checked(bias, "bias", (n,), device)
+        if y is None:
+            y = torch.empty(T, n, dtype=y_dtype or (bf16 if residual is None else residual.dtype), device=x.device)
+        py = _checked(y, "y", (T, n), device)
+        pr = _checked(residual, "residual", (T, n), device, y.dtype)
+        if pre is None and save:
+            pre = torch.empty(T, n, dtype=bf16, device=x.device)
+        pp = _checked(pre, "pre", (T, n), device, bf16)
+        code = (_lib or lib()).moe_linear_forward(self.ctx, px, T, pw, pb, MOE_BF16 if bias is None else
+                                                  _DTYPES[bias.dtype], pr, py, _DTYPES[y.dtype], pp,
+                                                  _handle(None, device))
+        if code:
+            _check(code, "moe_linear_forward")
+        return (y, pre) if pre is not None else y
+
+    def backward(self, x, pre, weight, bias, dy, dx=None, dweight=None, dbias=None, stream=None):
+        """(dx, dweight, dbias); pass ``False`` for one of them to leave it out (None comes back).  Of the bias only
+        the dtype is used, which dbias has; without one dbias is None.  ``pre`` may be None without an activation."""
+        torch = _t()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(x, pre, weight, bias, dy, dx, dweight, dbias)
+        k, n, bf16 = self.in_features, self.out_features, torch.bfloat16
+        T = _rows(x, "x", k)[0]
+        device = _device(x, "x", self.device)
+        px, pw = _checked(x, "x", (T, k), device, bf16), _checked(weight, "weight", (n, k), device, bf16)
+        ppre, pdy = _checked(pre, "pre", (T, n), device, bf16), _checked(dy, "dy", (T, n), device)
+        _checked(bias, "bias", (n,), device)
+
+        def output(t, name, like):
+            if t is False or like is None:
+                return None, None
+            if t is None:
+                t = torch.empty_like(like)
+                return t, t.data_ptr()
+            return t, _checked(t, name, like.shape, device, like.dtype)
+
+        dx, pdx = output(dx, "dx", x)
+        dweight, pdw = output(dweight, "dweight", weight)
+        dbias, pdb = output(dbias, "dbias", bias)
+        code = (_lib or lib()).moe_linear_backward(self.ctx, px, ppre, T, pw, pdy, _DTYPES[dy.dtype], pdx, pdw, pdb,
+                                                   MOE_BF16 if bias is None else _DTYPES[bias.dtype],
+                                                   _handle(None, device))
+        if code:
+            _check(code, "moe_linear_backward")
+        return dx, dweight, dbias
+
+    def status(self) -> int:
+        with _t().cuda.device(self.device):  # (it waits for the current device)
+            return moe_linear_status(self.ctx)
+
+    def close(self):
+        if self.ctx:
+            with _t().cuda.device(self.device):
+                moe_linear_destroy(self.ctx)
             self.ctx = None
 
     def __del__(self):

@@ -7,6 +7,7 @@
 //   dx        dx = dpre gate_up
 //   dgate_up  dpre^T x
 //   ddown     dy^T h
+//   linear    y = act(x weight^T + bias) + residual        (not gated; a block of its own)
 //
 // One persistent kernel.  A pair of CTAs on neighbouring SMs (a cluster of two)
 // computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA loads its
@@ -80,10 +81,10 @@ constexpr uint32_t kScaleCol = 2 * kBN - kSharedCols;
 // (a split divides that too); the exchange of a split.
 constexpr int kTileCost = 6, kSplitCost = 7, kLaunchCost = 8;  // (and of another launch)
 constexpr int kNextTileCost = 6;  // a weight gradient's tile after the pair's first
-constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 1 ? 9 : 16; }
+constexpr int epilogue_cost(int epi) { return epi == 0 ? 4 : epi == 2 ? 16 : 9; }
 constexpr int kGroupM = 8;                  // m-tiles that share a sweep over n (L2 reuse)
 
-enum { kEpiStore, kEpiGateUp, kEpiGrad };
+enum { kEpiStore, kEpiGateUp, kEpiGrad, kEpiLinear };
 
 // One product: result [M, N] = a b^T over K.
 struct Product {
@@ -101,9 +102,12 @@ struct GemmParams {
   int early;                       // MULTI: light tiles that take as long as a heavy one
   CUtensorMap as, bs0, bs1;        // mx8 scales: of A, and of the two 128-row halves of B
   uint8_t *hq, *hs;                // mx8 gate/up: codes and scales of h
-  uint16_t* pre_out;               // gate/up: pre [M, 2N], or NULL
+  uint16_t* pre_out;               // gate/up: pre [M, 2N], or NULL; linear: pre [M, N], or NULL
   const uint16_t* pre;             // grad: pre [M, 2N]
   uint16_t* dpre;                  // grad: [M, 2N]
+  const void *bias, *res;          // linear: [N] and [M, N], or NULL
+  int bias_bf16, y32;              // linear: the bias is bf16; result and residual are fp32
+  int wide32;                      // linear: rows of an fp32 result are 32-byte aligned
   int act;
   DevCtl ctl;
 };
@@ -487,8 +491,21 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         if (col + 8 < q.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     };
-    // grad: pre's values that belong to 16 columns of dh, asked for ahead of them
-    auto load_pre = [&](const Product& q, int row, int col, uint4(&in)[4]) {
+    // What 16 columns of a row need besides their sums, asked for ahead of them.  grad: pre's values; linear: the
+    // residual (first four) and the bias, as they lie in memory.
+    constexpr int kIn = EPI == kEpiLinear ? 8 : 4;
+    auto load_pre = [&](const Product& q, int row, int col, uint4(&in)[kIn]) {
+      if constexpr (EPI == kEpiLinear) {
+        auto load = [&](const void* from, bool wide, size_t at, bool ok, uint4* to) {  // 2 or 4 x 16 bytes, 8 columns at a time
+          const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + at * (wide ? 4 : 2));
+          const int n = wide ? 4 : 2;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < n) to[c] = ok && col + c * 16 / n < q.N ? v[c] : make_uint4(0, 0, 0, 0);
+        };
+        if (p.res) load(p.res, p.y32, (size_t)row * q.N + col, row < q.M, in);
+        if (p.bias) load(p.bias, !p.bias_bf16, col, true, in + 4);
+      }
       if (EPI != kEpiGrad) return;
       const uint16_t* gp = p.pre + (size_t)row * 2 * q.N + col;
 #pragma unroll
@@ -500,8 +517,44 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     };
     // One row's results: 16 columns of a product or of dh, or gate and up values of 16 neurons
     // (grad: pre's 16 gate and up values of the row in `in`)
-    auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16], const uint4(&in)[4]) {
-      if (EPI == kEpiStore) {
+    auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16], const uint4(&in)[kIn]) {
+      if constexpr (EPI == kEpiLinear) {
+        auto add = [&](const uint4* from, bool wide) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(from);
+          if (wide) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+          }
+        };
+        if (p.bias) add(in + 4, !p.bias_bf16);
+        if (p.pre_out) store16(q, p.pre_out, q.N, row, col, v);
+        with_act_or_none(p.act, [&](auto act) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = act_value<decltype(act)::value>(v[e]);
+        });
+        if (p.res) add(in, p.y32);
+        if (!p.y32) {
+          store16(q, q.y, q.N, row, col, v);
+        } else if (row < q.M) {
+          float* at = reinterpret_cast<float*>(q.y) + (size_t)row * q.N + col;
+#pragma unroll
+          for (int h = 0; h < 16; h += 8)
+            if (col + h < q.N) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[h + e]);
+              if (p.wide32) {
+                store32(at + h, w);
+              } else {
+                reinterpret_cast<uint4*>(at + h)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(at + h)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+        }
+      } else if (EPI == kEpiStore) {
         store16(q, q.y, q.N, row, col, v);
       } else if (EPI == kEpiGateUp) {
         if (p.pre_out) {  // (the up half lies N columns further)
@@ -561,7 +614,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         const int m = t.m, n = t.n, acc = lt & 1;
         const int row = (2 * m + (int)rank) * kBM + part * 32 + lane;
         constexpr int kChunks = EPI == kEpiGateUp ? 4 : 8;  // of 16 columns (neurons), see below
-        uint4 in[4];
+        uint4 in[kIn];
         load_pre(q, row, n * TN + half * kChunks * 16, in);  // in flight while the product is waited for
         if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
           set_abort(bar);
@@ -629,7 +682,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             float x[16], y[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = v[e], y[e] = u[e];
-            const uint4 now[4] = {in[0], in[1], in[2], in[3]};
+            uint4 now[kIn];
+#pragma unroll
+            for (int e = 0; e < kIn; ++e) now[e] = in[e];
             if (holds && i == kShared - 1) release();
             if (i + 1 < kChunks) {
               load(i + 1);
@@ -724,7 +779,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           sum16(48, b0 + 16, u + 16);
           finish_mx(q, row, n * TN + a0, g, u);
         } else if (EPI == kEpiGateUp) {
-          const uint4 none[4] = {};
+          const uint4 none[kIn] = {};
 #pragma unroll 1
           for (int c = 0; c < W; c += 16) {
             float g[16], u[16];
@@ -736,7 +791,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
 #pragma unroll 1
           for (int c = 0; c < 2 * W; c += 16) {
             float v[16];
-            uint4 in[4];
+            uint4 in[kIn];
             load_pre(q, row, n * TN + a0 + c, in);
             sum16(c, a0 + c, v);
             finish(q, row, n * TN + a0 + c, v, v, in);
@@ -914,6 +969,7 @@ cudaError_t prepare_ffn_gemm(FfnEngine* e) {
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, true, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, true, true, false>(e);
   if (err == cudaSuccess) err = prepare<kEpiStore, true, true, false, 1, true>(&e->pairs);
+  if (err == cudaSuccess) err = prepare_splits<kEpiLinear, false, false, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiGateUp, false, false, true>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, false, true>(e);
   return err == cudaSuccess && e->pairs < 1 ? cudaErrorInvalidConfiguration : err;
@@ -983,6 +1039,8 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBa
   return run<kEpiGrad, false, true, false>(e, p, st);
 }
 
+namespace {
+
 // dx = dpre gate_up (K = 2I), dgate_up = dpre^T x and ddown = dy^T h (K = T).
 // They do not depend on one another: they go into one launch, unless it is
 // shorter to split dx's few tiles over clusters and to launch the other two
@@ -991,13 +1049,7 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBa
 // grad_h: T = 501 in one launch 45.4 us, dx first 39.3; T = 256 each by itself
 // 38.6 us, dx first 33.6.  For few tokens launch_skinny_backward has done dx,
 // and the others have one k block.
-cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
-                             int* launches, cudaStream_t st) {
-  Product all[3] = {};  // dx, dgate_up, ddown
-  if (!set_product<kEpiStore, false, true, false>(e, all[0], sc.dpre, a.gate_up, s.T, s.d, 2 * s.I, s.d, a.dx) ||
-      !set_product<kEpiStore, true, true, false>(e, all[1], sc.dpre, a.x, 2 * s.I, s.d, s.T, s.d, a.dgate_up) ||
-      !set_product<kEpiStore, true, true, false>(e, all[2], a.dy, sc.h, s.d, s.I, s.T, s.I, a.ddown))
-    return cudaErrorInvalidValue;
+cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* launches, cudaStream_t st) {
   const bool dx_first = all[0].blocks >= all[1].blocks;  // the longer reduction
 
   // Times in k blocks.  One launch: at best even, at worst one light tile more, and no less than the heavy tiles' (a tile
@@ -1012,18 +1064,20 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
   together += first;
   double c[3];
   int split[3];
-  for (int i = 0; i < 3; ++i) split[i] = split_of<kEpiStore, false>(e, all[i], &c[i]);
+  for (int i = 0; i < 3; ++i) {
+    c[i] = 0, split[i] = 1;
+    if (all[i].tiles) split[i] = split_of<kEpiStore, false>(e, all[i], &c[i]);
+  }
   const double weights = (double)((weight_tiles + e.pairs - 1) / e.pairs) * (all[1].blocks + each) + first;
   // (these estimates are good to about a tenth, and one launch has less to go wrong)
   const double dx_apart = split[0] == 1 ? 1e30 : 1.12 * (c[0] + kLaunchCost + weights);
-  const double apart = 1.12 * (c[0] + c[1] + c[2] + 2 * kLaunchCost);
+  const double apart = 1.12 * (c[0] + c[1] + c[2] + (all[2].tiles ? 2 : 1) * kLaunchCost);
   const bool one = together <= dx_apart && together <= apart, two = !one && dx_apart <= apart;
 
   GemmParams p{};
   p.ctl = e.ctl;
   p.early = ch / cl;
   *launches = 0;
-  const bool few = few_tokens(s);
   if (few) {
     all[0].y = nullptr;
   } else if (two && all[0].y) {
@@ -1065,6 +1119,42 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
                         : run<kEpiStore, false, true, false>(e, one, st);
   }
   return err;
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
+                             int* launches, cudaStream_t st) {
+  Product all[3] = {};  // dx, dgate_up, ddown
+  if (!set_product<kEpiStore, false, true, false>(e, all[0], sc.dpre, a.gate_up, s.T, s.d, 2 * s.I, s.d, a.dx) ||
+      !set_product<kEpiStore, true, true, false>(e, all[1], sc.dpre, a.x, 2 * s.I, s.d, s.T, s.d, a.dgate_up) ||
+      !set_product<kEpiStore, true, true, false>(e, all[2], a.dy, sc.h, s.d, s.I, s.T, s.I, a.ddown))
+    return cudaErrorInvalidValue;
+  return launch_grads(e, all, few_tokens(s), launches, st);
+}
+
+cudaError_t launch_linear_grads(const FfnEngine& e, const LinearShape& s, const uint16_t* dpre, const void* x,
+                                const void* w, void* dx, void* dw, int* launches, cudaStream_t st) {
+  Product all[3] = {};  // dx, dw
+  if (!set_product<kEpiStore, false, true, false>(e, all[0], dpre, w, s.T, s.k, s.n, s.k, dx) ||
+      !set_product<kEpiStore, true, true, false>(e, all[1], dpre, x, s.n, s.k, s.T, s.k, dw))
+    return cudaErrorInvalidValue;
+  return launch_grads(e, all, few_tokens(s), launches, st);
+}
+
+cudaError_t launch_linear_tiles(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st) {
+  GemmParams p{};
+  p.act = s.act;
+  p.pre_out = a.pre;
+  p.bias = a.bias;
+  p.res = a.res;
+  p.bias_bf16 = a.bias_dtype == MOE_BF16;
+  p.y32 = a.y_dtype == MOE_F32;
+  p.wide32 = aligned32(a.y);
+  if (!set_product<kEpiLinear, false, false, false>(e, p.q[0], a.x, a.w, s.T, s.n, s.k, s.n, a.y))
+    return cudaErrorInvalidValue;
+  if (!aligned32(a.pre)) p.q[0].wide = 0;
+  return run<kEpiLinear, false, false, false>(e, p, st);
 }
 
 }  // namespace moe

@@ -134,6 +134,7 @@ MOE_DEV float logistic(float z) {
 // the loops over values have no branch; with_act() picks it once per loop.
 template <int ACT>
 MOE_DEV float act_value(float g) {
+  if (ACT == MOE_ACT_NONE) return g;
   if (ACT == MOE_ACT_SILU) return g * logistic(g);
   return g * logistic(1.5957691216057308f * (g + 0.044715f * g * g * g));
 }
@@ -163,8 +164,26 @@ MOE_DEV void with_act(int act, F&& f) {
     f(ActTag<MOE_ACT_GELU>());
 }
 
+template <typename F>
+MOE_DEV void with_act_or_none(int act, F&& f) {
+  if (act == MOE_ACT_NONE)
+    f(ActTag<MOE_ACT_NONE>());
+  else
+    with_act(act, f);
+}
+
 struct FfnShape {
   int T, d, I, act;
+};
+// The matrix product with its epilogue: y [T, n] from x [T, k] and weight [n, k].
+struct LinearShape {
+  int T, k, n, act;
+};
+struct LinearForwardArgs {
+  const void *x, *w, *bias, *res;  // (bias, res: NULL where absent)
+  void* y;
+  uint16_t* pre;                   // NULL: not wanted
+  int bias_dtype, y_dtype;         // res has y's
 };
 
 // ffn_norm.cu
@@ -269,6 +288,11 @@ cudaError_t launch_ffn_grad_h(const FfnEngine& e, const FfnShape& s, const FfnBa
 cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a, const FfnScratch& sc,
                              int* launches, cudaStream_t st);
 
+cudaError_t launch_linear_tiles(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st);
+// dx = dpre w and dw = dpre^T x, as far as wanted (with few tokens dw alone); *launches: kernels launched
+cudaError_t launch_linear_grads(const FfnEngine& e, const LinearShape& s, const uint16_t* dpre, const void* x,
+                                const void* w, void* dx, void* dw, int* launches, cudaStream_t st);
+
 // mx8.  up_s: the scales of gate_up's rows I .. 2I - 1 as a matrix of their own:
 // where I is a multiple of 128 they are one inside gate_up_s, else
 // launch_mx_up_scales lays them out.
@@ -292,10 +316,16 @@ constexpr int kSkinnyTokens = 64;
 inline bool few_tokens(const FfnShape& s) {
   return s.T <= 32 || (s.T <= kSkinnyTokens && 3LL * s.d * s.I >= 1LL << 25);
 }
+inline bool few_tokens(const LinearShape& s) {
+  return s.T <= 32 || (s.T <= kSkinnyTokens && (long long)s.n * s.k >= 1LL << 24);
+}
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,
                                   const uint8_t* up_s, const FfnScratch& sc, cudaStream_t st);
 cudaError_t launch_skinny_backward(const FfnEngine& e, const FfnShape& s, const FfnBackwardArgs& a,
                                    const FfnScratch& sc, cudaStream_t st);
+cudaError_t launch_linear_stream(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st);
+cudaError_t launch_linear_dx_stream(const FfnEngine& e, const LinearShape& s, const uint16_t* dpre, const void* w,
+                                    void* dx, cudaStream_t st);
 
 }  // namespace moe

@@ -51,8 +51,9 @@ constexpr int kThreads = 320;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 6;
 
-enum { kDown, kGateUp, kGradH, kDx };
-constexpr bool first_of(int kind) { return kind == kGateUp || kind == kGradH; }  // of a call's two kernels
+// kLinear, kLinearDx: the product with its epilogue and its dx, calls of one such kernel
+enum { kDown, kGateUp, kLinear, kGradH, kDx, kLinearDx };
+constexpr bool first_of(int kind) { return kind != kDown && kind != kDx; }  // of a call's two kernels
 constexpr bool w_mn(int kind) { return kind >= kGradH; }  // the weights lie [K, rows]
 
 struct SkinnyParams {
@@ -60,7 +61,9 @@ struct SkinnyParams {
   CUtensorMap next;                // the first kernel: the weights of the second, next_rows x next_K (0: there is none)
   int next_rows, next_K;
   CUtensorMap ws, us, xs;          // mx8 scales: of the rows (gate), of the up rows, of x or h
-  uint16_t *h, *pre, *y;           // y: of down, or dx
+  uint16_t *h, *pre, *y;           // y: of down or linear, or dx
+  const void *bias, *res;          // linear: or NULL
+  int bias_bf16, y32;              // linear: the bias is bf16; y and res are fp32
   uint16_t* dpre;
   uint8_t *hq, *hs;
   int T, N, K;                     // N: neurons (gate/up, grad_h) or columns of y
@@ -331,6 +334,37 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_skinny_kernel(const __grid_co
             }
           }
         });
+      } else if constexpr (KIND == kLinear) {
+        const float b = !p.bias || !in ? 0.f
+                        : p.bias_bf16  ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n])
+                                       : static_cast<const float*>(p.bias)[n];
+        float r[n_tok];
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i) {
+          const size_t at = (size_t)(t + i * step) * p.N + n;
+          const bool is = p.res && in && t + i * step < T;
+          r[i] = !is ? 0.f : p.y32 ? static_cast<const float*>(p.res)[at]
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[at]);
+        }
+        with_act_or_none(p.act, [&](auto act) {
+#pragma unroll
+          for (int i = 0; i < n_tok; ++i) {
+            const size_t at = (size_t)(t + i * step) * p.N + n;
+            v[i] += b;
+            if (p.pre && in && t + i * step < T) p.pre[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+            v[i] = act_value<decltype(act)::value>(v[i]) + r[i];
+          }
+        });
+#pragma unroll
+        for (int i = 0; i < n_tok; ++i) {
+          const size_t at = (size_t)(t + i * step) * p.N + n;
+          if (in && t + i * step < T) {
+            if (p.y32)
+              reinterpret_cast<float*>(p.y)[at] = v[i];
+            else
+              p.y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+          }
+        }
       } else if (GATE && MX) {
         uint32_t byte[n_tok];  // N is a multiple of 32: the warp's group is all in or all out
 #pragma unroll
@@ -509,6 +543,8 @@ cudaError_t prepare_ffn_skinny() {
   if (err == cudaSuccess) err = prepare_nt<true, kGateUp>();
   if (err == cudaSuccess) err = prepare_nt<false, kGradH>();
   if (err == cudaSuccess) err = prepare_nt<false, kDx>();
+  if (err == cudaSuccess) err = prepare_nt<false, kLinear>();
+  if (err == cudaSuccess) err = prepare_nt<false, kLinearDx>();
   return err;
 }
 
@@ -567,6 +603,39 @@ cudaError_t launch_skinny_backward(const FfnEngine& e, const FfnShape& s, const 
   cudaError_t err = run_nt<false, kGradH>(e, g, st);
   if (err == cudaSuccess && a.dx) err = run_nt<false, kDx>(e, d, st);
   return err;
+}
+
+cudaError_t launch_linear_stream(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st) {
+  SkinnyParams p{};
+  p.T = s.T;
+  p.N = s.n;
+  p.K = s.k;
+  p.act = s.act;
+  p.ctl = e.ctl;
+  p.y = static_cast<uint16_t*>(a.y);
+  p.pre = a.pre;
+  p.bias = a.bias;
+  p.res = a.res;
+  p.bias_bf16 = a.bias_dtype == MOE_BF16;
+  p.y32 = a.y_dtype == MOE_F32;
+  if (!make_bf16_map(e.encode, &p.w, a.w, s.k, s.n, s.k, 64, kRows) ||
+      !make_bf16_map(e.encode, &p.x, a.x, s.k, s.T, s.k, 64, token_rows(s.T)))
+    return cudaErrorInvalidValue;
+  return run_nt<false, kLinear>(e, p, st);
+}
+
+cudaError_t launch_linear_dx_stream(const FfnEngine& e, const LinearShape& s, const uint16_t* dpre, const void* w,
+                                    void* dx, cudaStream_t st) {
+  SkinnyParams p{};
+  p.T = s.T;
+  p.N = s.k;
+  p.K = s.n;
+  p.ctl = e.ctl;
+  p.y = static_cast<uint16_t*>(dx);
+  if (!make_bf16_map(e.encode, &p.w, w, s.k, s.n, s.k, 64, 64) ||
+      !make_bf16_map(e.encode, &p.x, dpre, s.n, s.T, s.n, 64, token_rows(s.T)))
+    return cudaErrorInvalidValue;
+  return run_nt<false, kLinearDx>(e, p, st);
 }
 
 }  // namespace moe

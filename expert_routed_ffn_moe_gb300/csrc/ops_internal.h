@@ -1,0 +1,64 @@
+// Internal declarations of the layer norm, of tokens sorted by expert and of the
+// matrix product with its epilogue: arguments and kernel launchers.
+#pragma once
+
+#include "ffn_internal.h"
+
+namespace moe {
+
+// layer_norm.cu
+struct LayerNormArgs {
+  const void *x, *res, *w, *b;
+  void *s, *y;
+  int T, d;
+  int x_dtype, s_dtype, w_dtype, y_dtype;
+  float eps;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t st);
+
+// layer_norm_grad.cu
+// Blocks of a backward call, each with its own partial gradients of weight and bias.
+constexpr int kLayerNormPartials = 608;  // 4 for each of 152 SMs
+struct LayerNormGradArgs {
+  const void *s, *w, *dy, *ds;
+  void *dx, *dw, *db;
+  float* partial;  // [kLayerNormPartials][2][d]
+  int T, d;
+  int dtype, w_dtype;
+  float eps;
+};
+cudaError_t launch_layer_norm_backward(const LayerNormGradArgs& a, cudaStream_t st);
+
+// moe_dispatch.cu
+constexpr int kMaxSortExperts = 1024;
+struct SortArgs {
+  const int32_t* idx;
+  int32_t *counts, *offsets, *perm, *slot;
+  int picks, k, E;
+};
+cudaError_t launch_sort_tokens(const SortArgs& a, cudaStream_t st);
+struct RowsArgs {
+  const void* tokens;      // x, dy or add [T, d]
+  const void* rows_in;     // [n_rows, d]
+  void* out;               // dispatch, combine's gradient: rows [n_rows, d]; combine: y [T, d]
+  const int32_t* slot;     // [T, k]
+  const float* w;          // [T, k]
+  float* dw;               // [T, k]
+  int T, k, d, n_rows;
+  int t_dtype, r_dtype;    // of the tokens' side and of the rows
+};
+cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t st);
+cudaError_t launch_combine_rows(const RowsArgs& a, cudaStream_t st);
+cudaError_t launch_combine_backward(const RowsArgs& a, cudaStream_t st);
+
+// linear_grad.cu: dpre = dy act'(pre) (dpre NULL: not stored), dbias = the sum of its rows (NULL: not wanted)
+struct LinearGradArgs {
+  const void* dy;
+  const uint16_t* pre;
+  uint16_t* dpre;
+  void* dbias;
+  int T, n, dy_dtype, bias_dtype, act;
+};
+cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,113 @@
+// What the kernels over rows share: 8 neighbouring columns as a chunk, a row's
+// sums over its threads, launches that overlap the kernel before.
+#pragma once
+
+#include "ffn_internal.h"
+
+namespace moe {
+
+struct F8 {
+  float v[8];
+};
+
+// These kernels are launched while the kernel before may still run
+// (programmatic stream serialization): their blocks come up during its end, and
+// read and write nothing before it has finished.
+MOE_DEV void follow() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// A chunk as it lies in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+  MOE_DEV void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  MOE_DEV void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  MOE_DEV F8 get() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a;
+  MOE_DEV void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  MOE_DEV void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  MOE_DEV F8 get() const {
+    return F8{{bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y), bf16_lo(a.z), bf16_hi(a.z), bf16_lo(a.w),
+               bf16_hi(a.w)}};
+  }
+};
+template <typename T>
+MOE_DEV F8 load8(const T* p) {
+  Raw<T> r;
+  r.load(p);
+  return r.get();
+}
+MOE_DEV void store8(float* p, const F8& f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+}
+MOE_DEV void store8(__nv_bfloat16* p, const F8& f) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f.v[0], f.v[1]), pack_bf16x2(f.v[2], f.v[3]),
+                                            pack_bf16x2(f.v[4], f.v[5]), pack_bf16x2(f.v[6], f.v[7]));
+}
+MOE_DEV float to_f(float v) { return v; }
+MOE_DEV float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+MOE_DEV void put(float* p, float v) { *p = v; }
+MOE_DEV void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The sums over the R threads of a row, in every one of them.  `red` is another
+// half of its memory from one row to the next, so one barrier per row suffices.
+template <int R, int N>
+MOE_DEV void row_sums(float (&v)[N], float (*red)[N][32]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  if (R == 32) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) (*red)[i][warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < R / 32 ? (*red)[i][lane] : 0.f);
+}
+
+// Blocks that walk the rows: as many as are resident on the device's SMs.
+template <typename K>
+int resident_blocks(K kernel, int block, size_t smem) {
+  int dev = 0, sms = 1, per = 1;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, smem) != cudaSuccess || per < 1) per = 1;
+  return sms * per;
+}
+
+// A kernel's limit on shared memory belongs to all its launches, which threads of the host may issue side by side: it
+// is set for the widest rows, never lower for narrower ones.
+template <typename K>
+cudaError_t allow(K kernel, size_t smem, size_t most) {
+  return smem <= 48 * 1024
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
+}  // namespace moe

@@ -93,6 +93,7 @@ extern "C" {
 /* activation of the feed-forward block's gate (moe_ffn_config.activation) */
 #define MOE_ACT_SILU 0         /* g / (1 + exp(-g)) */
 #define MOE_ACT_GELU 1         /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+#define MOE_ACT_NONE 2         /* g (moe_linear_config.activation only) */
 
 /* execution path for the expert FFNs (moe_set_path) */
 #define MOE_PATH_AUTO 0        /* T <= 4: GEMV over the selected experts; otherwise grouped GEMM */
@@ -408,6 +409,127 @@ int moe_ffn_status(moe_ffn* ctx);
 /* Free the context and its workspace (synchronises the device first).  NULL is
  * a no-op. */
 void moe_ffn_destroy(moe_ffn* ctx);
+
+/* ---------------------------------------------------------------------------
+ * What a block of the classic form needs beside these, in training and in
+ * serving: layer norm, tokens sorted by expert and back, and the matrix product
+ * with bias, activation and residual.  Same conventions as above.
+ * ------------------------------------------------------------------------- */
+
+/* Layer norm with the residual's addition, for every row t:
+ *   s = x + residual (s = x with residual NULL), c = s - mean(s),
+ *   y = c * rsqrt(mean(c^2) + eps) * weight + bias,
+ * in fp32, y from the sum before it is rounded into s_out.  x [T, d] (x_dtype),
+ * residual and s_out [T, d] (s_dtype; either may be NULL), weight and bias [d]
+ * (w_dtype; NULL: 1 and 0), y [T, d] (y_dtype).  Every dtype is MOE_F32 or
+ * MOE_BF16.  s_out may be residual itself, and y may be x where their dtypes are
+ * the same; no other output may overlap an input.  d is any width up to 16384 and
+ * T at most 2^30, MOE_ERR_UNSUPPORTED beyond; MOE_ERR_ARG for a dtype not listed
+ * or eps < 0.  No workspace, no context. */
+int moe_layer_norm(const void* x, int x_dtype, const void* residual, int s_dtype, const void* weight, const void* bias,
+                   int w_dtype, int T, int d, float eps, void* s_out, void* y, int y_dtype, void* stream);
+
+/* Bytes of the workspace of moe_layer_norm_backward for rows of width d. */
+long long moe_layer_norm_workspace(int d);
+
+/* Gradients of moe_layer_norm from the s it stored: with c as above, rstd =
+ * rsqrt(mean(c^2) + eps), n = c * rstd and g = dy * weight,
+ *   dx = rstd * (g - mean(g) - n * mean(g * n)) + ds,
+ *   dweight = sum over the rows of dy * n,  dbias = sum over the rows of dy.
+ * s, dy, ds [T, d] and dx [T, d] have `dtype`; ds is the gradient that reaches s
+ * by the residual path (NULL: none), and dx is the gradient of x and of the
+ * residual alike.  weight (NULL: 1), dweight and dbias [d] have w_dtype.  dx,
+ * dweight and dbias may be NULL to skip them (with T > 0 not all three), which
+ * does not change the others; dx may be dy or ds.  workspace:
+ * moe_layer_norm_workspace(d) bytes, needed for dweight and dbias; calls that
+ * overlap in time need one each.  The result does not depend on timing.  T == 0
+ * sets dweight and dbias to 0.  Limits of d and T as above. */
+int moe_layer_norm_backward(const void* s, const void* weight, const void* dy, const void* ds, int dtype, int w_dtype,
+                            int T, int d, float eps, void* dx, void* dweight, void* dbias, void* workspace,
+                            void* stream);
+
+/* Tokens sorted by expert: the tables of the picks idx [T, top_k] int32, in the
+ * order (expert, token, pick).  A pick whose id is not one of 0 .. n_experts - 1
+ * is dropped (by convention -1: over a capacity, or another device's expert).
+ * counts [n_experts] int32, offsets [n_experts + 1] int32 (exclusive prefix of
+ * counts), perm [T * top_k] int32 (the token of each sorted row; entries past
+ * offsets[n_experts] are left as they were), slot [T, top_k] int32 (the sorted
+ * row of each pick, -1 for a dropped one).  Any output may be NULL to skip it.  An expert
+ * may be picked twice by a token: it then has two rows of it.  Without dropped
+ * picks counts, offsets and perm are those of moe_route.  top_k is at most 32,
+ * n_experts at most 1024, T * top_k at most 2^30 (MOE_ERR_UNSUPPORTED beyond).
+ * T == 0 sets counts and offsets to 0.  No workspace, no context. */
+int moe_sort_tokens(const int32_t* idx, int T, int top_k, int n_experts, int32_t* counts, int32_t* offsets,
+                    int32_t* perm, int32_t* slot, void* stream);
+
+/* rows[slot[t, j]] = x[t]: x [T, d] (x_dtype) into rows [n_rows, d] (rows_dtype),
+ * slot [T, top_k] int32 as moe_sort_tokens leaves it.  Here and below a slot
+ * outside 0 .. n_rows - 1 stands for a dropped pick, rows that no slot names are
+ * left as they were, no two picks may have the same slot, and dtypes are MOE_F32
+ * or MOE_BF16, of tokens and rows each their own.  Any d; top_k is at most 32, T *
+ * top_k and T * ceil(d / 256) at most 2^30 (MOE_ERR_UNSUPPORTED beyond).  The
+ * gradient with respect to x is moe_combine of the rows' gradients without w. */
+int moe_dispatch(const void* x, int x_dtype, const int32_t* slot, int T, int top_k, int d, void* rows, int rows_dtype,
+                 int n_rows, void* stream);
+
+/* y[t] = sum over j of w[t, j] * rows[slot[t, j]] + add[t], in fp32, j ascending
+ * and add last.  rows [n_rows, d] (rows_dtype), w [T, top_k] fp32 (NULL: 1), add
+ * [T, d] (y_dtype; NULL: none), y [T, d] (y_dtype); y may be add.  A dropped pick
+ * adds nothing, whatever its weight. */
+int moe_combine(const void* rows, int rows_dtype, int n_rows, const int32_t* slot, const float* w, int T, int top_k,
+                int d, const void* add, void* y, int y_dtype, void* stream);
+
+/* Gradients of moe_combine: drows[slot[t, j]] = w[t, j] * dy[t], dw[t, j] = dy[t] .
+ * rows[slot[t, j]] (0 for a dropped pick); that of add is dy.  dy [T, d]
+ * (y_dtype), rows and drows [n_rows, d] (rows_dtype; rows is read only for dw, and
+ * drows may be rows), w and dw [T, top_k] fp32.  drows or dw may be NULL to skip
+ * it (with T > 0 not both).  Sums are fp32, in an order that depends on the sizes
+ * alone. */
+int moe_combine_backward(const void* dy, int y_dtype, const void* rows, int rows_dtype, int n_rows, const int32_t* slot,
+                         const float* w, int T, int top_k, int d, void* drows, float* dw, void* stream);
+
+typedef struct moe_linear_config {
+  int in_features;     /* columns of x and of the weight; a multiple of 8 */
+  int out_features;    /* rows of the weight, columns of y; a multiple of 8 */
+  int max_tokens;      /* largest T a call will use (the workspace is sized for it) */
+  int activation;      /* MOE_ACT_*, MOE_ACT_NONE among them */
+  int training;        /* 1: calls of moe_linear_backward are allowed; 0: forward only */
+} moe_linear_config;
+
+typedef struct moe_linear moe_linear;
+
+/* As moe_ffn_init, for a moe_linear context. */
+int moe_linear_init(const moe_linear_config* cfg, moe_linear** out);
+
+/* pre = x weight^T + bias, y = act(pre) + residual.  x [T, in], weight [out, in]
+ * bf16, bias [out] (bias_dtype; NULL: none), residual and y [T, out] (y_dtype;
+ * residual NULL: none), pre [T, out] bf16, what moe_linear_backward needs of a
+ * call with an activation, or NULL.  Dtypes are MOE_F32 or MOE_BF16.  Sums, bias,
+ * activation and residual are fp32, y is rounded once.  y may be residual; no
+ * other output may overlap an input.  Asynchronous on `stream`, nothing
+ * allocated, no host synchronisation: captures into a CUDA graph. */
+int moe_linear_forward(moe_linear* ctx, const void* x, int T, const void* weight, const void* bias, int bias_dtype,
+                       const void* residual, void* y, int y_dtype, void* pre, void* stream);
+
+/* Gradients of moe_linear_forward: with dpre = dy * act'(pre),
+ *   dx = dpre weight,  dweight = dpre^T x,  dbias = sum over the rows of dpre;
+ * that of the residual is dy.  x and weight are those of the forward call, pre is
+ * what it stored (not read, may be NULL, with MOE_ACT_NONE), dy [T, out]
+ * (dy_dtype).  dx [T, in] and dweight [out, in] are bf16, dbias [out] has
+ * bias_dtype; any of them may be NULL to skip it, which does not change the others
+ * (with T > 0 not all three).  Sums are fp32; dpre is held in bf16 for the two
+ * products, and unrounded in dbias's sum.  T == 0 sets dweight and dbias to 0.
+ * MOE_ERR_UNSUPPORTED without cfg.training. */
+int moe_linear_backward(moe_linear* ctx, const void* x, const void* pre, int T, const void* weight, const void* dy,
+                        int dy_dtype, void* dx, void* dweight, void* dbias, int bias_dtype, void* stream);
+
+/* As moe_ffn_launch_count, moe_ffn_set_spin_limit, moe_ffn_inject_stall,
+ * moe_ffn_status and moe_ffn_destroy, for a moe_linear context. */
+long long moe_linear_launch_count(moe_linear* ctx);
+int moe_linear_set_spin_limit(moe_linear* ctx, long long limit);
+int moe_linear_inject_stall(moe_linear* ctx, int on);
+int moe_linear_status(moe_linear* ctx);
+void moe_linear_destroy(moe_linear* ctx);
 
 /* Static description of a return code. */
 const char* moe_strerror(int code);
