@@ -4,183 +4,193 @@
 //   dx = rstd * (g - mean(g) - n * mean(g n)) + ds
 //   dw = sum over the rows of dy n,  db = sum over the rows of dy
 //
-// Bound by memory: one pass over s, dy and ds, rows in registers, as in the
-// forward pass; mean(s) and mean(g) come from one sum over the row's threads,
-// mean(c^2) and mean(g c) from a second.  A thread has the same columns in every
-// row and keeps their dw and db in registers (in shared memory where a block of
-// 1024 threads has 64 registers each, see kAccShared).  A block leaves the sums
-// over its rows in `partial`, which a second kernel adds up in a fixed order: no
-// atomics, the result does not depend on timing.
+// Bound by memory: one pass over s, dy and ds.  mean(s) and mean(g) come from one
+// sum over the row's threads, mean(c^2) and mean(g c) from a second.  The second sum
+// of a row goes with the first of the next one, so that a row costs one barrier:
+//   B(i)      c and g of row i; its squares and products
+//   A(i + 1)  the sums of row i + 1, which is read again in its turn
+//   barrier
+//   C(i)      dx, and what row i adds to dw and db
+// A thread has the same columns in every row and keeps their dw and db in registers.
+// A block leaves the sums over its rows in `partial`, which a second kernel adds up in
+// a fixed order: no atomics, the result does not depend on timing.
 #include "layer_norm.cuh"
 
 namespace moe {
 namespace {
 
-// Gradients of weight and bias in shared memory: where registers do not hold them beside the rows.
+// Operands that come through the ring (s and dy, and ds where that leaves room for a row more than the two in work), and
+// its rows; two blocks of 256 threads share an SM.
 template <typename T, int R>
-constexpr bool kAccShared = R == 1024;
-// The next row asked for while this one is finished: where registers hold both.
+constexpr int kOperands = R < 1024 ? 3 : 2;
 template <typename T, int R>
-constexpr bool kAhead = R < 1024 && (sizeof(T) == 2 || R < 512);
+constexpr int kStagesOf = [] {
+  const int row = ln_rows(R) * 16 * R * (int)sizeof(T) * kOperands<T, R>, most = (R <= 512 ? 220 / (512 / ln_block(R)) - 2 : 220) * 1024 / row;
+  return most < 4 ? most : 4;
+}();
 
-template <int VEC>
-MOE_DEV void add_shared(float* p, const float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-    F8 t = load8(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t.v[i] += f[i];
-    store8(p, t);
-  } else {
-    *p += f[0];
-  }
-}
-
-template <typename ST, int R, int C, int VEC>
-__global__ void __launch_bounds__(R == 32 ? 128 : R) layer_norm_grad_kernel(LayerNormGradArgs a) {
-  constexpr bool SHARED = kAccShared<ST, R>, AHEAD = kAhead<ST, R>;
-  __shared__ float red[2][2][32];
-  // SHARED: [2][d] sums; R == 32: the warps' sums at the end, [4][2][d]
-  extern __shared__ float4 sums4[];
-  float* sums = reinterpret_cast<float*>(sums4);
+template <typename ST, int R, bool ODD>
+__global__ void __launch_bounds__(ln_block(R), R <= 512 ? 512 / ln_block(R) : 1) layer_norm_grad_kernel(LayerNormGradArgs a) {
+  constexpr int kRows = ln_rows(R), S = kStagesOf<ST, R>, kOps = kOperands<ST, R>;
+  constexpr int kSlot = 16 * R * (int)sizeof(ST);  // bytes of a row
+  constexpr bool AHEAD = S >= 3;    // the next row's sums go with this one's
+  constexpr bool CACHE = R < 1024;  // weight, c and g in registers (else read again)
+  __shared__ RowRed<R, 4> red[2];
+  extern __shared__ float4 ring4[];  // [kRows][S][kOps] rows; at the end [kRows][2][16 R] sums
+  uint8_t* ring = reinterpret_cast<uint8_t*>(ring4);
   follow();
-  constexpr int kRows = R == 32 ? 4 : 1;
-  const int tid = R == 32 ? threadIdx.x & 31 : threadIdx.x, group = R == 32 ? threadIdx.x >> 5 : 0;
-  const int stride = gridDim.x * kRows;
-  const ST* s_in = static_cast<const ST*>(a.s);
-  const ST* dy_in = static_cast<const ST*>(a.dy);
-  const ST* ds_in = static_cast<const ST*>(a.ds);
-  ST* dx = static_cast<ST*>(a.dx);
+  const int tid = threadIdx.x % R, group = threadIdx.x / R;
+  const int stride = gridDim.x * kRows, first = blockIdx.x * kRows + group;
+  const Windows<R, ODD> win(tid, first, a.d);
+  const size_t n = (size_t)a.T * a.d;
+  const bool with_ds = a.ds && a.dx;
   const float inv_d = 1.0f / (float)a.d;
+  uint8_t* here = ring + group * S * kOps * kSlot + tid * 16;
+  auto from = [&](int k) { return static_cast<const ST*>(k == 0 ? a.s : k == 1 ? a.dy : a.ds); };
 
-  Chunk<ST, VEC> rs[C], rdy[C], rds[C];
+  auto issue = [&](int it, int slot) {  // the copies of the group's it-th row
+    const long long row = first + (long long)it * stride;
+    if (row < a.T) {
+      const size_t lo = (size_t)row * a.d;
+      const uint32_t to = smem_u32(here) + slot * kOps * kSlot;
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    rs[j].zero();
-    rdy[j].zero();
-    rds[j].zero();
-  }
-  auto load_row = [&](int row) {
-    const size_t lo = (size_t)row * a.d;
+      for (int k = 0; k < kOps; ++k) {
+        if (k == 2 && !with_ds) break;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = (tid + j * R) * VEC;
-      if (c < a.d) {
-        rs[j].load(s_in + lo + c);
-        rdy[j].load(dy_in + lo + c);
-        if (ds_in && dx) rds[j].load(ds_in + lo + c);
+        for (int o = 0; o < 2; ++o)
+          if (win.in[o]) win.copy(to + k * kSlot, from(k), lo, o, n);
       }
     }
+    copies_end();
   };
-  float dw[SHARED ? 1 : C][VEC], db[SHARED ? 1 : C][VEC];
-  if (SHARED) {
-    for (int k = threadIdx.x; k < 2 * a.d; k += R) sums[k] = 0.f;
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int j = 0; j < (SHARED ? 1 : C); ++j)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) dw[j][i] = db[j][i] = 0.f;
-  }
+  auto value = [&](int slot, int k, int o) {
+    F8 f = win.template take<ST>(here + (slot * kOps + k) * kSlot, o);
+    win.mask(o, f);
+    return f;
+  };
 
-  int row = blockIdx.x * kRows + group;
-  if (row < a.T) load_row(row);
-  for (; row < a.T; row += stride) {
-    const size_t lo = (size_t)row * a.d;
-    Chunk<ST, VEC> cs[C], cdy[C], cds[C];
-    float sum[2] = {0.f, 0.f};  // s and g
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = (tid + j * R) * VEC;
-      cs[j] = rs[j];
-      cdy[j] = rdy[j];
-      cds[j] = rds[j];
-      if (c < a.d) {
-        float w[VEC];
-        load_param<VEC>(w, a.w, a.w_dtype, c, 1.f);
+  for (int i = 0; i < S; ++i) issue(i, i);
+  F8 dw[2], db[2], w[2];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          sum[0] += cs[j].get(i);
-          sum[1] += cdy[j].get(i) * w[i];
-        }
-      }
-    }
-    if (AHEAD && row + stride < a.T) load_row(row + stride);
-    row_sums<R>(sum, &red[0]);
-    const float mean = sum[0] * inv_d, g_mean = sum[1] * inv_d;
-    sum[0] = sum[1] = 0.f;  // c^2 and g c
+  for (int o = 0; o < 2; ++o) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = (tid + j * R) * VEC;
-      if (c < a.d) {
-        float w[VEC];
-        load_param<VEC>(w, a.w, a.w_dtype, c, 1.f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float v = cs[j].get(i) - mean;
-          sum[0] += v * v;
-          sum[1] += cdy[j].get(i) * w[i] * v;
-        }
-      }
-    }
-    row_sums<R>(sum, &red[1]);
-    const float rstd = rsqrtf(sum[0] * inv_d + a.eps);
-    const float gn_mean = sum[1] * rstd * inv_d;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int c = (tid + j * R) * VEC;
-      if (c < a.d) {
-        float w[VEC], n[VEC];
-        load_param<VEC>(w, a.w, a.w_dtype, c, 1.f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float dy = cdy[j].get(i);
-          n[i] = (cs[j].get(i) - mean) * rstd;
-          w[i] = rstd * (dy * w[i] - g_mean - n[i] * gn_mean) + cds[j].get(i);
-          n[i] *= dy;
-        }
-        if (dx) Chunk<ST, VEC>::store(dx + lo + c, w);
-        if (SHARED) {
-          add_shared<VEC>(sums + c, n);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) n[i] = cdy[j].get(i);
-          add_shared<VEC>(sums + a.d + c, n);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            dw[SHARED ? 0 : j][i] += n[i];
-            db[SHARED ? 0 : j][i] += cdy[j].get(i);
-          }
-        }
-      }
-    }
-    if (!AHEAD && row + stride < a.T) load_row(row + stride);
+    for (int i = 0; i < 8; ++i) dw[o].v[i] = db[o].v[i] = 0.f;
+    if (CACHE) w[o] = param_of(win, a.w, a.w_dtype, o, 1.f);
   }
-  if (!a.dw && !a.db) return;
-  float* to = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  if (SHARED) {
-    __syncthreads();
-    for (int k = threadIdx.x; k < 2 * a.d; k += R) to[k] = sums[k];
-  } else {
-    float* at = R == 32 ? sums + group * 2 * a.d : to;
+  auto grad = [&](int slot, int o) {  // g = dy w
+    F8 y = value(slot, 1, o);
+    const F8 wo = CACHE ? w[o] : param_of(win, a.w, a.w_dtype, o, 1.f);
 #pragma unroll
-    for (int j = 0; j < (SHARED ? 1 : C); ++j) {
-      const int c = (tid + j * R) * VEC;
-      if (c < a.d) {
+    for (int i = 0; i < 8; ++i) y.v[i] *= wo.v[i];
+    return y;
+  };
+  // A: the sums of s and g
+  auto first_sums = [&](int row, int slot, float& s, float& g) {
+    s = g = 0.f;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          at[c + i] = dw[j][i];
-          at[a.d + c + i] = db[j][i];
+    for (int o = 0; o < 2; ++o)
+      if (win.in[o] && row < a.T) {
+        const F8 x = value(slot, 0, o), y = grad(slot, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x.v[i], g += y.v[i];
+      }
+  };
+
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};  // c^2 and g c of this row, s and g of the next
+  int base = blockIdx.x * kRows, slot = 0, parity = 0;
+  copies_wait<S - 1>();
+  first_sums(base + group, 0, sum[2], sum[3]);
+  ln_row_sums<R>(sum, red[1]);
+  for (int it = 0; base < a.T; base += stride, ++it) {
+    const int row = base + group;
+    const bool live = kRows == 1 || row < a.T;
+    const size_t lo = (size_t)row * a.d;
+    const int next = slot + 1 == S ? 0 : slot + 1;
+    const float mean = sum[2] * inv_d, g_mean = sum[3] * inv_d;
+    F8 c[2], g[2];
+    Raw<ST> late[2];  // ds where the ring does not hold it
+    sum[0] = sum[1] = 0.f;
+    auto centred = [&](int o) {
+      c[o] = value(slot, 0, o);
+      g[o] = grad(slot, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[o].v[i] -= mean;
+      win.mask(o, c[o]);
+    };
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      if (win.in[o] && live) {
+        if (kOps == 2 && with_ds) win.load(late[o], from(2), lo, o, n);
+        centred(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[0] += c[o].v[i] * c[o].v[i];
+          sum[1] += g[o].v[i] * c[o].v[i];
         }
       }
+    if (AHEAD) {
+      copies_wait<AHEAD ? S - 2 : 0>();
+      first_sums(row + stride, next, sum[2], sum[3]);
     }
-    if (R == 32) {
-      __syncthreads();
-      for (int k = threadIdx.x; k < 2 * a.d; k += 128) {
-        float v = sums[k];
-        for (int g = 1; g < kRows; ++g) v += sums[g * 2 * a.d + k];
-        to[k] = v;
+    ln_row_sums<R>(sum, red[parity]);
+    parity ^= 1;
+    const float rstd = rsqrtf(sum[0] * inv_d + a.eps);
+    // dx = rstd g - rstd mean(g) - c rstd^2 mean(g n) + ds
+    const float shift = -rstd * g_mean, slope = -rstd * rstd * (sum[1] * rstd * inv_d);
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      if (win.in[o] && live) {
+        if (!CACHE) centred(o);
+        const F8 y = value(slot, 1, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw[o].v[i] = fmaf(y.v[i], c[o].v[i] * rstd, dw[o].v[i]);
+          db[o].v[i] += y.v[i];
+        }
+        if (a.dx) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[o].v[i] = fmaf(rstd, g[o].v[i], fmaf(slope, c[o].v[i], shift));
+          if (with_ds) {
+            const F8 e = kOps == 2 ? late[o].get() : value(slot, 2, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[o].v[i] += e.v[i];
+          }
+          win.store(static_cast<ST*>(a.dx), lo, o, g[o]);
+        }
       }
+    issue(it + S, slot);
+    slot = next;
+    if (!AHEAD) {
+      copies_wait<S - 1>();
+      sum[0] = sum[1] = 0.f;
+      first_sums(row + stride, slot, sum[2], sum[3]);
+      ln_row_sums<R>(sum, red[parity]);
+      parity ^= 1;
     }
+  }
+  copies_wait<0>();
+  if (!a.dw && !a.db) return;
+  // The groups' sums side by side, by window, then added up and written by column.
+  float* sums = reinterpret_cast<float*>(ring4);
+  __syncthreads();  // (the ring is done with)
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    float* at = sums + group * 32 * R + (tid + o * R) * 8;
+    store8(at, dw[o]);
+    store8(at + 16 * R, db[o]);
+  }
+  __syncthreads();
+  float* to = a.partial + (size_t)blockIdx.x * 2 * a.d;
+  for (int k = threadIdx.x; k < 2 * a.d; k += ln_block(R)) {
+    const int half = k >= a.d, c = k - half * a.d;
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int head = ODD ? (int)((long long)(blockIdx.x * kRows + r) * a.d & 7) : 0;
+      v += sums[r * 32 * R + half * 16 * R + c + head];
+    }
+    to[k] = v;
   }
 }
 
@@ -193,8 +203,14 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_sum_kernel(const float* 
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < 2 * d) {
-#pragma unroll 4
-    for (int r = threadIdx.y; r < rows; r += 32) v += partial[(size_t)r * 2 * d + c];
+    constexpr int kBatch = 10;  // in flight at once: 304 partial rows
+    for (int r0 = threadIdx.y; r0 < rows; r0 += 32 * kBatch) {
+      float x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) x[i] = r0 + 32 * i < rows ? partial[(size_t)(r0 + 32 * i) * 2 * d + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v += x[i];
+    }
   }
   part[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
@@ -210,38 +226,33 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_sum_kernel(const float* 
   }
 }
 
-template <typename ST, int R, int C, int VEC>
-cudaError_t launch(const LayerNormGradArgs& a, cudaStream_t st) {
-  constexpr int kBlock = R == 32 ? 128 : R, kRows = kBlock / R;
-  constexpr int kWidest = R * C * VEC;
-  constexpr size_t kMost = kAccShared<ST, R> ? (size_t)2 * kWidest * 4 : R == 32 ? (size_t)8 * kWidest * 4 : 0;
-  const auto kernel = layer_norm_grad_kernel<ST, R, C, VEC>;
-  const size_t smem = kAccShared<ST, R> ? (size_t)2 * a.d * 4 : R == 32 ? (size_t)8 * a.d * 4 : 0;
-  const cudaError_t err = allow(kernel, smem, kMost);
-  if (err != cudaSuccess) return err;
-  int grid = (a.T + kRows - 1) / kRows;
-  if (grid > 128) {
-    static const int resident = resident_blocks(kernel, kBlock, kMost);
-    if (grid > resident) grid = resident;
-    if (grid > kLayerNormPartials) grid = kLayerNormPartials;
-  }
-  const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), smem, st, a);
-  if (e != cudaSuccess || (!a.dw && !a.db)) return e;
-  return launch_after(layer_norm_grad_sum_kernel, (2 * a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial,
-                      grid, a.d, a.dw, a.db, a.w_dtype);
-}
-template <typename ST, int VEC>
-cudaError_t by_width(const LayerNormGradArgs& a, cudaStream_t st) {
-  if (a.d <= 512) return launch<ST, 32, 16 / VEC, VEC>(a, st);
-  if (a.d <= 1024) return launch<ST, 128, 8 / VEC, VEC>(a, st);
-  if (a.d <= 2048) return launch<ST, 128, 16 / VEC, VEC>(a, st);
-  if (a.d <= 4096) return launch<ST, 256, 16 / VEC, VEC>(a, st);
-  if (a.d <= 8192) return launch<ST, 512, 16 / VEC, VEC>(a, st);
-  return launch<ST, 1024, 16 / VEC, VEC>(a, st);
-}
+template <typename ST, bool ODD>
+struct Backward {
+  template <int R>
+  struct Launch {
+    static cudaError_t run(const LayerNormGradArgs& a, cudaStream_t st) {
+      constexpr int kBlock = ln_block(R), kRows = ln_rows(R);
+      constexpr size_t per = kStagesOf<ST, R> * kOperands<ST, R> * sizeof(ST), smem = (size_t)kRows * 16 * R * per;
+      static_assert(kStagesOf<ST, R> >= 1 && smem <= 224 * 1024 && per >= 8, "the ring; the sums of two rows of fp32 in it");
+      const auto kernel = layer_norm_grad_kernel<ST, R, ODD>;
+      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      int grid = (a.T + kRows - 1) / kRows;
+      if (grid > 128) {
+        static const int resident = min(resident_blocks(kernel, kBlock, smem), kLayerNormPartials) / 8 * 8;
+        if (grid > resident) grid = resident;
+      }
+      const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), smem, st, a);
+      if (e != cudaSuccess || (!a.dw && !a.db)) return e;
+      return launch_after(layer_norm_grad_sum_kernel, (2 * a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial,
+                          grid, a.d, a.dw, a.db, a.w_dtype);
+    }
+  };
+};
 template <typename ST>
 cudaError_t typed(const LayerNormGradArgs& a, cudaStream_t st) {
-  return a.d % 8 == 0 ? by_width<ST, 8>(a, st) : by_width<ST, 1>(a, st);
+  return a.d % 8 == 0 ? by_width<Backward<ST, false>::template Launch>(a, st)
+                      : by_width<Backward<ST, true>::template Launch>(a, st);
 }
 
 }  // namespace

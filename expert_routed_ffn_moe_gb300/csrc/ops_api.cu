@@ -52,7 +52,7 @@ int moe_layer_norm(const void* x, int x_dtype, const void* residual, int s_dtype
   if (T < 0 || d <= 0 || !stream_dtype(x_dtype) || !stream_dtype(s_dtype) || !stream_dtype(w_dtype) ||
       !stream_dtype(y_dtype) || !(eps >= 0.f))
     return MOE_ERR_ARG;
-  if (d > kMaxNormWidth || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (!layer_norm_takes(d) || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !y) return MOE_ERR_ARG;
   if (!aligned16(x, residual, weight, bias, s_out, y)) return MOE_ERR_ALIGN;
@@ -67,7 +67,7 @@ int moe_layer_norm_backward(const void* s, const void* weight, const void* dy, c
                             int T, int d, float eps, void* dx, void* dweight, void* dbias, void* workspace,
                             void* stream) {
   if (T < 0 || d <= 0 || !stream_dtype(dtype) || !stream_dtype(w_dtype) || !(eps >= 0.f)) return MOE_ERR_ARG;
-  if (d > kMaxNormWidth || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (!layer_norm_takes(d) || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
   const bool sums = dweight || dbias;
   // (without rows dx is a tensor of no values, which may have no address)
   if (T > 0 && ((!dx && !sums) || !s || !dy || (sums && !workspace))) return MOE_ERR_ARG;

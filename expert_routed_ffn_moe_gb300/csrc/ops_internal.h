@@ -7,6 +7,8 @@
 namespace moe {
 
 // layer_norm.cu
+// Widths that the kernels take: 2048 windows of 8 columns, which rows that are not aligned may exceed by 7 columns.
+inline bool layer_norm_takes(int d) { return d <= kMaxNormWidth - (d % 8 ? 7 : 0); }
 struct LayerNormArgs {
   const void *x, *res, *w, *b;
   void *s, *y;

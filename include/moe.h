@@ -423,9 +423,9 @@ void moe_ffn_destroy(moe_ffn* ctx);
  * residual and s_out [T, d] (s_dtype; either may be NULL), weight and bias [d]
  * (w_dtype; NULL: 1 and 0), y [T, d] (y_dtype).  Every dtype is MOE_F32 or
  * MOE_BF16.  s_out may be residual itself, and y may be x where their dtypes are
- * the same; no other output may overlap an input.  d is any width up to 16384 and
- * T at most 2^30, MOE_ERR_UNSUPPORTED beyond; MOE_ERR_ARG for a dtype not listed
- * or eps < 0.  No workspace, no context. */
+ * the same; no other output may overlap an input.  d is any width up to 16377, or
+ * a multiple of 8 up to 16384, and T at most 2^30, MOE_ERR_UNSUPPORTED beyond;
+ * MOE_ERR_ARG for a dtype not listed or eps < 0.  No workspace, no context. */
 int moe_layer_norm(const void* x, int x_dtype, const void* residual, int s_dtype, const void* weight, const void* bias,
                    int w_dtype, int T, int d, float eps, void* s_out, void* y, int y_dtype, void* stream);
 

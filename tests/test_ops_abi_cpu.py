@@ -57,7 +57,7 @@ def test_layer_norm_arguments(lib):
     for kw in (dict(x=None), dict(y=None), dict(xt=M), dict(st=9), dict(wt=M), dict(yt=M), dict(T=-1), dict(d=0),
                dict(eps=-1.0), dict(eps=float("nan"))):
         assert norm(**kw) == ARG, kw
-    assert norm(d=16385) == UNSUP and norm(T=(1 << 30) + 1) == UNSUP
+    assert norm(d=16385) == UNSUP and norm(d=16378) == UNSUP and norm(d=16383) == UNSUP and norm(T=(1 << 30) + 1) == UNSUP
     for kw in (dict(x=P(8)), dict(w=P(20)), dict(b=P(2)), dict(y=P(24))):
         assert norm(**kw) == ALIGN, kw
 
