@@ -479,23 +479,49 @@ int cluster_of(int tiles, int KB, int sms) {
 }
 
 template <bool MX, int KIND, int NT>
-cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
-  const int depth = MX ? 128 : 64;
-  const int tiles = (p.N + kRows - 1) / kRows, C = cluster_of(tiles, (p.K + depth - 1) / depth, e.sms);
-  p.log_cluster = C == 8 ? 3 : C >> 1;
+cudaLaunchConfig_t config(int tiles, int C, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * C);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_of(MX, KIND, NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = C;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+  return cfg;
+}
+// Clusters of 8 on SMs of their own: half of what runs at a time, where two CTAs share an SM.
+template <bool MX, int KIND, int NT>
+int lone_clusters() {
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = config<MX, KIND, NT>(1, kMaxCluster, at);
+  cfg.numAttrs = 1;
+  int n = 0, per = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, ffn_skinny_kernel<MX, KIND, NT>, &cfg) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, ffn_skinny_kernel<MX, KIND, NT>, kThreads, cfg.dynamicSmemBytes) !=
+          cudaSuccess || per < 1)
+    return 0;
+  return n / per;
+}
+template <bool MX, int KIND, int NT>
+cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
+  const int depth = MX ? 128 : 64;
+  const int tiles = (p.N + kRows - 1) / kRows;
+  int C = cluster_of(tiles, (p.K + depth - 1) / depth, e.sms);
+  if constexpr (KIND == kLinear || KIND == kLinearDx) {
+    // A call is this kernel alone, and clusters of 8 that have to share SMs, as they find no eight free ones in their part
+    // of the device, cost more than they bring: 16 tiles (T = 16, d = 4096 to 2048) 13.6 us with 8, 9.0 with 4; 8 tiles
+    // (4096 to 1024) 6.8 with 8, 8.0 with 4.
+    static const int lone = lone_clusters<MX, KIND, NT>();
+    if (C == 8 && tiles > lone) C = 4;
+  }
+  p.log_cluster = C == 8 ? 3 : C >> 1;
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = config<MX, KIND, NT>(tiles, C, at);
+  cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, ffn_skinny_kernel<MX, KIND, NT>, p);
 }
 template <bool MX, int KIND>

@@ -19,24 +19,9 @@ namespace moe {
 constexpr int ln_rows(int R) { return R < 256 ? 256 / R : 1; }
 constexpr int ln_block(int R) { return ln_rows(R) * R; }
 
-// Rows come through a ring in shared memory, filled by asynchronous copies of 16
-// bytes some rows ahead; a thread copies the windows that it reads itself, and so
-// waits for its own copies alone.
-// The rest of the 16 bytes becomes 0.  A window of fp32 is two copies of half its sectors each, of which the second finds
-// the first's in L1 (through L2 alone: d = 4096 fp32 backward 260 us for 179; a window of bf16 gains from passing L1 by,
-// 94 for 98).
-template <typename T>
-MOE_DEV void copy16(uint32_t to, const T* from, int bytes) {
-  if (sizeof(T) == 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-}
-MOE_DEV void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-MOE_DEV void copies_wait() {  // all but the last N groups of this thread
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// Rows come through a ring in shared memory, filled by asynchronous copies some rows
+// ahead; a thread copies the windows that it reads itself, and so waits for its own
+// copies alone.
 
 // A thread's windows; the same in every row that it walks over.
 template <int R, bool ODD>

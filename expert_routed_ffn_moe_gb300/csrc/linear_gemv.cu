@@ -1,0 +1,213 @@
+// The product with its epilogue for one to four tokens: y = act(x w^T + bias) + residual.
+//
+// Bound by reading the weights once, on the CUDA cores: each 16 bytes of weights are 8
+// multiply-adds per token, below what the SMs can do, and rows can be dealt out to all
+// of them evenly, which tiles of 128 rows cannot (4096 rows are 32 tiles).  A block of
+// 16 warps per SM; a group of 1 to 16 of its warps has a contiguous range of rows, eight
+// at a time, and its warps take the rows' length in turn, 256 columns each (16 bytes per
+// lane).  Weights come through each warp's own ring of three steps in shared memory by
+// bulk copies, a row's 512 bytes each (loads into registers one step ahead do not cover
+// the memory's latency, and 16-byte copies cost more instructions than the sums).  A
+// warp's sums of eight rows meet by nine exchanges, the group's warps' in shared memory,
+// in order; then one thread finishes each result.
+#include "ops_internal.h"
+#include "rows_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kRows = 8, kCols = 256, kSteps = 3;
+constexpr int kStepBytes = kRows * kCols * 2;  // of a warp
+constexpr size_t kRingBytes = (size_t)kWarps * kSteps * kStepBytes;
+
+struct GemvArgs {
+  const __nv_bfloat16 *x, *w;
+  LinearForwardArgs f;
+  int K, N, act;
+  int log_split;  // warps of a group: 1 << log_split
+  DevCtl ctl;
+};
+
+MOE_DEV void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(from), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// a + b * c for two neighbouring values at once.
+MOE_DEV void fma2(float2& a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)),
+        "l"(*reinterpret_cast<const uint64_t*>(&a)));
+  a = *reinterpret_cast<const float2*>(&r);
+}
+MOE_DEV float2 two(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
+
+// Sums over the warp of eight values: lane l gets that of value l / 4.
+MOE_DEV float warp_sum8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = (lane & 16) != 0;
+    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = (lane & 8) != 0;
+    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+  }
+  const bool up = (lane & 4) != 0;
+  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+template <int T>
+__global__ void __launch_bounds__(kThreads, 1) linear_gemv_kernel(const __grid_constant__ GemvArgs a) {
+  __shared__ float part[2][kWarps][T][kRows];
+  __shared__ uint64_t full[kWarps][kSteps], never;
+  extern __shared__ __align__(128) uint8_t ring[];  // [kWarps][kSteps][kRows][kCols]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane < kSteps) mbar_init(&full[warp][lane], 1);
+  if (threadIdx.x == 0) mbar_init(&never, 1);
+  fence_mbar_init();
+  __syncthreads();
+  follow();
+
+  const int split = 1 << a.log_split, groups = kWarps >> a.log_split;
+  const int group = warp >> a.log_split, sub = warp & (split - 1);
+  const int all = gridDim.x * groups;
+  auto first_row = [&](int g) { return (int)((long long)a.N * (blockIdx.x * groups + g) / all); };
+  const int r0 = first_row(group), r1 = first_row(group + 1);
+  const int chunks = ((a.N + all - 1) / all + kRows - 1) / kRows;  // (the same for all: the block has barriers)
+  const int stride = split * kCols, segs = (a.K + stride - 1) / stride;
+  const int c0 = sub * kCols;
+  uint8_t* mine = ring + warp * kSteps * kStepBytes;
+  bool ok = true;
+  if (a.ctl.stall) ok = mbar_wait(&never, 0, a.ctl);  // test hook: nothing arrives there
+
+  // The copies of the next step: eight rows' 256 columns, as far as there are any.
+  int ahead_chunk = 0, ahead_seg = 0, ahead_slot = 0, issued = 0;
+  auto issue = [&]() {
+    if (ahead_chunk >= chunks) return;
+    const int row = r0 + ahead_chunk * kRows, c = c0 + ahead_seg * stride;
+    const int rows = max(0, min(kRows, r1 - row)), bytes = max(0, min(kCols, a.K - c)) * 2;
+    uint64_t* bar = &full[warp][ahead_slot];
+    if (lane == 0) mbar_expect_tx(bar, rows * bytes);
+    __syncwarp();
+    if (lane < rows && bytes)
+      bulk_copy(smem_u32(mine + ahead_slot * kStepBytes) + lane * kCols * 2, a.w + (size_t)(row + lane) * a.K + c, bytes, bar);
+    ++issued;
+    if (++ahead_seg == segs) ahead_seg = 0, ++ahead_chunk;
+    if (++ahead_slot == kSteps) ahead_slot = 0;
+  };
+  if (ok) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) issue();
+  }
+  int slot = 0, parity = 0, used = 0;
+
+  // What this thread finishes of every eight rows: row i_out of group g, token t_out.
+  const int g = threadIdx.x / (T * kRows), t_out = threadIdx.x / kRows % T, i_out = threadIdx.x % kRows;
+  static_assert(kWarps * T * kRows <= kThreads, "a thread per result");
+  const int g0 = first_row(g) + i_out, g1 = g < groups ? first_row(g + 1) : 0;
+  const LinearForwardArgs& f = a.f;
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    // its bias and residual, asked for before the sums are there
+    const int n = g0 + chunk * kRows;
+    const size_t at = (size_t)t_out * a.N + n;
+    float bias = 0.f, res = 0.f;
+    if (n < g1) {
+      if (f.bias)
+        bias = f.bias_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(f.bias)[n])
+                                        : static_cast<const float*>(f.bias)[n];
+      if (f.res)
+        res = f.y_dtype == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(f.res)[at])
+                                    : static_cast<const float*>(f.res)[at];
+    }
+    float2 acc[T][kRows];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) acc[t][i] = make_float2(0.f, 0.f);
+    for (int seg = 0; seg < segs; ++seg) {
+      const int c = c0 + seg * stride + lane * 8;
+      const bool in = c < a.K;
+      uint4 x[T];
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        x[t] = in ? *reinterpret_cast<const uint4*>(a.x + (size_t)t * a.K + c) : make_uint4(0, 0, 0, 0);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, a.ctl));
+      if (!ok) continue;
+      ++used;
+      if (in) {
+        const uint4* w = reinterpret_cast<const uint4*>(mine + slot * kStepBytes) + lane;
+        float2 xf[T][4];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          xf[t][0] = two(x[t].x), xf[t][1] = two(x[t].y), xf[t][2] = two(x[t].z), xf[t][3] = two(x[t].w);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {  // (rows past the group's last are not used)
+          const uint4 v = w[i * (kCols / 8)];
+          const float2 vf[4] = {two(v.x), two(v.y), two(v.z), two(v.w)};
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fma2(acc[t][i], vf[e], xf[t][e]);
+        }
+      }
+      __syncwarp();
+      issue();  // (into the step just read)
+      if (++slot == kSteps) slot = 0, parity ^= 1;
+    }
+    float(&to)[kWarps][T][kRows] = part[chunk & 1];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      float v[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) v[i] = acc[t][i].x + acc[t][i].y;
+      const float s = warp_sum8(v);
+      if ((lane & 3) == 0) to[warp][t][lane >> 2] = s;
+    }
+    __syncthreads();  // (a part's memory is written again two chunks later, after the next barrier)
+    if (n < g1) {
+      float v = 0.f;
+      for (int s = 0; s < split; ++s) v += to[g * split + s][t_out][i_out];
+      v += bias;
+      if (f.pre) f.pre[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      with_act_or_none(a.act, [&](auto act) { v = act_value<decltype(act)::value>(v); });
+      v += res;
+      if (f.y_dtype == MOE_BF16)
+        put(static_cast<__nv_bfloat16*>(f.y) + at, v);
+      else
+        put(static_cast<float*>(f.y) + at, v);
+    }
+  }
+  // after a wait that ran out: what is still in flight lands before the block leaves
+  for (; used < issued; ++used) mbar_wait(&full[warp][used % kSteps], used / kSteps & 1, drain_ctl(a.ctl));
+}
+
+}  // namespace
+
+cudaError_t launch_linear_gemv(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& f, cudaStream_t st) {
+  GemvArgs a{static_cast<const __nv_bfloat16*>(f.x), static_cast<const __nv_bfloat16*>(f.w), f, s.k, s.n, s.act, 0, e.ctl};
+  while (a.log_split < 4 && (kCols << (a.log_split + 1)) <= s.k) ++a.log_split;
+  const int groups = kWarps >> a.log_split;
+  int grid = (s.n + groups - 1) / groups;
+  if (grid > e.sms) grid = e.sms;
+  auto launch = [&](auto kernel) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+    return err != cudaSuccess ? err : launch_after(kernel, grid, dim3(kThreads), kRingBytes, st, a);
+  };
+  switch (s.T) {
+    case 1: return launch(linear_gemv_kernel<1>);
+    case 2: return launch(linear_gemv_kernel<2>);
+    case 3: return launch(linear_gemv_kernel<3>);
+    case 4: return launch(linear_gemv_kernel<4>);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moe

@@ -230,7 +230,9 @@ int moe_linear_forward(moe_linear* ctx, const void* x, int T, const void* weight
   const LinearForwardArgs a{x, weight, bias, residual, y, static_cast<uint16_t*>(pre), bias_dtype, y_dtype};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ++ctx->launches;
-  return cuda_code(few_tokens(s) ? launch_linear_stream(ctx->eng, s, a, st) : launch_linear_tiles(ctx->eng, s, a, st));
+  return cuda_code(gemv_tokens(s) ? launch_linear_gemv(ctx->eng, s, a, st)
+                   : few_tokens(s) ? launch_linear_stream(ctx->eng, s, a, st)
+                                   : launch_linear_tiles(ctx->eng, s, a, st));
 }
 
 int moe_linear_backward(moe_linear* ctx, const void* x, const void* pre, int T, const void* weight, const void* dy,
