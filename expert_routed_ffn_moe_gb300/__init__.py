@@ -809,21 +809,27 @@ class TokenDispatch:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.sort(idx, counts, offsets, perm, slot)
-        device, int32 = _device(idx, "idx"), torch.int32
+        device, int32, E, k = _device(idx, "idx"), torch.int32, self.n_experts, self.top_k
         pi, T = self._picks(idx, "idx", device, int32)
-        E = self.n_experts
-
-        def output(t, name, shape):
-            if t is None:
-                t = torch.empty(shape, dtype=int32, device=idx.device)
-                return t, t.data_ptr()
-            return t, _checked(t, name, shape, device, int32)
-
-        counts, pc = output(counts, "counts", (E,))
-        offsets, po = output(offsets, "offsets", (E + 1,))
-        perm, pp = output(perm, "perm", (T * self.top_k,))
-        slot, psl = output(slot, "slot", (T, self.top_k))
-        code = (_lib or lib()).moe_sort_tokens(pi, T, self.top_k, E, pc, po, pp, psl, _handle(None, device))
+        here = idx.device
+        if counts is None:
+            counts = torch.empty(E, dtype=int32, device=here)
+        else:
+            _checked(counts, "counts", (E,), device, int32)
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=int32, device=here)
+        else:
+            _checked(offsets, "offsets", (E + 1,), device, int32)
+        if perm is None:
+            perm = torch.empty(T * k, dtype=int32, device=here)
+        else:
+            _checked(perm, "perm", (T * k,), device, int32)
+        if slot is None:
+            slot = torch.empty_like(idx)
+        else:
+            _checked(slot, "slot", (T, k), device, int32)
+        code = (_lib or lib()).moe_sort_tokens(pi, T, k, E, counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
+                                               slot.data_ptr(), _handle(None, device))
         if code:
             _check(code, "moe_sort_tokens")
         return counts, offsets, perm, slot
@@ -885,15 +891,20 @@ class TokenDispatch:
         pr = _checked(rows, "rows", (n, d), device)
         psl, T = self._picks(slot, "slot", device, torch.int32)
         pdy, pw = _checked(dy, "dy", (T, d), device), _checked(w, "w", (T, self.top_k), device, torch.float32)
-
-        def output(t, name, like):
-            if t is None:
-                t = torch.empty_like(like)
-                return t, t.data_ptr()
-            return (None, None) if t is False else (t, _checked(t, name, like.shape, device, like.dtype))
-
-        drows, pdr = output(drows, "drows", rows)
-        dw, pdw = output(dw, "dw", w)
+        if drows is None:
+            drows = torch.empty_like(rows)
+            pdr = drows.data_ptr()
+        elif drows is False:
+            drows = pdr = None
+        else:
+            pdr = _checked(drows, "drows", rows.shape, device, rows.dtype)
+        if dw is None:
+            dw = torch.empty_like(w)
+            pdw = dw.data_ptr()
+        elif dw is False:
+            dw = pdw = None
+        else:
+            pdw = _checked(dw, "dw", w.shape, device, w.dtype)
         code = (_lib or lib()).moe_combine_backward(pdy, _DTYPES[dy.dtype], pr, _DTYPES[rows.dtype], n, psl, pw, T,
                                                     self.top_k, d, pdr, pdw, _handle(None, device))
         if code:

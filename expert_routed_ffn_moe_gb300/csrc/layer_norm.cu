@@ -245,7 +245,8 @@ struct Odd {
       constexpr int kBlock = ln_block(R), kRows = ln_rows(R);
       constexpr size_t smem = (size_t)kRows * kStagesOf<XT, ST, R> * 16 * R * (sizeof(XT) + sizeof(ST));
       const auto kernel = layer_norm_odd_kernel<XT, ST, R>;
-      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      static std::atomic<uint64_t> allowed{0};
+      const cudaError_t err = allow_once(kernel, smem, allowed);
       if (err != cudaSuccess) return err;
       int grid = (a.T + kRows - 1) / kRows;
       if (grid > 128) {

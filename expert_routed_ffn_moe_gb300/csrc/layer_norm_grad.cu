@@ -235,7 +235,8 @@ struct Backward {
       constexpr size_t per = kStagesOf<ST, R> * kOperands<ST, R> * sizeof(ST), smem = (size_t)kRows * 16 * R * per;
       static_assert(kStagesOf<ST, R> >= 1 && smem <= 224 * 1024 && per >= 8, "the ring; the sums of two rows of fp32 in it");
       const auto kernel = layer_norm_grad_kernel<ST, R, ODD>;
-      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      static std::atomic<uint64_t> allowed{0};
+      const cudaError_t err = allow_once(kernel, smem, allowed);
       if (err != cudaSuccess) return err;
       int grid = (a.T + kRows - 1) / kRows;
       if (grid > 128) {

@@ -33,17 +33,6 @@ MOE_DEV void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint64_t* 
                "l"(from), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// a + b * c for two neighbouring values at once.
-MOE_DEV void fma2(float2& a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<const uint64_t*>(&b)), "l"(*reinterpret_cast<const uint64_t*>(&c)),
-        "l"(*reinterpret_cast<const uint64_t*>(&a)));
-  a = *reinterpret_cast<const float2*>(&r);
-}
-MOE_DEV float2 two(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
-
 // Sums over the warp of eight values: lane l gets that of value l / 4.
 MOE_DEV float warp_sum8(const float (&v)[8]) {
   const int lane = threadIdx.x & 31;
@@ -147,15 +136,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemv_kernel(const __grid_c
         float2 xf[T][4];
 #pragma unroll
         for (int t = 0; t < T; ++t)
-          xf[t][0] = two(x[t].x), xf[t][1] = two(x[t].y), xf[t][2] = two(x[t].z), xf[t][3] = two(x[t].w);
+          xf[t][0] = bf16_two(x[t].x), xf[t][1] = bf16_two(x[t].y), xf[t][2] = bf16_two(x[t].z), xf[t][3] = bf16_two(x[t].w);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {  // (rows past the group's last are not used)
           const uint4 v = w[i * (kCols / 8)];
-          const float2 vf[4] = {two(v.x), two(v.y), two(v.z), two(v.w)};
+          const float2 vf[4] = {bf16_two(v.x), bf16_two(v.y), bf16_two(v.z), bf16_two(v.w)};
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fma2(acc[t][i], vf[e], xf[t][e]);
+            for (int e = 0; e < 4; ++e) acc[t][i] = fma2(vf[e], xf[t][e], acc[t][i]);
         }
       }
       __syncwarp();
@@ -189,6 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemv_kernel(const __grid_c
   for (; used < issued; ++used) mbar_wait(&full[warp][used % kSteps], used / kSteps & 1, drain_ctl(a.ctl));
 }
 
+template <int T>
+cudaError_t launch(const GemvArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t err = allow_once(linear_gemv_kernel<T>, kRingBytes, allowed);
+  return err != cudaSuccess ? err : launch_after(linear_gemv_kernel<T>, grid, dim3(kThreads), kRingBytes, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_gemv(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& f, cudaStream_t st) {
@@ -197,15 +193,11 @@ cudaError_t launch_linear_gemv(const FfnEngine& e, const LinearShape& s, const L
   const int groups = kWarps >> a.log_split;
   int grid = (s.n + groups - 1) / groups;
   if (grid > e.sms) grid = e.sms;
-  auto launch = [&](auto kernel) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
-    return err != cudaSuccess ? err : launch_after(kernel, grid, dim3(kThreads), kRingBytes, st, a);
-  };
   switch (s.T) {
-    case 1: return launch(linear_gemv_kernel<1>);
-    case 2: return launch(linear_gemv_kernel<2>);
-    case 3: return launch(linear_gemv_kernel<3>);
-    case 4: return launch(linear_gemv_kernel<4>);
+    case 1: return launch<1>(a, grid, st);
+    case 2: return launch<2>(a, grid, st);
+    case 3: return launch<3>(a, grid, st);
+    case 4: return launch<4>(a, grid, st);
   }
   return cudaErrorInvalidValue;
 }

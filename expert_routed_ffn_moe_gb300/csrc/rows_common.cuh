@@ -2,6 +2,8 @@
 // sums over its threads, launches that overlap the kernel before.
 #pragma once
 
+#include <atomic>
+
 #include "ffn_internal.h"
 
 namespace moe {
@@ -74,6 +76,27 @@ MOE_DEV float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 MOE_DEV void put(float* p, float v) { *p = v; }
 MOE_DEV void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Two values at once.  (Written out, these are not contracted: a product is rounded before it is added to.)
+MOE_DEV uint64_t bits2(float2 a) { return *reinterpret_cast<const uint64_t*>(&a); }
+MOE_DEV float2 float2_of(uint64_t a) { return *reinterpret_cast<const float2*>(&a); }
+MOE_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return float2_of(r);
+}
+MOE_DEV float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+MOE_DEV float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+MOE_DEV float2 both(float v) { return make_float2(v, v); }
+MOE_DEV float2 bf16_two(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
+
 // The sums over the R threads of a row, in every one of them.  `red` is another
 // half of its memory from one row to the next, so one barrier per row suffices.
 template <int R, int N>
@@ -117,6 +140,18 @@ int resident_blocks(K kernel, int block, size_t smem) {
   return sms * per;
 }
 
+// Sets a kernel's limit on shared memory once for each device (`done`: the devices that have it).
+template <typename K>
+cudaError_t allow_once(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return err;
+}
 // A kernel's limit on shared memory belongs to all its launches, which threads of the host may issue side by side: it
 // is set for the widest rows, never lower for narrower ones.
 template <typename K>
