@@ -745,13 +745,13 @@ class LayerNorm:
         pb = _checked(bias, "bias", (d,), device, None if weight is None else weight.dtype)
         param = weight if weight is not None else bias
         like = x if residual is None else residual
+        if y_dtype != MOE_BF16 and y_dtype != MOE_F32:
+            raise ValueError("y_dtype must be MOE_F32 or MOE_BF16")
         if s_out is None:
             s_out = x if residual is None else torch.empty_like(residual)
             ps = None if residual is None else s_out.data_ptr()
         else:
             ps = _checked(s_out, "s_out", shape, device, like.dtype)
-        if y_dtype != MOE_BF16 and y_dtype != MOE_F32:
-            raise ValueError("y_dtype must be MOE_F32 or MOE_BF16")
         y = torch.empty_like(x, dtype=torch.bfloat16 if y_dtype == MOE_BF16 else torch.float32)
         code = (_lib or lib()).moe_layer_norm(px, _DTYPES[x.dtype], pr, _DTYPES[like.dtype], pw, pb,
                                               MOE_F32 if param is None else _DTYPES[param.dtype], T, d, self.eps, ps,
