@@ -16,7 +16,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kRows = 8, kCols = 256, kSteps = 3;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kRows = 8, kCols = 512, kSteps = 3;
+constexpr int kPieces = kCols / 256;  // of 8 columns per lane
 constexpr int kStepBytes = kRows * kCols * 2;  // of a warp
 constexpr size_t kRingBytes = (size_t)kWarps * kSteps * kStepBytes;
 
@@ -123,20 +124,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemv_kernel(const __grid_c
       for (int i = 0; i < kRows; ++i) acc[t][i] = make_float2(0.f, 0.f);
     for (int seg = 0; seg < segs; ++seg) {
       const int c = c0 + seg * stride + lane * 8;
-      const bool in = c < a.K;
-      uint4 x[T];
+      uint4 x[kPieces][T];
 #pragma unroll
-      for (int t = 0; t < T; ++t)
-        x[t] = in ? *reinterpret_cast<const uint4*>(a.x + (size_t)t * a.K + c) : make_uint4(0, 0, 0, 0);
+      for (int q = 0; q < kPieces; ++q)
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          if (c + q * 256 < a.K) x[q][t] = *reinterpret_cast<const uint4*>(a.x + (size_t)t * a.K + c + q * 256);
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], parity, a.ctl));
       if (!ok) continue;
       ++used;
-      if (in) {
-        const uint4* w = reinterpret_cast<const uint4*>(mine + slot * kStepBytes) + lane;
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        if (c + q * 256 >= a.K) continue;
+        const uint4* w = reinterpret_cast<const uint4*>(mine + slot * kStepBytes) + q * 32 + lane;
         float2 xf[T][4];
 #pragma unroll
-        for (int t = 0; t < T; ++t)
-          xf[t][0] = bf16_two(x[t].x), xf[t][1] = bf16_two(x[t].y), xf[t][2] = bf16_two(x[t].z), xf[t][3] = bf16_two(x[t].w);
+        for (int t = 0; t < T; ++t) {
+          const uint4 v = x[q][t];
+          xf[t][0] = bf16_two(v.x), xf[t][1] = bf16_two(v.y), xf[t][2] = bf16_two(v.z), xf[t][3] = bf16_two(v.w);
+        }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {  // (rows past the group's last are not used)
           const uint4 v = w[i * (kCols / 8)];
@@ -189,7 +195,7 @@ cudaError_t launch(const GemvArgs& a, int grid, cudaStream_t st) {
 
 cudaError_t launch_linear_gemv(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& f, cudaStream_t st) {
   GemvArgs a{static_cast<const __nv_bfloat16*>(f.x), static_cast<const __nv_bfloat16*>(f.w), f, s.k, s.n, s.act, 0, e.ctl};
-  while (a.log_split < 4 && (kCols << (a.log_split + 1)) <= s.k) ++a.log_split;
+  while ((1 << a.log_split) < kWarps && (kCols << (a.log_split + 1)) <= s.k) ++a.log_split;
   const int groups = kWarps >> a.log_split;
   int grid = (s.n + groups - 1) / groups;
   if (grid > e.sms) grid = e.sms;

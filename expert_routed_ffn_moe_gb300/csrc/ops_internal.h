@@ -54,10 +54,11 @@ cudaError_t launch_combine_rows(const RowsArgs& a, cudaStream_t st);
 cudaError_t launch_combine_backward(const RowsArgs& a, cudaStream_t st);
 
 // linear_gemv.cu: the product with its epilogue for up to four tokens.  Against a stream of tensor-core tiles (us), one
-// token: 8192 to 4096 14.8, 15.9; 16384 to 4096 24.6, 26.1; 2048 to 2048 3.5, 6.4.  With more tokens the multiply-adds
-// take as long as large weights: T = 4, 2048 to 2048 4.5 against 6.4, but 8192 to 4096 21.0 against 15.9.
+// token: 8192 to 4096 14.5, 15.9; 16384 to 4096 24.5, 26.1; 2048 to 2048 3.4, 6.4.  With more tokens the multiply-adds
+// take as long as large weights: T = 4, 2048 to 2048 4.1 against 6.3, 2048 to 4096 7.3 against 7.8, but 4096 to 4096 12.0
+// against 10.3 and 8192 to 4096 20.0 against 15.9.
 inline bool gemv_tokens(const LinearShape& s) {
-  return s.T == 1 || (s.T <= 4 && (long long)s.n * s.k < 1LL << 23);
+  return s.T == 1 || (s.T <= 4 && (long long)s.n * s.k <= 1LL << 23);
 }
 cudaError_t launch_linear_gemv(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st);
 
