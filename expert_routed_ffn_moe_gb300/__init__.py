@@ -989,18 +989,28 @@ class Linear:
         px, pw = _checked(x, "x", (T, k), device, bf16), _checked(weight, "weight", (n, k), device, bf16)
         ppre, pdy = _checked(pre, "pre", (T, n), device, bf16), _checked(dy, "dy", (T, n), device)
         _checked(bias, "bias", (n,), device)
-
-        def output(t, name, like):
-            if t is False or like is None:
-                return None, None
-            if t is None:
-                t = torch.empty_like(like)
-                return t, t.data_ptr()
-            return t, _checked(t, name, like.shape, device, like.dtype)
-
-        dx, pdx = output(dx, "dx", x)
-        dweight, pdw = output(dweight, "dweight", weight)
-        dbias, pdb = output(dbias, "dbias", bias)
+        pdx = pdw = pdb = None
+        if dx is None:
+            dx = torch.empty_like(x)
+            pdx = dx.data_ptr()
+        elif dx is False:
+            dx = None
+        else:
+            pdx = _checked(dx, "dx", (T, k), device, bf16)
+        if dweight is None:
+            dweight = torch.empty_like(weight)
+            pdw = dweight.data_ptr()
+        elif dweight is False:
+            dweight = None
+        else:
+            pdw = _checked(dweight, "dweight", (n, k), device, bf16)
+        if bias is None or dbias is False:
+            dbias = None
+        elif dbias is None:
+            dbias = torch.empty_like(bias)
+            pdb = dbias.data_ptr()
+        else:
+            pdb = _checked(dbias, "dbias", (n,), device, bias.dtype)
         code = (_lib or lib()).moe_linear_backward(self.ctx, px, ppre, T, pw, pdy, _DTYPES[dy.dtype], pdx, pdw, pdb,
                                                    MOE_BF16 if bias is None else _DTYPES[bias.dtype],
                                                    _handle(None, device))

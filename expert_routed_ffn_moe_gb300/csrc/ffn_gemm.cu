@@ -1071,7 +1071,10 @@ cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* l
   const double weights = (double)((weight_tiles + e.pairs - 1) / e.pairs) * (all[1].blocks + each) + first;
   // (these estimates are good to about a tenth, and one launch has less to go wrong)
   const double dx_apart = split[0] == 1 ? 1e30 : 1.12 * (c[0] + kLaunchCost + weights);
-  const double apart = 1.12 * (c[0] + c[1] + c[2] + (all[2].tiles ? 2 : 1) * kLaunchCost);
+  // (two products that are not split gain nothing from a launch each: T = 2000, 2048 to 2048 31.8 us in one, 37.0 in two)
+  const double apart = all[2].tiles         ? 1.12 * (c[0] + c[1] + c[2] + 2 * kLaunchCost)
+                       : split[0] * split[1] > 1 ? 1.12 * (c[0] + c[1] + kLaunchCost)
+                                                 : 1e30;
   const bool one = together <= dx_apart && together <= apart, two = !one && dx_apart <= apart;
 
   GemmParams p{};
