@@ -159,10 +159,101 @@ cudaError_t by_act(const LinearGradArgs& a, cudaStream_t st) {
                                  : launch<DY, MOE_ACT_NONE>(a, st);
 }
 
+// ------------------------------------------------------------------ few tokens
+// For up to 16 tokens the same with the weight's gradient, dweight = dpre^T x, in one
+// pass: bound by writing it and, from some eight tokens on, by a multiply-add per token
+// and value on the CUDA cores.  A block has 64 rows of it and 256 columns, a warp 8 rows,
+// a lane 8 columns of each; dpre is made in shared memory, rounded to bf16 as the other
+// product reads it, each value twice, so that a multiply-add of two values finds its pair.
+// The blocks of the first columns leave dpre and dbias.  (Tiles of the tensor cores have
+// one k block each here and then an epilogue of ~2.4 us: few_grad_tokens() has the times.)
+constexpr int kFewRows = 64, kFewCols = 256;
+
+template <typename DY, int ACT>
+__global__ void __launch_bounds__(kThreads) linear_few_grad_kernel(LinearGradArgs a, const __nv_bfloat16* x,
+                                                                   __nv_bfloat16* dw, int k, int col_tiles) {
+  __shared__ __align__(16) float2 d[kFewTokens][kFewRows];  // (each value twice)
+  __shared__ float2 exact[kFewTokens][kFewRows / 2];        // before the rounding
+  __shared__ uint4 xs[kFewTokens][kFewCols / 8];
+  follow();
+  const int ct = blockIdx.x % col_tiles, n0 = blockIdx.x / col_tiles * kFewRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const __nv_bfloat16* pre = reinterpret_cast<const __nv_bfloat16*>(a.pre);
+  const int c = ct * kFewCols + lane * 8, row = n0 + warp * 8;
+#pragma unroll
+  for (int t = warp; t < kFewTokens; t += kThreads / 32)
+    if (t < a.T && c < k) xs[t][lane] = *reinterpret_cast<const uint4*>(x + (size_t)t * k + c);
+  for (int i = threadIdx.x; i < a.T * (kFewRows / 2); i += kThreads) {
+    const int t = i / (kFewRows / 2), j = i % (kFewRows / 2), n = n0 + 2 * j;
+    float2 v = both(0.f);
+    if (n < a.n) {
+      const size_t at = (size_t)t * a.n + n;
+      v = sizeof(DY) == 2 ? bf16_two(*reinterpret_cast<const uint32_t*>(static_cast<const DY*>(a.dy) + at))
+                          : *reinterpret_cast<const float2*>(static_cast<const DY*>(a.dy) + at);
+      if constexpr (ACT != MOE_ACT_NONE)
+        v = mul2(v, act_grad2<ACT>(bf16_two(*reinterpret_cast<const uint32_t*>(pre + at))));
+      if (ct == 0 && a.dpre) *reinterpret_cast<uint32_t*>(a.dpre + at) = pack_bf16x2(v.x, v.y);
+    }
+    exact[t][j] = v;
+    const float2 r = bf16_two(pack_bf16x2(v.x, v.y));
+    d[t][2 * j] = both(r.x);
+    d[t][2 * j + 1] = both(r.y);
+  }
+  __syncthreads();
+  if (ct == 0 && a.dbias && threadIdx.x < kFewRows && n0 + (int)threadIdx.x < a.n) {
+    float v = 0.f;  // in the tokens' order, as linear_grad_kernel
+    for (int t = 0; t < a.T; ++t) v += reinterpret_cast<const float*>(&exact[t][0])[threadIdx.x];
+    if (a.bias_dtype == MOE_BF16)
+      put(static_cast<__nv_bfloat16*>(a.dbias) + n0 + threadIdx.x, v);
+    else
+      put(static_cast<float*>(a.dbias) + n0 + threadIdx.x, v);
+  }
+  if (c >= k || row >= a.n) return;
+  float2 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = both(0.f);
+#pragma unroll 2
+  for (int t = 0; t < a.T; ++t) {
+    const uint4 w = xs[t][lane];
+    const float2 xf[4] = {bf16_two(w.x), bf16_two(w.y), bf16_two(w.z), bf16_two(w.w)};
+    const float4* dt = reinterpret_cast<const float4*>(&d[t][warp * 8]);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float4 q = dt[i / 2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[i][e] = fma2(make_float2(q.x, q.y), xf[e], acc[i][e]);
+        acc[i + 1][e] = fma2(make_float2(q.z, q.w), xf[e], acc[i + 1][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(dw + (size_t)(row + i) * k + c) =
+        make_uint4(pack_bf16x2(acc[i][0].x, acc[i][0].y), pack_bf16x2(acc[i][1].x, acc[i][1].y),
+                   pack_bf16x2(acc[i][2].x, acc[i][2].y), pack_bf16x2(acc[i][3].x, acc[i][3].y));
+}
+template <typename DY>
+cudaError_t few_by_act(const LinearGradArgs& a, const void* x, void* dw, int k, cudaStream_t st) {
+  const int col_tiles = (k + kFewCols - 1) / kFewCols, row_tiles = (a.n + kFewRows - 1) / kFewRows;
+  if ((long long)col_tiles * row_tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  const auto kernel = a.act == MOE_ACT_SILU   ? linear_few_grad_kernel<DY, MOE_ACT_SILU>
+                      : a.act == MOE_ACT_GELU ? linear_few_grad_kernel<DY, MOE_ACT_GELU>
+                                              : linear_few_grad_kernel<DY, MOE_ACT_NONE>;
+  return launch_after(kernel, col_tiles * row_tiles, dim3(kThreads), 0, st, a, static_cast<const __nv_bfloat16*>(x),
+                      static_cast<__nv_bfloat16*>(dw), k, col_tiles);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   return a.dy_dtype == MOE_BF16 ? by_act<__nv_bfloat16>(a, st) : by_act<float>(a, st);
+}
+
+cudaError_t launch_linear_few_grad(const LinearGradArgs& a, const void* x, void* dw, int k, cudaStream_t st) {
+  return a.dy_dtype == MOE_BF16 ? few_by_act<__nv_bfloat16>(a, x, dw, k, st) : few_by_act<float>(a, x, dw, k, st);
 }
 
 }  // namespace moe

@@ -257,20 +257,24 @@ int moe_linear_backward(moe_linear* ctx, const void* x, const void* pre, int T, 
   const LinearShape s{T, c.in_features, c.out_features, c.activation};
   const bool as_is = linear && dy_dtype == MOE_BF16;  // dpre is dy
   const uint16_t* dpre = as_is ? static_cast<const uint16_t*>(dy) : ctx->dpre;
-  const bool products = dx || dweight;
+  const bool products = dx || dweight, few = few_tokens(s), least = few_grad_tokens(s);
+  LinearGradArgs g{dy, static_cast<const uint16_t*>(pre), nullptr, dbias, T, c.out_features, dy_dtype, bias_dtype,
+                   c.activation};
   cudaError_t err = cudaSuccess;
-  if (dbias || (products && !as_is)) {
-    const LinearGradArgs g{dy, static_cast<const uint16_t*>(pre), products && !as_is ? ctx->dpre : nullptr, dbias, T,
-                           c.out_features, dy_dtype, bias_dtype, c.activation};
+  if (least && dweight) {
+    g.dpre = dx && !as_is ? ctx->dpre : nullptr;
+    err = launch_linear_few_grad(g, x, dweight, c.in_features, st);
+    ++ctx->launches;
+  } else if (dbias || (products && !as_is)) {
+    g.dpre = products && !as_is ? ctx->dpre : nullptr;
     err = launch_linear_grad(g, st);
     ++ctx->launches;
   }
-  const bool few = few_tokens(s);
   if (err == cudaSuccess && few && dx) {
     err = launch_linear_dx_stream(ctx->eng, s, dpre, weight, dx, st);
     ++ctx->launches;
   }
-  if (err == cudaSuccess && ((!few && dx) || dweight)) {
+  if (err == cudaSuccess && ((!few && dx) || (!least && dweight))) {
     int n = 0;
     err = launch_linear_grads(ctx->eng, s, dpre, x, weight, dx, dweight, &n, st);
     ctx->launches += n;

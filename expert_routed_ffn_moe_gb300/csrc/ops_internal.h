@@ -71,5 +71,12 @@ struct LinearGradArgs {
   int T, n, dy_dtype, bias_dtype, act;
 };
 cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st);
+// For up to kFewTokens tokens the same with dw [n, k] = dpre^T x.  A backward call with gelu, against dw as tensor-core
+// tiles (us): 4096 to 4096 T = 1 18, 23, T = 8 22, 25, but T = 12 26, 25; 2048 to 2048 T = 16 12, 15.
+constexpr int kFewTokens = 16;
+inline bool few_grad_tokens(const LinearShape& s) {
+  return s.T <= 8 || (s.T <= kFewTokens && (long long)s.n * s.k < 1LL << 23);
+}
+cudaError_t launch_linear_few_grad(const LinearGradArgs& a, const void* x, void* dw, int k, cudaStream_t st);
 
 }  // namespace moe
