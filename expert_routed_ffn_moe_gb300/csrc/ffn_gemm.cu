@@ -28,7 +28,8 @@
 // same 128 neurons, so the activation finishes in the accumulator's columns.
 //
 // A product with fewer tiles than pairs splits the reduction over 2 or 4 pairs
-// of one cluster (SPLIT).  Each pair ends with fp32 sums of the whole tile; the
+// of one cluster (SPLIT; `linear` also over 3: 16 tiles find 15 clusters of 4 pairs
+// on the device, T = 128, 4096 to 4096 17.5 us with 2, 16.0 with 3).  Each pair ends with fp32 sums of the whole tile; the
 // columns are divided among the pairs, every CTA sends its sums of the others'
 // columns to them through distributed shared memory (the ring's memory, free by
 // then), and each adds its columns' sums in the order of k and finishes them.
@@ -696,8 +697,18 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       }
     } else {
       // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
-      constexpr int W = kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
-      auto a0_of = [&](int owner) { return EPI == kEpiGateUp ? (owner * 2 + half) * W : (owner * 2 + half) * 2 * W; };
+      // (SPLIT == 3, linear only: the 16 chunks of 16 columns go two or three to each of the six.)
+      constexpr int W = SPLIT == 3 ? 24 : kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
+      static_assert(SPLIT != 3 || EPI == kEpiLinear, "columns of one range per warp");
+      auto chunk0 = [](int o) { return o * 16 / 6; };
+      auto width_of = [&](int owner) {  // columns of its share, both ranges
+        return SPLIT == 3 ? (chunk0(owner * 2 + half + 1) - chunk0(owner * 2 + half)) * 16 : 2 * W;
+      };
+      auto a0_of = [&](int owner) {
+        return SPLIT == 3           ? chunk0(owner * 2 + half) * 16
+               : EPI == kEpiGateUp ? (owner * 2 + half) * W
+                                   : (owner * 2 + half) * 2 * W;
+      };
       auto b0_of = [&](int owner) { return a0_of(owner) + (EPI == kEpiGateUp ? kBN / 2 : W); };
       const uint32_t src = tmem + lanes;
       uint8_t* send = base;                                         // [SPLIT - 1][warp] x kSendBytes
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       // Place of column c of row `lane`: 16-byte pieces of 4 columns, rows side by side.
       auto at = [&](uint8_t* buf, int c) { return reinterpret_cast<float4*>(buf + ((c >> 2) * 32 + lane) * 16); };
       bool ok = mbar_wait(&bar->tfull[0], 0, p.ctl) && !aborted(bar);
-      if (lane == 0) mbar_expect_tx(&bar->recv[ew], (SPLIT - 1) * kSendBytes);
+      if (lane == 0) mbar_expect_tx(&bar->recv[ew], (SPLIT - 1) * width_of(slot) * 128);
       __syncwarp();
       ok = all_of_256(ok);  // (all give up or none)
       if (ok) {
@@ -718,9 +729,9 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           const int owner = (slot + i) % SPLIT;
           uint8_t* out = send + ((i - 1) * kEpiWarps + ew) * kSendBytes;
 #pragma unroll 1
-          for (int c = 0; c < 2 * W; c += 16) {
+          for (int c = 0; c < width_of(owner); c += 16) {
             float v[16];
-            tmem_ld16_async(src + (c < W ? a0_of(owner) + c : b0_of(owner) + c - W), v);
+            tmem_ld16_async(src + (SPLIT == 3 || c < W ? a0_of(owner) + c : b0_of(owner) + c - W), v);
             tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < 16; q += 4) *at(out, c + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
@@ -733,7 +744,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             } else {
               const int by = slot < owner ? slot : slot - 1;  // this pair among the owner's senders
               const uint32_t to = (uint32_t)(2 * owner) + rank;
-              copy_to_cta(map_cta(recv + (by * kEpiWarps + ew) * kSendBytes, to), out, kSendBytes,
+              copy_to_cta(map_cta(recv + (by * kEpiWarps + ew) * kSendBytes, to), out, width_of(owner) * 128,
                           map_cta(&bar->recv[ew], to));
             }
           }
@@ -789,7 +800,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 2 * W; c += 16) {
+          for (int c = 0; c < width_of(slot); c += 16) {
             float v[16];
             uint4 in[kIn];
             load_pre(q, row, n * TN + a0 + c, in);
@@ -902,8 +913,8 @@ int split_of(const FfnEngine& e, const Product& q, double* cost) {
   constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
   int split = 1;
   *cost = 1e30;
-  for (int s = 1; s <= kMost && s <= q.blocks; s *= 2) {
-    const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : e.pairs4;  // clusters that run at a time
+  for (int s = 1; s <= kMost && s <= q.blocks; s += EPI == kEpiLinear || s == 1 ? 1 : 2) {
+    const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : s == 3 ? e.pairs3 : e.pairs4;  // clusters that run at a time
     if (fit < 1) break;
     const double rounds = (double)((q.tiles + fit - 1) / fit);
     const double c =
@@ -920,6 +931,8 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, cudaStream_t st) {
   const int split = split_of<EPI, MX>(e, p.q[0], &cost), tiles = p.q[0].tiles;
   if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? tiles : e.pairs, st);
   if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, tiles, st);
+  if constexpr (EPI == kEpiLinear)
+    if (split == 3) return launch<EPI, A_MN, B_MN, MX, 3>(p, tiles, st);
   if constexpr (!(MX && EPI == kEpiGateUp)) return launch<EPI, A_MN, B_MN, MX, 4>(p, tiles, st);
   return cudaErrorInvalidValue;
 }
@@ -941,6 +954,8 @@ template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t prepare_splits(FfnEngine* e) {
   cudaError_t err = prepare<EPI, A_MN, B_MN, MX, 1>(&e->pairs);
   if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 2>(&e->pairs2);
+  if constexpr (EPI == kEpiLinear)
+    if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 3>(&e->pairs3);
   if constexpr (!(MX && EPI == kEpiGateUp))
     if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 4>(&e->pairs4);
   return err;
@@ -962,7 +977,7 @@ __global__ void __launch_bounds__(256) shift_scales_kernel(const uint32_t* src, 
 }  // namespace
 
 cudaError_t prepare_ffn_gemm(FfnEngine* e) {
-  e->pairs = e->pairs2 = e->pairs4 = e->sms / 2;
+  e->pairs = e->pairs2 = e->pairs3 = e->pairs4 = e->sms / 2;
   cudaError_t err = prepare_splits<kEpiGateUp, false, false, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiStore, false, false, false>(e);
   if (err == cudaSuccess) err = prepare_splits<kEpiGrad, false, true, false>(e);

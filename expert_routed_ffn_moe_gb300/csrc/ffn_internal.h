@@ -272,7 +272,7 @@ inline bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr
 struct FfnEngine {
   EncodeTiledFn encode;
   int sms;
-  int pairs, pairs2, pairs4;  // clusters of 1, 2 and 4 CTA pairs that run at a time
+  int pairs, pairs2, pairs3, pairs4;  // clusters of 1 to 4 CTA pairs that run at a time
   DevCtl ctl;
 };
 
