@@ -1157,7 +1157,7 @@ cudaError_t launch_linear_grads(const FfnEngine& e, const LinearShape& s, const 
   if (!set_product<kEpiStore, false, true, false>(e, all[0], dpre, w, s.T, s.k, s.n, s.k, dx) ||
       !set_product<kEpiStore, true, true, false>(e, all[1], dpre, x, s.n, s.k, s.T, s.k, dw))
     return cudaErrorInvalidValue;
-  return launch_grads(e, all, few_tokens(s), launches, st);
+  return launch_grads(e, all, few_tokens(s, s.k), launches, st);
 }
 
 cudaError_t launch_linear_tiles(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st) {

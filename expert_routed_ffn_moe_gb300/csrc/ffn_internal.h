@@ -316,8 +316,11 @@ constexpr int kSkinnyTokens = 64;
 inline bool few_tokens(const FfnShape& s) {
   return s.T <= 32 || (s.T <= kSkinnyTokens && 3LL * s.d * s.I >= 1LL << 25);
 }
-inline bool few_tokens(const LinearShape& s) {
-  return s.T <= 32 || (s.T <= kSkinnyTokens && (long long)s.n * s.k >= 1LL << 24);
+// The product with its epilogue (outputs: n; of its dx: k): up to 64 tokens where the outputs are few tiles of 256, which the
+// pair kernel would split.  T = 33 and 64, as a stream against as tiles (us): 4096 to 4096: 13.7, 15.1 against 16.0, 16.0;
+// 2048 to 2048: 9.3, 10.7 against 10.2, 10.3; but 4096 to 16384: 33.1, 34.6 against 30.5, 30.6.
+inline bool few_tokens(const LinearShape& s, int outputs) {
+  return s.T <= 32 || (s.T <= kSkinnyTokens && outputs < 8192);
 }
 cudaError_t prepare_ffn_skinny();
 cudaError_t launch_skinny_forward(const FfnEngine& e, const FfnShape& s, bool mx, const FfnForwardArgs& a,

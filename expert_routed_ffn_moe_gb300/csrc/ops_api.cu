@@ -231,8 +231,8 @@ int moe_linear_forward(moe_linear* ctx, const void* x, int T, const void* weight
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ++ctx->launches;
   return cuda_code(gemv_tokens(s) ? launch_linear_gemv(ctx->eng, s, a, st)
-                   : few_tokens(s) ? launch_linear_stream(ctx->eng, s, a, st)
-                                   : launch_linear_tiles(ctx->eng, s, a, st));
+                   : few_tokens(s, s.n) ? launch_linear_stream(ctx->eng, s, a, st)
+                                        : launch_linear_tiles(ctx->eng, s, a, st));
 }
 
 int moe_linear_backward(moe_linear* ctx, const void* x, const void* pre, int T, const void* weight, const void* dy,
@@ -257,7 +257,7 @@ int moe_linear_backward(moe_linear* ctx, const void* x, const void* pre, int T, 
   const LinearShape s{T, c.in_features, c.out_features, c.activation};
   const bool as_is = linear && dy_dtype == MOE_BF16;  // dpre is dy
   const uint16_t* dpre = as_is ? static_cast<const uint16_t*>(dy) : ctx->dpre;
-  const bool products = dx || dweight, few = few_tokens(s), least = few_grad_tokens(s);
+  const bool products = dx || dweight, few = few_tokens(s, s.k), least = few_grad_tokens(s);
   LinearGradArgs g{dy, static_cast<const uint16_t*>(pre), nullptr, dbias, T, c.out_features, dy_dtype, bias_dtype,
                    c.activation};
   cudaError_t err = cudaSuccess;

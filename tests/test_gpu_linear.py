@@ -18,7 +18,7 @@ def operands(g, T, k, n, bias=BF, res=None):
 
 # few tokens as a weight stream; one tile and split ones; several tiles per pair of CTAs; no multiple of a tile
 SIZES = [(1, 8, 8), (1, 2048, 4096), (1, 8200, 1000), (2, 64, 136), (3, 520, 2400), (4, 4096, 3000), (4, 16, 17000), (5, 264, 1000), (8, 4096, 4096), (12, 2048, 4104), (13, 1024, 776), (16, 256, 1000), (17, 72, 128), (31, 1000, 264), (33, 512, 64),
-         (48, 4096, 4096), (64, 4104, 4096), (65, 256, 512), (128, 4096, 4096), (200, 1024, 768), (200, 1000, 5000), (300, 136, 2744), (777, 1000, 2744),
+         (48, 4096, 4096), (64, 4104, 4096), (40, 128, 8200), (50, 8200, 136), (65, 256, 512), (128, 4096, 4096), (200, 1024, 768), (200, 1000, 5000), (300, 136, 2744), (777, 1000, 2744),
          (1025, 264, 8), (2500, 512, 4352)]
 
 
