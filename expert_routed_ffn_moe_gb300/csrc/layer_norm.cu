@@ -253,6 +253,7 @@ struct Odd {
         static const int resident = resident_blocks(kernel, kBlock, smem) / 8 * 8;  // (see Windows)
         if (grid > resident) grid = resident;
       }
+      if (!steps_of_eight(a.T, grid * kRows)) return cudaErrorInvalidValue;
       return launch_after(kernel, grid, dim3(kBlock), smem, st, a);
     }
   };

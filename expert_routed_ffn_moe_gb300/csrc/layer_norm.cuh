@@ -118,6 +118,9 @@ MOE_DEV F8 param_of(const Windows<R, ODD>& win, const void* p, int dtype, int o,
   return f;
 }
 
+// Whether rows that are not aligned may be walked over in steps of `stride`: see Windows.
+inline bool steps_of_eight(int T, int stride) { return stride >= T || stride % 8 == 0; }
+
 // Sums of two values over a warp, each in every lane: the halves of the warp add
 // up one value each after the first exchange.
 MOE_DEV void warp_sum2(float& a, float& b) {

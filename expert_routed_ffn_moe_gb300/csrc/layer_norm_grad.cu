@@ -190,7 +190,14 @@ __global__ void __launch_bounds__(ln_block(R), R <= 512 ? 512 / ln_block(R) : 1)
       const int head = ODD ? (int)((long long)(blockIdx.x * kRows + r) * a.d & 7) : 0;
       v += sums[r * 32 * R + half * 16 * R + c + head];
     }
-    to[k] = v;
+    if (gridDim.x > 1) {
+      to[k] = v;
+    } else if (void* out = half ? a.db : a.dw) {  // the only block's sums: no second kernel
+      if (a.w_dtype == MOE_BF16)
+        put(static_cast<__nv_bfloat16*>(out) + c, v);
+      else
+        put(static_cast<float*>(out) + c, v);
+    }
   }
 }
 
@@ -243,8 +250,9 @@ struct Backward {
         static const int resident = min(resident_blocks(kernel, kBlock, smem), kLayerNormPartials) / 8 * 8;
         if (grid > resident) grid = resident;
       }
+      if (ODD && !steps_of_eight(a.T, grid * kRows)) return cudaErrorInvalidValue;
       const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), smem, st, a);
-      if (e != cudaSuccess || (!a.dw && !a.db)) return e;
+      if (e != cudaSuccess || (!a.dw && !a.db) || grid == 1) return e;
       return launch_after(layer_norm_grad_sum_kernel, (2 * a.d + 31) / 32, dim3(32, 32), 0, st, (const float*)a.partial,
                           grid, a.d, a.dw, a.db, a.w_dtype);
     }

@@ -20,7 +20,7 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------ sort
-// One cluster of up to 8 CTAs of 32 warps.  A warp owns a contiguous range of the
+// One cluster of up to 16 CTAs of 32 warps.  A warp owns a contiguous range of the
 // picks.  It counts its picks per expert, the counts become start positions by a
 // prefix over the warps, the CTAs (distributed shared memory) and the experts, and a
 // second walk over the picks hands them out in order: of 32 picks those of the same
@@ -29,7 +29,7 @@ namespace {
 //
 // Bound by its chain of steps: a launch, a read of idx, two walks, and the exchange
 // between the CTAs.
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 8;
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCluster = 16;
 constexpr int kSortAhead = 4;  // loads of 32 picks in flight per warp
 
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(SortArgs a) {
@@ -491,13 +491,45 @@ struct CombineGrad {
 
 }  // namespace
 
+// Prepares the sort on the current device: the most CTAs of a cluster there, 16 (more than every device promises a cluster)
+// or 8.  0 on an error.
+static int prepare_sort() {
+  constexpr size_t most = (size_t)(kSortWarps + 2) * kMaxSortExperts * 4;  // (parts: 1024 sums at most)
+  if (cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
+    return 0;
+  if (cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return 8;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(kSortCluster);
+  c.blockDim = dim3(kSortThreads);
+  c.dynamicSmemBytes = most;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kSortCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, sort_tokens_kernel, &c) != cudaSuccess) cudaGetLastError();
+  return n > 0 ? kSortCluster : 8;
+}
+
 cudaError_t launch_sort_tokens(const SortArgs& a, cudaStream_t st) {
-  const size_t most = (size_t)(kSortWarps + 1 + 1) * kMaxSortExperts * 4;  // (parts: 1024 sums at most)
-  const size_t smem = (size_t)(kSortWarps + 1) * a.E * 4 + 1024 * 4;
-  const cudaError_t err = allow(sort_tokens_kernel, smem, most);
+  static std::atomic<int> prepared[64];  // by device: prepare_sort()'s answer, 0 before
+  int dev = 0;
+  const cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  int most_ranks = dev < 64 ? prepared[dev].load(std::memory_order_acquire) : 0;
+  if (!most_ranks) {
+    most_ranks = prepare_sort();
+    if (!most_ranks) return cudaGetLastError();
+    if (dev < 64) prepared[dev].store(most_ranks, std::memory_order_release);
+  }
+  const size_t smem = (size_t)(kSortWarps + 1) * a.E * 4 + 1024 * 4;
   int ranks = 1;
-  while (ranks < kSortCluster && ranks * 2 * kSortThreads <= a.picks) ranks *= 2;
+  while (ranks < most_ranks && ranks * 2 * kSortThreads <= a.picks) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kSortThreads);
