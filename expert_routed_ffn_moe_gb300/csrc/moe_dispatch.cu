@@ -212,12 +212,12 @@ MOE_DEV int slot_of(const RowsArgs& a, int t, int j) {
   return s < 0 || s >= a.n_rows ? -1 : s;
 }
 
-template <typename XT, typename RT, int VEC>
+template <int VEC>
 constexpr int kDispatchPieces = VEC == 8 ? 2 : VEC == 2 ? 4 : 8;
 
 template <typename XT, typename RT, int VEC>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(RowsArgs a) {
-  constexpr int P = kDispatchPieces<XT, RT, VEC>, kCols = slice_columns(VEC, P);
+  constexpr int P = kDispatchPieces<VEC>, kCols = slice_columns(VEC, P);
   follow();
   const int lane = threadIdx.x & 31;
   const int slices = (a.d + kCols - 1) / kCols;
@@ -333,11 +333,11 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(RowsArgs a) {
 
 // A token belongs to W warps of a block, which take its slices in turn; their parts
 // of dw meet in shared memory, in order.  K picks at a time.
-template <typename YT, typename RT, int VEC, int K>
+template <int VEC, int K>
 constexpr int kGradPieces = (VEC == 8 ? 1 : VEC == 2 ? 2 : 4) * (K == 2 ? VEC == 8 ? 4 : 2 : 1);
 template <typename YT, typename RT, int VEC, int W, int K>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(RowsArgs a) {
-  constexpr int P = kGradPieces<YT, RT, VEC, K>, kTokens = kRowThreads / 32 / W, kPicks = K;
+  constexpr int P = kGradPieces<VEC, K>, kTokens = kRowThreads / 32 / W, kPicks = K;
   constexpr int kStep = 32 * VEC * P;  // columns of a warp at a time
   __shared__ float part[kTokens][W][kPicks];
   follow();
@@ -448,7 +448,7 @@ cudaError_t pick(const RowsArgs& a, int first, int second, cudaStream_t st) {
 template <typename XT, typename RT, int VEC>
 struct Dispatch {
   static cudaError_t run(const RowsArgs& a, cudaStream_t st) {
-    const int grid = blocks_of(a, slice_columns(VEC, kDispatchPieces<XT, RT, VEC>));
+    const int grid = blocks_of(a, slice_columns(VEC, kDispatchPieces<VEC>));
     return launch_after(dispatch_kernel<XT, RT, VEC>, grid, dim3(kRowThreads), 0, st, a);
   }
 };
@@ -482,7 +482,7 @@ struct CombineGrad {
     // 8.4, 7.3, 8.1 us with 1, 2, 4, 8; T = 2000 23.2, 25.0, 26.7, 29.9).  Others move smaller pieces, which several warps
     // side by side do better at any T (T = 4000, d = 2501: 115, 107, 117, 90; d = 2502: 85, 73, 67, 72), as far as each has
     // two rounds of them.
-    const int rounds = a.d / (2 * 32 * VEC * kGradPieces<YT, RT, VEC, K>);
+    const int rounds = a.d / (2 * 32 * VEC * kGradPieces<VEC, K>);
     const int most = VEC == 8 ? 16 * 152 / a.T : rounds < 1 ? 1 : VEC == 1 ? rounds : rounds < 4 ? rounds : 4;
     return most >= 8 ? launch<8, K>(a, st) : most >= 4 ? launch<4, K>(a, st) : most >= 2 ? launch<2, K>(a, st) : launch<1, K>(a, st);
   }
