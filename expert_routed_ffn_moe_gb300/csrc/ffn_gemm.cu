@@ -58,7 +58,7 @@
 // its scales' copies and the sight of both have to come in time for 512 cycles of
 // MMAs (TMEM has room for four blocks' scales).  Few tiles: the ~1 us that each
 // of a launch's start, first loads, epilogue and end take.
-#include "ffn_internal.h"
+#include "rows_common.cuh"
 
 namespace moe {
 namespace {
@@ -69,10 +69,8 @@ constexpr int kRowBytes = 128;              // a k block: 64 bf16 or 128 e4m3 va
 constexpr int kBK = 64;                     // k block of bf16
 constexpr int kOpBytes = 128 * kRowBytes;   // one operand's half tile: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;   // per CTA
-constexpr int kEpiWarps = 8;
-constexpr int kBWarp = 2 + kEpiWarps;       // producers: A on warp 0, B on this, mx8's scales on the next
-constexpr int roles_of(bool mx) { return mx ? 3 : 2; }  // A, B; mx8: and the scales
-constexpr int threads_of(bool mx) { return (kBWarp + roles_of(mx) - 1) * 32; }
+constexpr int kEpiWarps = 8;                // epilogue warps; twice as many where results are staged, see there
+constexpr int roles_of(bool mx) { return mx ? 3 : 2; }  // producers: A on warp 0, B on the first after the epilogue's, mx8's scales
 constexpr int kScaleBytes = 3 * 512;        // mx8 scales of a k block: A's 128 rows, B's 2 x 128
 constexpr int kScaleSets = 4;               // mx8: k blocks whose scales TMEM holds, 12 columns each
 constexpr int kSharedCols = 12 * kScaleSets;  // mx8: accumulator columns that both tiles use
@@ -130,8 +128,17 @@ struct __align__(8) Bars {
   uint32_t any_abort;     // some CTA of the cluster has given up
 };
 
-constexpr size_t smem_of(bool mx) { return 1024 + (size_t)kStages * stage_bytes(mx) + sizeof(Bars); }
-static_assert(smem_of(true) <= 227 * 1024, "shared memory of one CTA");
+// Results that go to memory by way of shared memory: an epilogue warp's place there has its 32 rows of 128 bytes.
+constexpr int kPlaceBytes = 32 * 128;
+constexpr bool staged(int epi, bool mx, int split) { return epi == kEpiLinear && !mx && split == 1; }
+constexpr int stages_of(int epi, bool mx, int split) { return staged(epi, mx, split) ? kStages - 1 : kStages; }
+constexpr int epi_warps(int epi, bool mx, int split) { return staged(epi, mx, split) ? 2 * kEpiWarps : kEpiWarps; }
+constexpr int threads_of(int epi, bool mx, int split) { return (2 + epi_warps(epi, mx, split) + roles_of(mx) - 1) * 32; }
+constexpr size_t smem_of(int epi, bool mx, int split) {
+  return 1024 + (size_t)stages_of(epi, mx, split) * stage_bytes(mx) + (staged(epi, mx, split) ? 2 * kEpiWarps * kPlaceBytes : 0) + sizeof(Bars);
+}
+static_assert(smem_of(kEpiGateUp, true, 1) <= 227 * 1024 && smem_of(kEpiLinear, false, 1) <= 227 * 1024,
+              "shared memory of one CTA");
 
 MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -149,6 +156,7 @@ MOE_DEV void store32(void* to, const uint32_t(&w)[8]) {  // 32-byte aligned
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
+MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 MOE_DEV void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -268,16 +276,18 @@ MOE_DEV bool tile_of(const GemmParams& p, int pair, int pairs, int j, Tile& t) {
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT, bool MULTI>
-__global__ void __launch_bounds__(threads_of(MX), 1)
+__global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
     ffn_gemm_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int S = kStages;
+  constexpr int S = stages_of(EPI, MX, SPLIT);
   constexpr uint32_t kTx = stage_bytes(MX);        // bytes per CTA and k block
   static_assert(!MX || (!A_MN && !B_MN && EPI != kEpiGrad), "mx8: forward products only");
   constexpr int TN = EPI == kEpiGateUp ? kBN / 2 : kBN;  // result columns per tile
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* scales = base + S * kStageBytes;
-  Bars* bar = reinterpret_cast<Bars*>(scales + (MX ? S * kScaleBytes : 0));
+  uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (the compiler still sees shared memory in it)
+  uint8_t* scales = base + S * kStageBytes;  // mx8; else, where results are staged, the places
+  constexpr bool kStaged = staged(EPI, MX, SPLIT);
+  constexpr int E = epi_warps(EPI, MX, SPLIT), kBWarp = 2 + E;
+  Bars* bar = reinterpret_cast<Bars*>(scales + (MX ? S * kScaleBytes : kStaged ? E * kPlaceBytes : 0));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;  // rank in the pair, its first CTA
@@ -293,7 +303,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->tfull[i], 1);
-      mbar_init(&bar->tempty[i], 2 * kEpiWarps);
+      mbar_init(&bar->tempty[i], 2 * E);
     }
     mbar_init(&bar->mma_done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bar->free[i], 1);
@@ -492,20 +502,21 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         if (col + 8 < q.N) *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     };
+    // 16 columns from column col on as 2 or 4 x 16 bytes, 8 columns at a time.
+    auto load16 = [&](const Product& q, const void* from, bool wide, size_t at, int col, bool ok, uint4* to) {
+      const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + at * (wide ? 4 : 2));
+      const int n = wide ? 4 : 2;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) to[c] = ok && col + c * 16 / n < q.N ? v[c] : make_uint4(0, 0, 0, 0);
+    };
     // What 16 columns of a row need besides their sums, asked for ahead of them.  grad: pre's values; linear: the
     // residual (first four) and the bias, as they lie in memory.
     constexpr int kIn = EPI == kEpiLinear ? 8 : 4;
     auto load_pre = [&](const Product& q, int row, int col, uint4(&in)[kIn]) {
       if constexpr (EPI == kEpiLinear) {
-        auto load = [&](const void* from, bool wide, size_t at, bool ok, uint4* to) {  // 2 or 4 x 16 bytes, 8 columns at a time
-          const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + at * (wide ? 4 : 2));
-          const int n = wide ? 4 : 2;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < n) to[c] = ok && col + c * 16 / n < q.N ? v[c] : make_uint4(0, 0, 0, 0);
-        };
-        if (p.res) load(p.res, p.y32, (size_t)row * q.N + col, row < q.M, in);
-        if (p.bias) load(p.bias, !p.bias_bf16, col, true, in + 4);
+        if (p.res) load16(q, p.res, p.y32, (size_t)row * q.N + col, col, row < q.M, in);
+        if (p.bias) load16(q, p.bias, !p.bias_bf16, col, col, true, in + 4);
       }
       if (EPI != kEpiGrad) return;
       const uint16_t* gp = p.pre + (size_t)row * 2 * q.N + col;
@@ -516,27 +527,34 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         in[2 + c] = ok ? *reinterpret_cast<const uint4*>(gp + q.N + c * 8) : make_uint4(0, 0, 0, 0);
       }
     };
+    auto activate = [&](float(&v)[16]) {  // linear
+      with_act_or_none(p.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float2 a = act_value2<decltype(act)::value>(make_float2(v[e], v[e + 1]));
+          v[e] = a.x, v[e + 1] = a.y;
+        }
+      });
+    };
+    // Values of 16 columns, as they lie in memory, added to v.
+    auto add = [&](float(&v)[16], const uint4* from, bool wide) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(from);
+      if (wide) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] += e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+      }
+    };
     // One row's results: 16 columns of a product or of dh, or gate and up values of 16 neurons
     // (grad: pre's 16 gate and up values of the row in `in`)
     auto finish = [&](const Product& q, int row, int col, float(&v)[16], const float(&u)[16], const uint4(&in)[kIn]) {
       if constexpr (EPI == kEpiLinear) {
-        auto add = [&](const uint4* from, bool wide) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(from);
-          if (wide) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-          }
-        };
-        if (p.bias) add(in + 4, !p.bias_bf16);
+        if (p.bias) add(v, in + 4, !p.bias_bf16);
         if (p.pre_out) store16(q, p.pre_out, q.N, row, col, v);
-        with_act_or_none(p.act, [&](auto act) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = act_value<decltype(act)::value>(v[e]);
-        });
-        if (p.res) add(in, p.y32);
+        activate(v);
+        if (p.res) add(v, in, p.y32);
         if (!p.y32) {
           store16(q, q.y, q.N, row, col, v);
         } else if (row < q.M) {
@@ -608,7 +626,145 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
       p.hs[mx_scale_word(row, col / 128, mx_tile_cols(q.N)) + col / 32 % 4] = (uint8_t)byte;
     };
 
-    if constexpr (SPLIT == 1) {
+    auto release = [&](int acc) {  // an accumulator (mx8: the shared columns) is read
+      tc_fence_before();
+      __syncwarp();
+      // relaxed: only the TMEM reads above come before it, which have completed (a release would first wait for the
+      // rows stored so far, ~1 us)
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         map_cta(&bar->tempty[MX ? 0 : acc], lead))
+                     : "memory");
+    };
+    if constexpr (kStaged) {
+      // The sums of 32 columns at a time change hands through the warp's place in shared memory, so that a thread, which
+      // reads a row of them, finishes 8 neighbouring columns (the same in every row) of every eighth row: bias, residual and
+      // results then move 64 or 128 bytes of a row at a time, and a column's bias is read once.  (In the place the 16-byte
+      // pieces of a row are swapped by the row: neither side finds a bank twice.)  What the next columns need is asked for
+      // ahead of them, and the next tile's residual brought to L2.
+      const Product& q = p.q[0];
+      const int M = q.M, N = q.N;
+      const bool f32 = p.y32, bias_bf16 = p.bias_bf16;
+      const uint8_t *res_in = static_cast<const uint8_t*>(p.res), *bias_in = static_cast<const uint8_t*>(p.bias);
+      uint8_t* const y = reinterpret_cast<uint8_t*>(q.y);
+      uint16_t* const pre_out = p.pre_out;
+      const int size = f32 ? 4 : 2;
+      float4* const place = reinterpret_cast<float4*>(scales + ew * kPlaceBytes);
+      const int to = lane * 8 + (lane & 7);              // piece e of row `lane` at to ^ e
+      const int r0 = lane >> 2, piece = (lane & 3) * 2;  // a thread's rows are r0 + 8 i: from + 64 i
+      const int from = r0 * 8 + (piece ^ r0);            // the second piece at from ^ 1
+      struct Group {  // a thread's part of 32 columns of a tile
+        int rows;     // of its four rows how many there are (its 8 columns are there or not)
+        size_t at;    // the first of its values in the matrix
+      };
+      auto row_of = [&](const Tile& t) { return (2 * t.m + (int)rank) * kBM + part * 32; };
+      auto col_of = [&](const Tile& t) { return t.n * TN + half * 64; };
+      auto group_of = [&](const Tile& t, int g) {
+        const int row = row_of(t) + r0, col = col_of(t) + g * 32 + (lane & 3) * 8;
+        return Group{col < N && row < M ? min((M - row + 7) >> 3, 4) : 0, (size_t)row * N + col};
+      };
+      uint4 res[8], bias[2];
+      auto fetch_bias = [&](const Tile& t, int g) {
+        const int col = col_of(t) + g * 32 + (lane & 3) * 8;
+        if (!bias_in || col >= N) return;
+        const uint4* b = reinterpret_cast<const uint4*>(bias_in + (size_t)col * (bias_bf16 ? 2 : 4));
+        bias[0] = b[0];
+        if (!bias_bf16) bias[1] = b[1];
+      };
+      auto fetch_row = [&](const Group& gr, int i, uint4* to) {
+        if (!res_in || i >= gr.rows) return;
+        const uint4* r = reinterpret_cast<const uint4*>(res_in + (gr.at + (size_t)(i * 8) * N) * size);
+        to[0] = r[0];
+        if (f32) to[1] = r[1];
+      };
+      auto prefetch = [&](const Tile& t) {  // the residual's 64 columns of row `lane`, by their first and last line
+        const int row = row_of(t) + lane, col = col_of(t);
+        if (!res_in || row >= M || col >= N) return;
+        const uint8_t* r = res_in + ((size_t)row * N + col) * size;
+        prefetch_l2(r);
+        prefetch_l2(r + min(64, N - col) * size - 1);
+      };
+      Tile next;
+      bool more = tile_of<MULTI>(p, pair, pairs, 0, next);
+      Group ahead{};
+      if (more) {
+        ahead = group_of(next, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch_row(ahead, i, res + 2 * i);
+        prefetch(next);
+      }
+      for (int lt = 0; more; ++lt) {
+        const int acc = lt & 1;
+        t = next;
+        more = tile_of<MULTI>(p, pair, pairs, lt + 1, next);
+        if (more) prefetch(next);
+        if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
+          set_abort(bar);
+          break;
+        }
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t src = tmem + lanes + acc * kBN + half * 64;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const Group here = ahead;
+          float v[32];
+          tmem_ld16_async(src + g * 32, v);
+          tmem_ld16_async(src + g * 32 + 16, v + 16);
+          fetch_bias(t, g);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            place[to ^ e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          if (g == 1) release(acc);
+          __syncwarp();
+          ahead = g == 0 ? group_of(t, 1) : more ? group_of(next, 0) : Group{};
+          const uint32_t bw[8] = {bias[0].x, bias[0].y, bias[0].z, bias[0].w, bias[1].x, bias[1].y, bias[1].z, bias[1].w};
+          float2 b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            b[e] = !bias_in    ? both(0.f)
+                   : bias_bf16 ? bf16_two(bw[e])
+                               : make_float2(__uint_as_float(bw[2 * e]), __uint_as_float(bw[2 * e + 1]));
+          with_act_or_none(p.act, [&](auto a) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 lo = place[from + i * 64], hi = place[(from ^ 1) + i * 64];
+              float2 x[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
+              const size_t at = here.at + (size_t)(i * 8) * N;
+              auto packed = [&]() {
+                return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                                  pack_bf16x2(x[3].x, x[3].y));
+              };
+              const bool live = i < here.rows;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = add2(x[e], b[e]);
+              if (pre_out && live) *reinterpret_cast<uint4*>(pre_out + at) = packed();
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = act_value2<decltype(a)::value>(x[e]);
+              if (res_in) {
+                const uint4 l = res[2 * i], h = res[2 * i + 1];
+                const uint32_t w[8] = {l.x, l.y, l.z, l.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  x[e] = add2(x[e], f32 ? make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]))
+                                        : bf16_two(w[e]));
+                fetch_row(ahead, i, res + 2 * i);
+              }
+              if (!live) continue;
+              if (!f32) {
+                *reinterpret_cast<uint4*>(y + at * 2) = packed();
+              } else {
+                float4* out = reinterpret_cast<float4*>(y + at * 4);
+                out[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                out[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+              }
+            }
+          });
+          __syncwarp();
+        }
+      }
+    } else if constexpr (SPLIT == 1) {
       int lt = 0;
       for (; tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
         const Product& q = p.q[MULTI ? t.q : 0];
@@ -626,18 +782,8 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
         const uint32_t src = tmem + lanes + acc * (MX ? kBN - kSharedCols : kBN);
         // mx8: the part with the shared columns first (the last columns of accumulator 0, the first of 1)
         const bool back = MX && acc == 0;
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          // relaxed: only the TMEM reads above come before it, which have completed (a release would first wait for the
-          // rows stored so far, ~1 us)
-          if (lane == 0)
-            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                             map_cta(&bar->tempty[MX ? 0 : acc], lead))
-                         : "memory");
-        };
         const bool holds = !MX || half == (back ? 1 : 0);  // mx8: this warp reads shared columns
-        if (!holds) release();
+        if (!holds) release(acc);
         if (EPI == kEpiGateUp && MX) {
           // Two groups of 32 neurons.  The shared columns are up values (back) or gate values of both groups, so the
           // second group's are read with the first.
@@ -651,7 +797,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
           load(u, 128 + column(0));
           load(next, (back ? 128 : 0) + column(1));
           tmem_ld_wait();
-          if (holds) release();
+          if (holds) release(acc);
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
             finish_mx(q, row, n * TN + column(i), g, u);
@@ -686,7 +832,7 @@ __global__ void __launch_bounds__(threads_of(MX), 1)
             uint4 now[kIn];
 #pragma unroll
             for (int e = 0; e < kIn; ++e) now[e] = in[e];
-            if (holds && i == kShared - 1) release();
+            if (holds && i == kShared - 1) release(acc);
             if (i + 1 < kChunks) {
               load(i + 1);
               load_pre(q, row, n * TN + (half * kChunks + i + 1) * 16, in);
@@ -855,8 +1001,8 @@ template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT>
 cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * SPLIT * clusters);
-  cfg.blockDim = dim3(threads_of(MX));
-  cfg.dynamicSmemBytes = smem_of(MX);
+  cfg.blockDim = dim3(threads_of(EPI, MX, SPLIT));
+  cfg.dynamicSmemBytes = smem_of(EPI, MX, SPLIT);
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2 * SPLIT;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -940,7 +1086,8 @@ cudaError_t run(const FfnEngine& e, GemmParams& p, cudaStream_t st) {
 template <int EPI, bool A_MN, bool B_MN, bool MX, int SPLIT, bool MULTI = false>
 cudaError_t prepare(int* clusters) {
   auto k = ffn_gemm_kernel<EPI, A_MN, B_MN, MX, SPLIT, MULTI>;
-  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(MX));
+  cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem_of(EPI, MX, SPLIT));
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = config<EPI, A_MN, B_MN, MX, SPLIT>(1, at);

@@ -18,30 +18,12 @@ namespace {
 constexpr int kCols = 64, kThreads = 256, kLanes = kThreads / (kCols / 8);  // 32 rows at a time
 constexpr int kMaxRanks = 8;
 
-MOE_DEV float exp2_fast(float v) {  // 2^v
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-MOE_DEV float reciprocal_fast(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 // act'(g) of two values, as act_and_grad(): with p = logistic(z), z = g or the argument of gelu's tanh form doubled,
 //   act' = p + g p (1 - p) z'(g).
 template <int ACT>
 MOE_DEV float2 act_grad2(float2 g) {
-  constexpr float kLog2e = 1.4426950408889634f, kGelu = 1.5957691216057308f, kFar = 80.f * kLog2e;
-  const float2 g2 = mul2(g, g);
-  // e = -z log2(e)
-  const float2 e = ACT == MOE_ACT_SILU
-                       ? mul2(g, both(-kLog2e))
-                       : mul2(g, fma2(g2, both(-kLog2e * kGelu * 0.044715f), both(-kLog2e * kGelu)));
-  const float2 d = add2(make_float2(exp2_fast(fminf(e.x, kFar)), exp2_fast(fminf(e.y, kFar))), both(1.f));
-  float2 p = make_float2(reciprocal_fast(d.x), reciprocal_fast(d.y));
-  p.x = e.x > kFar ? 0.f : p.x;  // (a huge negative g gives 0 and not g e^-80)
-  p.y = e.y > kFar ? 0.f : p.y;
+  constexpr float kGelu = 1.5957691216057308f;
+  const float2 g2 = mul2(g, g), p = logistic2(act_exponent2<ACT>(g, g2));
   const float2 a = mul2(g, p), q = fma2(p, both(-1.f), both(1.f));
   if (ACT == MOE_ACT_SILU) return fma2(a, q, p);
   // (beyond |g| = 10 the second term vanishes; the bound keeps an overflowing g^2 out)

@@ -97,6 +97,41 @@ MOE_DEV float2 add2(float2 a, float2 b) {
 MOE_DEV float2 both(float v) { return make_float2(v, v); }
 MOE_DEV float2 bf16_two(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
 
+MOE_DEV float exp2_fast(float v) {  // 2^v
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+MOE_DEV float reciprocal_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// The activations' common part for two values: e = -z log2(e), where logistic(z) = 1 / (1 + 2^e) is what act(g) multiplies
+// g by, z = g or the argument of gelu's tanh form doubled.  g2 = g^2.
+template <int ACT>
+MOE_DEV float2 act_exponent2(float2 g, float2 g2) {
+  constexpr float kLog2e = 1.4426950408889634f, kGelu = 1.5957691216057308f;
+  if (ACT == MOE_ACT_SILU) return mul2(g, both(-kLog2e));
+  return mul2(g, fma2(g2, both(-kLog2e * kGelu * 0.044715f), both(-kLog2e * kGelu)));
+}
+// 1 / (1 + 2^e), 0 from 2^-60 down (a huge negative g then gives 0; NaN stays NaN through the product with g): one
+// reciprocal for both values, 1 / (a b) times b and a, as the special functions are what a tile's epilogue takes longest for.
+MOE_DEV float2 logistic2(float2 e) {
+  constexpr float kFar = 60.f;
+  const float2 d = add2(make_float2(exp2_fast(fminf(e.x, kFar)), exp2_fast(fminf(e.y, kFar))), both(1.f));
+  const float r = reciprocal_fast(d.x * d.y);
+  float2 p = mul2(make_float2(d.y, d.x), both(r));
+  p.x = e.x > kFar ? 0.f : p.x;
+  p.y = e.y > kFar ? 0.f : p.y;
+  return p;
+}
+template <int ACT>
+MOE_DEV float2 act_value2(float2 g) {
+  if (ACT == MOE_ACT_NONE) return g;
+  return mul2(g, logistic2(act_exponent2<ACT>(g, mul2(g, g))));
+}
+
 // The sums over the R threads of a row, in every one of them.  `red` is another
 // half of its memory from one row to the next, so one barrier per row suffices.
 template <int R, int N>
