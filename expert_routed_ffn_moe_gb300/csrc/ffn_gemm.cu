@@ -130,14 +130,14 @@ struct __align__(8) Bars {
 
 // Results that go to memory by way of shared memory: an epilogue warp's place there has its 32 rows of 128 bytes.
 constexpr int kPlaceBytes = 32 * 128;
-constexpr bool staged(int epi, bool mx, int split) { return epi == kEpiLinear && !mx && split == 1; }
-constexpr int stages_of(int epi, bool mx, int split) { return staged(epi, mx, split) ? kStages - 1 : kStages; }
-constexpr int epi_warps(int epi, bool mx, int split) { return staged(epi, mx, split) ? 2 * kEpiWarps : kEpiWarps; }
+constexpr bool staged(int epi, bool mx, int split) { return (epi == kEpiStore || epi == kEpiLinear) && !mx && split == 1; }
+constexpr int stages_of(int epi, bool mx, int split) { return staged(epi, mx, split) && epi == kEpiLinear ? kStages - 1 : kStages; }
+constexpr int epi_warps(int epi, bool mx, int split) { return staged(epi, mx, split) && epi == kEpiLinear ? 2 * kEpiWarps : kEpiWarps; }
 constexpr int threads_of(int epi, bool mx, int split) { return (2 + epi_warps(epi, mx, split) + roles_of(mx) - 1) * 32; }
 constexpr size_t smem_of(int epi, bool mx, int split) {
-  return 1024 + (size_t)stages_of(epi, mx, split) * stage_bytes(mx) + (staged(epi, mx, split) ? 2 * kEpiWarps * kPlaceBytes : 0) + sizeof(Bars);
+  return 1024 + (size_t)stages_of(epi, mx, split) * stage_bytes(mx) + (staged(epi, mx, split) ? epi_warps(epi, mx, split) * kPlaceBytes : 0) + sizeof(Bars);
 }
-static_assert(smem_of(kEpiGateUp, true, 1) <= 227 * 1024 && smem_of(kEpiLinear, false, 1) <= 227 * 1024,
+static_assert(smem_of(kEpiGateUp, true, 1) <= 227 * 1024 && smem_of(kEpiStore, false, 1) <= 227 * 1024 && smem_of(kEpiLinear, false, 1) <= 227 * 1024,
               "shared memory of one CTA");
 
 MOE_DEV void store_cluster(uint32_t addr, uint32_t v) {
@@ -636,7 +636,45 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
                          map_cta(&bar->tempty[MX ? 0 : acc], lead))
                      : "memory");
     };
-    if constexpr (kStaged) {
+    if constexpr (kStaged && EPI == kEpiStore) {
+      // 64 columns at a time go through the warp's place, as bf16, to leave as 128 bytes of a row.
+      uint4* const place = reinterpret_cast<uint4*>(scales + ew * kPlaceBytes);
+      const int to = lane * 8 + (lane & 7);  // piece e of row `lane` at to ^ e
+      const int r0 = lane >> 3, from = r0 * 8 + ((lane & 7) ^ r0);  // a thread's rows are r0 + 4 i: from + 32 i, odd i's ^ 4
+      for (int lt = 0; tile_of<MULTI>(p, pair, pairs, lt, t); ++lt) {
+        const int acc = lt & 1;
+        const Product& q = p.q[MULTI ? t.q : 0];
+        const int N = q.N, row = (2 * t.m + (int)rank) * kBM + part * 32 + r0;
+        const int rows = q.M > row ? (q.M - row + 3) >> 2 : 0;  // of this thread
+        uint16_t* const y = q.y + (size_t)row * N;
+        if (!mbar_wait(&bar->tfull[acc], (lt >> 1) & 1, p.ctl) || aborted(bar)) {
+          set_abort(bar);
+          break;
+        }
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t src = tmem + lanes + acc * kBN + half * 128;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          float v[64];
+#pragma unroll
+          for (int e = 0; e < 64; e += 16) tmem_ld16_async(src + g * 64 + e, v + e);
+          tmem_ld_wait();
+          if (g == 1) release(acc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            place[to ^ e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                       pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          __syncwarp();
+          const int col = t.n * TN + half * 128 + g * 64 + (lane & 7) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < rows && col < N)
+              *reinterpret_cast<uint4*>(y + col + (size_t)(4 * i) * N) = place[(from ^ (i & 1) * 4) + 32 * i];
+          __syncwarp();
+        }
+      }
+    } else if constexpr (kStaged) {
       // The sums of 32 columns at a time change hands through the warp's place in shared memory, so that a thread, which
       // reads a row of them, finishes 8 neighbouring columns (the same in every row) of every eighth row: bias, residual and
       // results then move 64 or 128 bytes of a row at a time, and a column's bias is read once.  (In the place the 16-byte
@@ -845,7 +883,7 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
       // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
       // (SPLIT == 3, linear only: the 16 chunks of 16 columns go two or three to each of the six.)
       constexpr int W = SPLIT == 3 ? 24 : kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
-      static_assert(SPLIT != 3 || EPI == kEpiLinear, "columns of one range per warp");
+      static_assert(SPLIT != 3 || EPI != kEpiGateUp, "columns of one range per warp");
       auto chunk0 = [](int o) { return o * 16 / 6; };
       auto width_of = [&](int owner) {  // columns of its share, both ranges
         return SPLIT == 3 ? (chunk0(owner * 2 + half + 1) - chunk0(owner * 2 + half)) * 16 : 2 * W;
@@ -1055,11 +1093,11 @@ bool set_product(const FfnEngine& e, Product& q, const void* a, const void* b, i
 // = 2048, I = 2048: 29.9, 36.2, 79.5 -> 27.1; T = 2048, d = 2048, I = 8192:
 // 120.4, 223.5, 427.3 -> 120.7.
 template <int EPI, bool MX>
-int split_of(const FfnEngine& e, const Product& q, double* cost) {
+int split_of(const FfnEngine& e, const Product& q, bool three, double* cost) {
   constexpr int kMost = MX && EPI == kEpiGateUp ? 2 : 4;  // mx8: a warp must keep whole groups of 32 neurons
   int split = 1;
   *cost = 1e30;
-  for (int s = 1; s <= kMost && s <= q.blocks; s += EPI == kEpiLinear || s == 1 ? 1 : 2) {
+  for (int s = 1; s <= kMost && s <= q.blocks; s += three || s == 1 ? 1 : 2) {
     const int fit = s == 1 ? e.pairs : s == 2 ? e.pairs2 : s == 3 ? e.pairs3 : e.pairs4;  // clusters that run at a time
     if (fit < 1) break;
     const double rounds = (double)((q.tiles + fit - 1) / fit);
@@ -1070,14 +1108,16 @@ int split_of(const FfnEngine& e, const Product& q, double* cost) {
   return split;
 }
 
+constexpr bool has_three(int epi, bool b_mn) { return epi == kEpiLinear || (epi == kEpiStore && b_mn); }
+
 template <int EPI, bool A_MN, bool B_MN, bool MX>
-cudaError_t run(const FfnEngine& e, GemmParams& p, cudaStream_t st) {
+cudaError_t run(const FfnEngine& e, GemmParams& p, cudaStream_t st, bool three = false) {
   p.ctl = e.ctl;
   double cost;
-  const int split = split_of<EPI, MX>(e, p.q[0], &cost), tiles = p.q[0].tiles;
+  const int split = split_of<EPI, MX>(e, p.q[0], three, &cost), tiles = p.q[0].tiles;
   if (split == 1) return launch<EPI, A_MN, B_MN, MX, 1>(p, tiles < e.pairs ? tiles : e.pairs, st);
   if (split == 2) return launch<EPI, A_MN, B_MN, MX, 2>(p, tiles, st);
-  if constexpr (EPI == kEpiLinear)
+  if constexpr (has_three(EPI, B_MN))
     if (split == 3) return launch<EPI, A_MN, B_MN, MX, 3>(p, tiles, st);
   if constexpr (!(MX && EPI == kEpiGateUp)) return launch<EPI, A_MN, B_MN, MX, 4>(p, tiles, st);
   return cudaErrorInvalidValue;
@@ -1101,7 +1141,7 @@ template <int EPI, bool A_MN, bool B_MN, bool MX>
 cudaError_t prepare_splits(FfnEngine* e) {
   cudaError_t err = prepare<EPI, A_MN, B_MN, MX, 1>(&e->pairs);
   if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 2>(&e->pairs2);
-  if constexpr (EPI == kEpiLinear)
+  if constexpr (has_three(EPI, B_MN))
     if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 3>(&e->pairs3);
   if constexpr (!(MX && EPI == kEpiGateUp))
     if (err == cudaSuccess) err = prepare<EPI, A_MN, B_MN, MX, 4>(&e->pairs4);
@@ -1211,7 +1251,7 @@ namespace {
 // grad_h: T = 501 in one launch 45.4 us, dx first 39.3; T = 256 each by itself
 // 38.6 us, dx first 33.6.  For few tokens launch_skinny_backward has done dx,
 // and the others have one k block.
-cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* launches, cudaStream_t st) {
+cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, bool three, int* launches, cudaStream_t st) {
   const bool dx_first = all[0].blocks >= all[1].blocks;  // the longer reduction
 
   // Times in k blocks.  One launch: at best even, at worst one light tile more, and no less than the heavy tiles' (a tile
@@ -1228,7 +1268,7 @@ cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* l
   int split[3];
   for (int i = 0; i < 3; ++i) {
     c[i] = 0, split[i] = 1;
-    if (all[i].tiles) split[i] = split_of<kEpiStore, false>(e, all[i], &c[i]);
+    if (all[i].tiles) split[i] = split_of<kEpiStore, false>(e, all[i], three, &c[i]);
   }
   const double weights = (double)((weight_tiles + e.pairs - 1) / e.pairs) * (all[1].blocks + each) + first;
   // (these estimates are good to about a tenth, and one launch has less to go wrong)
@@ -1248,7 +1288,7 @@ cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* l
   } else if (two && all[0].y) {
     GemmParams dx{};
     dx.q[0] = all[0];
-    const cudaError_t err = run<kEpiStore, false, true, false>(e, dx, st);
+    const cudaError_t err = run<kEpiStore, false, true, false>(e, dx, st, three);
     if (err != cudaSuccess) return err;
     *launches = 1;
     all[0].y = nullptr;
@@ -1280,8 +1320,8 @@ cudaError_t launch_grads(const FfnEngine& e, Product (&all)[3], bool few, int* l
   for (int i = 0; i < p.count && err == cudaSuccess; ++i) {
     GemmParams one{};
     one.q[0] = p.q[i];
-    err = one.q[0].a_mn ? run<kEpiStore, true, true, false>(e, one, st)
-                        : run<kEpiStore, false, true, false>(e, one, st);
+    err = one.q[0].a_mn ? run<kEpiStore, true, true, false>(e, one, st, three)
+                        : run<kEpiStore, false, true, false>(e, one, st, three);
   }
   return err;
 }
@@ -1295,7 +1335,7 @@ cudaError_t launch_ffn_grads(const FfnEngine& e, const FfnShape& s, const FfnBac
       !set_product<kEpiStore, true, true, false>(e, all[1], sc.dpre, a.x, 2 * s.I, s.d, s.T, s.d, a.dgate_up) ||
       !set_product<kEpiStore, true, true, false>(e, all[2], a.dy, sc.h, s.d, s.I, s.T, s.I, a.ddown))
     return cudaErrorInvalidValue;
-  return launch_grads(e, all, few_tokens(s), launches, st);
+  return launch_grads(e, all, few_tokens(s), false, launches, st);
 }
 
 cudaError_t launch_linear_grads(const FfnEngine& e, const LinearShape& s, const uint16_t* dpre, const void* x,
@@ -1304,7 +1344,7 @@ cudaError_t launch_linear_grads(const FfnEngine& e, const LinearShape& s, const 
   if (!set_product<kEpiStore, false, true, false>(e, all[0], dpre, w, s.T, s.k, s.n, s.k, dx) ||
       !set_product<kEpiStore, true, true, false>(e, all[1], dpre, x, s.n, s.k, s.T, s.k, dw))
     return cudaErrorInvalidValue;
-  return launch_grads(e, all, few_tokens(s, s.k), launches, st);
+  return launch_grads(e, all, few_tokens(s, s.k), true, launches, st);
 }
 
 cudaError_t launch_linear_tiles(const FfnEngine& e, const LinearShape& s, const LinearForwardArgs& a, cudaStream_t st) {
@@ -1319,7 +1359,7 @@ cudaError_t launch_linear_tiles(const FfnEngine& e, const LinearShape& s, const 
   if (!set_product<kEpiLinear, false, false, false>(e, p.q[0], a.x, a.w, s.T, s.n, s.k, s.n, a.y))
     return cudaErrorInvalidValue;
   if (!aligned32(a.pre)) p.q[0].wide = 0;
-  return run<kEpiLinear, false, false, false>(e, p, st);
+  return run<kEpiLinear, false, false, false>(e, p, st, true);
 }
 
 }  // namespace moe
