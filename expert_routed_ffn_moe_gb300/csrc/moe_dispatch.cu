@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(RowsArgs a) {
 // A token belongs to W warps of a block, which take its slices in turn; their parts
 // of dw meet in shared memory, in order.  K picks at a time.
 template <int VEC, int K>
-constexpr int kGradPieces = (VEC == 8 ? 1 : VEC == 2 ? 2 : 4) * (K == 2 ? VEC == 8 ? 4 : 2 : 1);
+constexpr int kGradPieces = (VEC == 8 ? 1 : VEC == 2 ? 2 : 4) * (K == 2 ? VEC == 8 ? 4 : 2 : K == 4 && VEC == 8 ? 2 : 1);
 template <typename YT, typename RT, int VEC, int W, int K>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(RowsArgs a) {
   constexpr int P = kGradPieces<VEC, K>, kTokens = kRowThreads / 32 / W, kPicks = K;
@@ -486,7 +486,12 @@ struct CombineGrad {
     const int most = VEC == 8 ? 16 * 152 / a.T : rounds < 1 ? 1 : VEC == 1 ? rounds : rounds < 4 ? rounds : 4;
     return most >= 8 ? launch<8, K>(a, st) : most >= 4 ? launch<4, K>(a, st) : most >= 2 ? launch<2, K>(a, st) : launch<1, K>(a, st);
   }
-  static cudaError_t run(const RowsArgs& a, cudaStream_t st) { return a.k <= 2 ? split<2>(a, st) : split<8>(a, st); }
+  // Picks at a time: 2, 4 or 8, with as many loads in flight (T = 2458, d = 3688, k = 4 28.8 us for 43.1 with 8 places for
+  // them; k = 8 the other way round, T = 4000, d = 2048 in fp32 48.6 for 56.7 with 4).  Odd widths, whose loads are of one
+  // value, have no registers for 8: k = 8, T = 16384, d = 513 137 us for 77.8 with 4; T = 4000, d = 2501 89.3 for 80.4.
+  static cudaError_t run(const RowsArgs& a, cudaStream_t st) {
+    return a.k <= 2 ? split<2>(a, st) : a.k <= 4 || VEC == 1 ? split<4>(a, st) : split<VEC == 1 ? 4 : 8>(a, st);
+  }
 };
 
 }  // namespace
