@@ -480,7 +480,7 @@ struct CombineGrad {
   static cudaError_t split(const RowsArgs& a, cudaStream_t st) {
     // Warps per token.  Aligned: as many as keep the warps of all tokens below 16 per SM (k = 8, d = 2048: T = 500 12.2,
     // 8.4, 7.3, 8.1 us with 1, 2, 4, 8; T = 2000 23.2, 25.0, 26.7, 29.9).  Others move smaller pieces, which several warps
-    // side by side do better at any T (T = 4000, d = 2501: 115, 107, 117, 90; d = 2502: 85, 73, 67, 72), as far as each has
+    // side by side do better at any T (k = 8, T = 4000, d = 2501: 89, 90, 82, 81; d = 2502: 85, 73, 67, 72), as far as each has
     // two rounds of them.
     const int rounds = a.d / (2 * 32 * VEC * kGradPieces<VEC, K>);
     const int most = VEC == 8 ? 16 * 152 / a.T : rounds < 1 ? 1 : VEC == 1 ? rounds : rounds < 4 ? rounds : 4;
