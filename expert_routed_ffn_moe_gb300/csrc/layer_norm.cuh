@@ -149,13 +149,12 @@ MOE_DEV void warp_sum4(float (&v)[4]) {
 // Sums over the R threads of a row, in every one of them: the warps' sums meet in
 // `red`, another array from one call to the next, so that one barrier per call
 // suffices.
-// The rows of a block need not keep step: a row's threads have a barrier of their own.
-template <int R, int N, int ROWS = ln_rows(R)>
+template <int R, int N>
 struct RowRed {
-  float v[ROWS][N][(R / 32 + 3) / 4 * 4];
+  float v[ln_rows(R)][N][(R / 32 + 3) / 4 * 4];
 };
-template <int R, int N, int ROWS>
-MOE_DEV void ln_row_sums(float (&v)[N], RowRed<R, N, ROWS>& red) {
+template <int R, int N>
+MOE_DEV void ln_row_sums(float (&v)[N], RowRed<R, N>& red) {
   static_assert(N == 1 || N == 2 || N == 4, "see the sums over a warp");
   if constexpr (N == 4)
     warp_sum4(v);
@@ -169,10 +168,7 @@ MOE_DEV void ln_row_sums(float (&v)[N], RowRed<R, N, ROWS>& red) {
 #pragma unroll
       for (int i = 0; i < N; ++i) red.v[group][i][warp] = v[i];
     }
-    if (ROWS == 1)
-      __syncthreads();
-    else
-      asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(group + 1), "n"(R) : "memory");
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float s = 0.f;

@@ -19,35 +19,28 @@
 namespace moe {
 namespace {
 
-// Rows of a block: as many as 512 threads have, and one block per SM, so that few blocks leave sums to add up; a call of
-// fewer rows has fewer in a block.  Against blocks of 256 threads, two to an SM (us): T = 16384, d = 4096 86.0 for 94.5, fp32
-// 174 for 190, d = 1024 29.0 for 29.3; T = 64, d = 2048 5.7 for 9.1; T = 1076, d = 2192, fp32 16.6 for 15.4.
-constexpr int kMost = 512;
-constexpr int grad_rows(int R) { return R < kMost ? kMost / R : 1; }
-
 // Operands that come through the ring (s and dy, and ds where that leaves room for a row more than the two in work), and
-// its rows.
+// its rows; two blocks of 256 threads share an SM.
 template <typename T, int R>
 constexpr int kOperands = R < 1024 ? 3 : 2;
 template <typename T, int R>
 constexpr int kStagesOf = [] {
-  const int row = grad_rows(R) * 16 * R * (int)sizeof(T) * kOperands<T, R>, most = 218 * 1024 / row;
+  const int row = ln_rows(R) * 16 * R * (int)sizeof(T) * kOperands<T, R>, most = (R <= 512 ? 220 / (512 / ln_block(R)) - 2 : 220) * 1024 / row;
   return most < 4 ? most : 4;
 }();
 
 template <typename ST, int R, bool ODD>
-__global__ void __launch_bounds__(grad_rows(R) * R, 1) layer_norm_grad_kernel(LayerNormGradArgs a) {
-  const int rows = blockDim.x / R;  // at most grad_rows(R)
-  constexpr int S = kStagesOf<ST, R>, kOps = kOperands<ST, R>;
+__global__ void __launch_bounds__(ln_block(R), R <= 512 ? 512 / ln_block(R) : 1) layer_norm_grad_kernel(LayerNormGradArgs a) {
+  constexpr int kRows = ln_rows(R), S = kStagesOf<ST, R>, kOps = kOperands<ST, R>;
   constexpr int kSlot = 16 * R * (int)sizeof(ST);  // bytes of a row
   constexpr bool AHEAD = S >= 3;    // the next row's sums go with this one's
   constexpr bool CACHE = R < 1024;  // weight, c and g in registers (else read again)
-  __shared__ RowRed<R, 4, grad_rows(R)> red[2];
-  extern __shared__ float4 ring4[];  // [rows][S][kOps] rows; at the end [rows][2][16 R] sums
+  __shared__ RowRed<R, 4> red[2];
+  extern __shared__ float4 ring4[];  // [kRows][S][kOps] rows; at the end [kRows][2][16 R] sums
   uint8_t* ring = reinterpret_cast<uint8_t*>(ring4);
   follow();
   const int tid = threadIdx.x % R, group = threadIdx.x / R;
-  const int stride = gridDim.x * rows, first = blockIdx.x * rows + group;
+  const int stride = gridDim.x * kRows, first = blockIdx.x * kRows + group;
   const Windows<R, ODD> win(tid, first, a.d);
   const size_t n = (size_t)a.T * a.d;
   const bool with_ds = a.ds && a.dx;
@@ -105,11 +98,13 @@ __global__ void __launch_bounds__(grad_rows(R) * R, 1) layer_norm_grad_kernel(La
   };
 
   float sum[4] = {0.f, 0.f, 0.f, 0.f};  // c^2 and g c of this row, s and g of the next
-  int row = first, slot = 0, parity = 0;
+  int base = blockIdx.x * kRows, slot = 0, parity = 0;
   copies_wait<S - 1>();
-  first_sums(first, 0, sum[2], sum[3]);
+  first_sums(base + group, 0, sum[2], sum[3]);
   ln_row_sums<R>(sum, red[1]);
-  for (int it = 0; row < a.T; row += stride, ++it) {
+  for (int it = 0; base < a.T; base += stride, ++it) {
+    const int row = base + group;
+    const bool live = kRows == 1 || row < a.T;
     const size_t lo = (size_t)row * a.d;
     const int next = slot + 1 == S ? 0 : slot + 1;
     const float mean = sum[2] * inv_d, g_mean = sum[3] * inv_d;
@@ -125,7 +120,7 @@ __global__ void __launch_bounds__(grad_rows(R) * R, 1) layer_norm_grad_kernel(La
     };
 #pragma unroll
     for (int o = 0; o < 2; ++o)
-      if (win.in[o]) {
+      if (win.in[o] && live) {
         if (kOps == 2 && with_ds) win.load(late[o], from(2), lo, o, n);
         centred(o);
 #pragma unroll
@@ -145,7 +140,7 @@ __global__ void __launch_bounds__(grad_rows(R) * R, 1) layer_norm_grad_kernel(La
     const float shift = -rstd * g_mean, slope = -rstd * rstd * (sum[1] * rstd * inv_d);
 #pragma unroll
     for (int o = 0; o < 2; ++o)
-      if (win.in[o]) {
+      if (win.in[o] && live) {
         if (!CACHE) centred(o);
         const F8 y = value(slot, 1, o);
 #pragma unroll
@@ -187,11 +182,12 @@ __global__ void __launch_bounds__(grad_rows(R) * R, 1) layer_norm_grad_kernel(La
   }
   __syncthreads();
   float* to = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  for (int k = threadIdx.x; k < 2 * a.d; k += blockDim.x) {
+  for (int k = threadIdx.x; k < 2 * a.d; k += ln_block(R)) {
     const int half = k >= a.d, c = k - half * a.d;
     float v = 0.f;
-    for (int r = 0; r < rows; ++r) {
-      const int head = ODD ? (int)((long long)(blockIdx.x * rows + r) * a.d & 7) : 0;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int head = ODD ? (int)((long long)(blockIdx.x * kRows + r) * a.d & 7) : 0;
       v += sums[r * 32 * R + half * 16 * R + c + head];
     }
     if (gridDim.x > 1) {
@@ -214,7 +210,7 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_sum_kernel(const float* 
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < 2 * d) {
-    constexpr int kBatch = 5;  // in flight at once: 160 partial rows
+    constexpr int kBatch = 10;  // in flight at once: 304 partial rows
     for (int r0 = threadIdx.y; r0 < rows; r0 += 32 * kBatch) {
       float x[kBatch];
 #pragma unroll
@@ -242,16 +238,18 @@ struct Backward {
   template <int R>
   struct Launch {
     static cudaError_t run(const LayerNormGradArgs& a, cudaStream_t st) {
-      constexpr size_t per = kStagesOf<ST, R> * kOperands<ST, R> * sizeof(ST), row = (size_t)16 * R * per;
-      static_assert(kStagesOf<ST, R> >= 1 && grad_rows(R) * row <= 220 * 1024 && per >= 8, "the ring; two rows of fp32 in it");
+      constexpr int kBlock = ln_block(R), kRows = ln_rows(R);
+      constexpr size_t per = kStagesOf<ST, R> * kOperands<ST, R> * sizeof(ST), smem = (size_t)kRows * 16 * R * per;
+      static_assert(kStagesOf<ST, R> >= 1 && smem <= 224 * 1024 && per >= 8, "the ring; the sums of two rows of fp32 in it");
       const auto kernel = layer_norm_grad_kernel<ST, R, ODD>;
       static std::atomic<uint64_t> allowed{0};
-      const cudaError_t err = allow_once(kernel, grad_rows(R) * row, allowed);
+      const cudaError_t err = allow_once(kernel, smem, allowed);
       if (err != cudaSuccess) return err;
-      static const int resident = min(resident_blocks(kernel, grad_rows(R) * R, grad_rows(R) * row), kLayerNormPartials) / 8 * 8;
-      const int kRows = min((a.T + resident - 1) / resident, grad_rows(R));
-      const int grid = min((a.T + kRows - 1) / kRows, resident), kBlock = kRows * R;
-      const size_t smem = kRows * row;
+      int grid = (a.T + kRows - 1) / kRows;
+      if (grid > 128) {
+        static const int resident = min(resident_blocks(kernel, kBlock, smem), kLayerNormPartials) / 8 * 8;
+        if (grid > resident) grid = resident;
+      }
       if (ODD && !steps_of_eight(a.T, grid * kRows)) return cudaErrorInvalidValue;
       const cudaError_t e = launch_after(kernel, grid, dim3(kBlock), smem, st, a);
       if (e != cudaSuccess || (!a.dw && !a.db) || grid == 1) return e;
