@@ -13,24 +13,27 @@
 // computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA loads its
 // own 128 rows of A and half of B's 256 rows, so a 64-deep k block costs each
 // SM 32 KB of shared-memory fill for 512 cycles of MMA (a lone CTA's 128 x 256
-// tile takes 48 KB for the same work).  Per CTA 11 warps (12 for mx8):
-//   warps 0, 10, 11  TMA producers (one thread each) of a ring of k blocks,
+// tile takes 48 KB for the same work).  Per CTA 11 warps (12 for mx8, 19 for linear):
+//   warp 0 and the last  TMA producers (one thread each) of a ring of k blocks,
 //              128-byte swizzle: A, B, and mx8's scales.  A thread takes some 100
 //              cycles to issue a copy and up to 300 to see that a stage is free,
 //              against a k block's 512 cycles of MMAs;
 //   warp 1     allocates all 512 TMEM columns: two fp32 accumulators of 256
 //              columns; in the pair's first CTA one thread issues the MMAs;
-//   warps 2-9  epilogue: two warps for each quarter of the TMEM lanes, each
-//              taking one half of the columns; a thread has a row and writes
-//              16 columns (32 bytes) at a time.
+//   warps 2 on  epilogue: two warps (linear: four) for each quarter of the TMEM
+//              lanes, each taking its part of the columns; a thread has a row of
+//              the sums.  Products leave through shared memory by whole lines; for
+//              linear the sums change hands there (see the two blocks below); the
+//              other forms write 16 columns (32 bytes) of a row at a time.
 // The epilogue of tile i overlaps the main loop of tile i + 1.  In the gate/up
 // product B's first half holds gate rows and the second half the up rows of the
 // same 128 neurons, so the activation finishes in the accumulator's columns.
 //
 // A product with fewer tiles than pairs splits the reduction over 2 or 4 pairs
-// of one cluster (SPLIT; `linear` also over 3: 16 tiles find 15 clusters of 4 pairs
-// on the device, T = 128, 4096 to 4096 17.5 us with 2, 16.0 with 3).  Each pair ends with fp32 sums of the whole tile; the
-// columns are divided among the pairs, every CTA sends its sums of the others'
+// of one cluster (SPLIT; linear and its gradients also over 3: 16 tiles find 15
+// clusters of 4 pairs on the device, T = 128, 4096 to 4096 17.5 us with 2, 16.0
+// with 3; backward T = 300, 2048 to 8192 50.0 and 43.3).  Each pair ends with fp32
+// sums of the whole tile; the columns are divided among the pairs, every CTA sends its sums of the others'
 // columns to them through distributed shared memory (the ring's memory, free by
 // then), and each adds its columns' sums in the order of k and finishes them.
 //
@@ -637,7 +640,9 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
                      : "memory");
     };
     if constexpr (kStaged && EPI == kEpiStore) {
-      // 64 columns at a time go through the warp's place, as bf16, to leave as 128 bytes of a row.
+      // 64 columns at a time go through the warp's place, as bf16, to leave as 128 bytes of a row.  Against 32 bytes of
+      // each of a warp's rows, a backward call (us): 41 tokens, 1256 to 11376 28.6 for 31.8; T = 387, 1976 to 7472 49 for
+      // 53; T = 512, 4096 to 4096 33.9 for 35.5; T = 4096, 4096 to 16384 (long reductions) 640-665 for 640-650.
       uint4* const place = reinterpret_cast<uint4*>(scales + ew * kPlaceBytes);
       const int to = lane * 8 + (lane & 7);  // piece e of row `lane` at to ^ e
       const int r0 = lane >> 3, from = r0 * 8 + ((lane & 7) ^ r0);  // a thread's rows are r0 + 4 i: from + 32 i, odd i's ^ 4
@@ -679,7 +684,13 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
       // reads a row of them, finishes 8 neighbouring columns (the same in every row) of every eighth row: bias, residual and
       // results then move 64 or 128 bytes of a row at a time, and a column's bias is read once.  (In the place the 16-byte
       // pieces of a row are swapped by the row: neither side finds a bank twice.)  What the next columns need is asked for
-      // ahead of them, and the next tile's residual brought to L2.
+      // ahead of them, and the next tile's residual brought to L2.  All this waits more than it computes, so that sixteen
+      // warps are worth a stage of the ring (whose memory their places take).  Against eight warps whose threads write their
+      // own rows (us; T, in, out): 4719, 304, 15616 gelu 70 for 117, as it is 52 for 73, with an fp32 residual 133 for 160;
+      // 4096, 1024, 4096 gelu and a residual 33.7 for 42.7; 16384, 1024, 4096 gelu, fp32 residual, pre 159 for 187; one
+      // tile for a pair (777, 1000, 2744) 19.0 for 18.3.  Eight warps this way 93 (first), sixteen with 16 columns at a
+      // time and all six stages 78.  A short reduction is bound by this epilogue (3.4-4.6 us a tile, of which ~1.6 are
+      // accesses to shared memory; a tile of K = 304 multiplies for 1.4), from K = ~1000 on by the MMAs.
       const Product& q = p.q[0];
       const int M = q.M, N = q.N;
       const bool f32 = p.y32, bias_bf16 = p.bias_bf16;
@@ -1108,6 +1119,7 @@ int split_of(const FfnEngine& e, const Product& q, bool three, double* cost) {
   return split;
 }
 
+// Products that may be split over three pairs: linear and its gradients' (the feed-forward block's are not).
 constexpr bool has_three(int epi, bool b_mn) { return epi == kEpiLinear || (epi == kEpiStore && b_mn); }
 
 template <int EPI, bool A_MN, bool B_MN, bool MX>
