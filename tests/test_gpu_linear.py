@@ -171,3 +171,53 @@ def test_launch_count_and_errors():
     with pytest.raises(moe.MoeError) as e:  # an activation's gradient needs pre
         op.backward(x, None, w, None, x)
     assert e.value.code == moe.MOE_ERR_ARG
+
+
+# a stream's kinds, split and unsplit tiles, and many tiles of a short reduction per pair of CTAs
+SOME = [(1, 64, 200), (9, 64, 200), (70, 4096, 264), (300, 136, 520), (2100, 72, 5000)]
+
+
+@pytest.mark.parametrize("T,k,n", SOME)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_a_value_beyond_the_range_stays_alone(T, k, n, act):
+    x, w, b, r = operands(gen(T + n), T, k, n, F32, F32)
+    op = moe.Linear(k, n, T, activation=ACTS[act], training=True)
+    want = oc.linear(x, w, b, r, act, F32)["y"]
+    pre = op.forward(x, w, b, r, save=True, y_dtype=F32)[1]
+    cols = torch.tensor([0, 3, 6, 17, 33, 66, 134, 199])
+    far = torch.tensor([float("nan"), float("inf"), 1e30, -1e30, float("nan"), 3e38, -3e38, float("inf")], device="cuda")
+    b[cols] = far
+    got = op.forward(x, w, b, r, y_dtype=F32)
+    others = torch.ones(n, dtype=torch.bool)
+    others[cols] = False
+    # A value's last bits may follow its neighbour, with which it shares a reciprocal: the logistic function is then off by
+    # the rounding of the two denominators' product (2^-24), the reciprocal's last place (2^-23) and that of the product
+    # with the other denominator (2^-24); times the value once more 2^-24: 2.5 * 2^-23 < 2^-21, within the bound.
+    near(got[:, others], *(v[:, others] for v in want), "y")
+    far_y = torch.where(far < 0, 0.0, far) + r[:, cols]  # act is the value itself, or 0
+    off = torch.where(far_y.isfinite() & (far > 0), 2.0 ** -21 * far_y.abs(), 0.0)
+    same = (got[:, cols] == far_y) | (got[:, cols].isnan() & far_y.isnan()) | ((got[:, cols] - far_y).abs() <= off)
+    assert same.all(), got[:, cols][~same]
+
+    dy = normal(gen(T), T, n)
+    want = oc.linear_backward(x, pre, w, dy, act, F32)
+    pre[:, cols] = far.to(BF)
+    dw, db = op.backward(x, pre, w, b, dy, dx=False)[1:]
+    near(dw[others], *(v[others] for v in want["dweight"]), "dweight")
+    near(db[others], *(v[others] for v in want["dbias"]), "dbias")
+    nan, down = torch.isnan(far).cpu(), (far < 0).cpu()
+    assert torch.isnan(db[cols[nan]]).all()
+    assert (db[cols[down]] == 0).all() and (dw[cols[down]] == 0).all()
+    assert op.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T,k,n", SOME + [(2500, 512, 4352)])
+@pytest.mark.parametrize("y", [BF, F32])
+def test_the_result_may_take_the_residuals_place(T, k, n, y):
+    x, w, b, r = operands(gen(T + k), T, k, n, BF, y)
+    op = moe.Linear(k, n, T, activation=moe.MOE_ACT_GELU)
+    want = oc.linear(x, w, b, r, "gelu", y)["y"]
+    apart = op.forward(x, w, b, r)
+    near(apart, *want, "y")
+    assert op.forward(x, w, b, r, y=r).data_ptr() == r.data_ptr()
+    assert torch.equal(r, apart) and op.status() == moe.MOE_OK
