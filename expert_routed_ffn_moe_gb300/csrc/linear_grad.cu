@@ -18,15 +18,16 @@ namespace {
 constexpr int kCols = 64, kThreads = 256, kLanes = kThreads / (kCols / 8);  // 32 rows at a time
 constexpr int kMaxRanks = 8;
 
-// act'(g) of two values, as act_and_grad(): with p = logistic(z), z = g or the argument of gelu's tanh form doubled,
-//   act' = p + g p (1 - p) z'(g).
+// act'(g) of two values: with p = logistic(z), z = g or the argument of gelu's tanh form doubled, and q = 1 - p,
+//   act' = p + g p q z'(g).
+// Beyond g = 10 (gelu) or 88 (silu) q is 0 and act' is p, 1 to 2^-22; below -7.5 or -42 p and act' are 0.
 template <int ACT>
 MOE_DEV float2 act_grad2(float2 g) {
   constexpr float kGelu = 1.5957691216057308f;
-  const float2 g2 = mul2(g, g), p = logistic2(act_exponent2<ACT>(g, g2));
-  const float2 a = mul2(g, p), q = fma2(p, both(-1.f), both(1.f));
+  float2 q;
+  const float2 g2 = mul2(g, g), p = logistic2(act_exponent2<ACT>(g, g2), q), a = mul2(g, p);
   if (ACT == MOE_ACT_SILU) return fma2(a, q, p);
-  // (beyond |g| = 10 the second term vanishes; the bound keeps an overflowing g^2 out)
+  // (beyond |g| = 10 the second term is 0; the bound keeps an overflowing g^2 out)
   const float2 dz = fma2(make_float2(fminf(g2.x, 100.f), fminf(g2.y, 100.f)), both(kGelu * 0.134145f), both(kGelu));
   return fma2(mul2(a, q), dz, p);
 }

@@ -117,14 +117,21 @@ MOE_DEV float2 act_exponent2(float2 g, float2 g2) {
 }
 // 1 / (1 + 2^e), 0 from 2^-60 down (a huge negative g then gives 0; NaN stays NaN through the product with g): one
 // reciprocal for both values, 1 / (a b) times b and a, as the special functions are what a tile's epilogue takes longest for.
-MOE_DEV float2 logistic2(float2 e) {
+// A value's last places thus follow its neighbour, and where 2^e vanishes the result is 1 to 2^-22, not exactly: one minus
+// it is `rest`, 2^e / (1 + 2^e), which is 0 there, and never a difference (a gradient multiplies it by g).
+MOE_DEV float2 logistic2(float2 e, float2& rest) {
   constexpr float kFar = 60.f;
-  const float2 d = add2(make_float2(exp2_fast(fminf(e.x, kFar)), exp2_fast(fminf(e.y, kFar))), both(1.f));
+  const float2 t = make_float2(exp2_fast(fminf(e.x, kFar)), exp2_fast(fminf(e.y, kFar))), d = add2(t, both(1.f));
   const float r = reciprocal_fast(d.x * d.y);
   float2 p = mul2(make_float2(d.y, d.x), both(r));
+  rest = mul2(t, p);
   p.x = e.x > kFar ? 0.f : p.x;
   p.y = e.y > kFar ? 0.f : p.y;
   return p;
+}
+MOE_DEV float2 logistic2(float2 e) {
+  float2 rest;
+  return logistic2(e, rest);
 }
 template <int ACT>
 MOE_DEV float2 act_value2(float2 g) {
