@@ -150,7 +150,7 @@ MOE_DEV void warp_sum4(float (&v)[4]) {
 // `red`, another array from one call to the next, so that one barrier per call
 // suffices.
 template <int R, int N>
-struct RowRed {
+struct __align__(16) RowRed {
   float v[ln_rows(R)][N][(R / 32 + 3) / 4 * 4];
 };
 template <int R, int N>
@@ -174,6 +174,7 @@ MOE_DEV void ln_row_sums(float (&v)[N], RowRed<R, N>& red) {
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < R / 32; w += 4) {
+        static_assert(alignof(RowRed<R, N>) >= alignof(float4), "read four at a time");
         const float4 q = *reinterpret_cast<const float4*>(&red.v[group][i][w]);
         s += q.x;
         if (w + 1 < R / 32) s += q.y;
