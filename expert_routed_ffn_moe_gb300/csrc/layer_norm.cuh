@@ -121,19 +121,7 @@ MOE_DEV F8 param_of(const Windows<R, ODD>& win, const void* p, int dtype, int o,
 // Whether rows that are not aligned may be walked over in steps of `stride`: see Windows.
 inline bool steps_of_eight(int T, int stride) { return stride >= T || stride % 8 == 0; }
 
-// Sums of two values over a warp, each in every lane: the halves of the warp add
-// up one value each after the first exchange.
-MOE_DEV void warp_sum2(float& a, float& b) {
-  const bool up = (threadIdx.x & 16) != 0;
-  float mine = up ? b : a;
-  mine += __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
-  a = up ? other : mine;
-  b = up ? mine : other;
-}
-// The same of four values: two exchanges leave one value each to a quarter of the warp.
+// Sums of four values over a warp, each in every lane: two exchanges leave one value each to a quarter of the warp.
 MOE_DEV void warp_sum4(float (&v)[4]) {
   const bool up = (threadIdx.x & 16) != 0, odd = (threadIdx.x & 8) != 0;
   float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
@@ -155,11 +143,9 @@ struct __align__(16) RowRed {
 };
 template <int R, int N>
 MOE_DEV void ln_row_sums(float (&v)[N], RowRed<R, N>& red) {
-  static_assert(N == 1 || N == 2 || N == 4, "see the sums over a warp");
+  static_assert(N == 1 || N == 4, "see the sums over a warp");
   if constexpr (N == 4)
     warp_sum4(v);
-  else if constexpr (N == 2)
-    warp_sum2(v[0], v[1]);
   else
     v[0] = warp_sum(v[0]);
   if constexpr (R > 32) {
