@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 #include "moe_common.cuh"
 
@@ -267,6 +269,23 @@ inline bool make_scale_map(EncodeTiledFn encode, CUtensorMap* m, const void* ptr
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A number that a device is asked for once; devices may differ, so it is kept by device (plus one).  After a query that
+// failed the call goes on with the number that `ask` left, which is not kept, and no error stays behind.
+typedef std::atomic<int> ByDevice[64];
+template <typename Ask>
+int once_per_device(ByDevice& known, Ask ask) {
+  int dev = 64, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) {
+    const int kept = known[dev].load(std::memory_order_acquire);
+    if (kept) return kept - 1;
+  }
+  if (ask(&n) != cudaSuccess)
+    cudaGetLastError();
+  else if (dev < 64)
+    known[dev].store(n + 1, std::memory_order_release);
+  return n;
 }
 
 struct FfnEngine {

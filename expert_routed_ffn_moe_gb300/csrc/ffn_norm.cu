@@ -426,14 +426,14 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
   const int rows = a.y_dtype == MOE_MX8 ? (a.T + 127) / 128 * 128 : a.T;
   int grid = (rows + kRows - 1) / kRows;
   // (a grid of fewer blocks than SMs needs no look at what is resident; without the weight in shared memory the answer
-  // is one number per kernel)
+  // is one number per kernel and device)
   if (grid > 128) {
     int most;
     if constexpr (ODD) {
       most = resident_blocks(kernel, kBlock, smem);
     } else {
-      static const int resident = resident_blocks(kernel, kBlock, 0);
-      most = resident;
+      static ByDevice known;
+      most = resident_blocks(kernel, kBlock, 0, known);
     }
     if (grid > most) grid = most;
   }
@@ -471,8 +471,8 @@ cudaError_t grad_launch(const NormGradArgs& a, cudaStream_t st) {
     if constexpr (ODD) {
       most = resident_blocks(kernel, kBlock, smem);
     } else {
-      static const int resident = resident_blocks(kernel, kBlock, R == 32 ? 512 * 4 * kRows : 0);  // (the widest)
-      most = resident;
+      static ByDevice known;
+      most = resident_blocks(kernel, kBlock, R == 32 ? 512 * 4 * kRows : 0, known);  // (the widest)
     }
     if (most > kNormPartials) most = kNormPartials;
     if (grid > most) grid = most;

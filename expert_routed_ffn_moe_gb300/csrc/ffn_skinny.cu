@@ -495,16 +495,16 @@ cudaLaunchConfig_t config(int tiles, int C, cudaLaunchAttribute (&at)[2]) {
 }
 // Clusters of 8 on SMs of their own: half of what runs at a time, where two CTAs share an SM.
 template <bool MX, int KIND, int NT>
-int lone_clusters() {
+cudaError_t lone_clusters(int* lone) {
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = config<MX, KIND, NT>(1, kMaxCluster, at);
   cfg.numAttrs = 1;
-  int n = 0, per = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, ffn_skinny_kernel<MX, KIND, NT>, &cfg) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, ffn_skinny_kernel<MX, KIND, NT>, kThreads, cfg.dynamicSmemBytes) !=
-          cudaSuccess || per < 1)
-    return 0;
-  return n / per;
+  int n = 0, per = 0;
+  cudaError_t err = cudaOccupancyMaxActiveClusters(&n, ffn_skinny_kernel<MX, KIND, NT>, &cfg);
+  if (err == cudaSuccess)
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, ffn_skinny_kernel<MX, KIND, NT>, kThreads, cfg.dynamicSmemBytes);
+  *lone = err == cudaSuccess && per > 0 ? n / per : 0;
+  return err;
 }
 template <bool MX, int KIND, int NT>
 cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
@@ -515,8 +515,8 @@ cudaError_t run(const FfnEngine& e, SkinnyParams p, cudaStream_t st) {
     // A call is this kernel alone, and clusters of 8 that have to share SMs, as they find no eight free ones in their part
     // of the device, cost more than they bring: 16 tiles (T = 16, d = 4096 to 2048) 13.6 us with 8, 9.0 with 4; 8 tiles
     // (4096 to 1024) 6.8 with 8, 8.0 with 4.
-    static const int lone = lone_clusters<MX, KIND, NT>();
-    if (C == 8 && tiles > lone) C = 4;
+    static ByDevice known;
+    if (C == 8 && tiles > once_per_device(known, lone_clusters<MX, KIND, NT>)) C = 4;
   }
   p.log_cluster = C == 8 ? 3 : C >> 1;
   cudaLaunchAttribute at[2];

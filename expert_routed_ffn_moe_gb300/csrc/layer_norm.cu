@@ -119,7 +119,8 @@ cudaError_t launch(const LayerNormArgs& a, cudaStream_t st) {
   const auto kernel = layer_norm_kernel<XT, ST, R, C>;
   int grid = (a.T + kRows - 1) / kRows;
   if (grid > 128) {  // (fewer blocks than SMs need no look at what is resident)
-    static const int resident = resident_blocks(kernel, kBlock, 0);
+    static ByDevice known;
+    const int resident = resident_blocks(kernel, kBlock, 0, known);
     if (grid > resident) grid = resident;
   }
   return launch_after(kernel, grid, dim3(kBlock), 0, st, a);
@@ -250,7 +251,8 @@ struct Odd {
       if (err != cudaSuccess) return err;
       int grid = (a.T + kRows - 1) / kRows;
       if (grid > 128) {
-        static const int resident = resident_blocks(kernel, kBlock, smem) / 8 * 8;  // (see Windows)
+        static ByDevice known;
+        const int resident = resident_blocks(kernel, kBlock, smem, known) / 8 * 8;  // (see Windows)
         if (grid > resident) grid = resident;
       }
       if (!steps_of_eight(a.T, grid * kRows)) return cudaErrorInvalidValue;

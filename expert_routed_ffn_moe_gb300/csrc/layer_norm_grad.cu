@@ -247,7 +247,8 @@ struct Backward {
       if (err != cudaSuccess) return err;
       int grid = (a.T + kRows - 1) / kRows;
       if (grid > 128) {
-        static const int resident = min(resident_blocks(kernel, kBlock, smem), kLayerNormPartials) / 8 * 8;
+        static ByDevice known;
+        const int resident = min(resident_blocks(kernel, kBlock, smem, known), kLayerNormPartials) / 8 * 8;
         if (grid > resident) grid = resident;
       }
       if (ODD && !steps_of_eight(a.T, grid * kRows)) return cudaErrorInvalidValue;

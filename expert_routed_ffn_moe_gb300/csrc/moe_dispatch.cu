@@ -459,7 +459,8 @@ struct Combine {
     const auto kernel = combine_rows_kernel<RT, YT, VEC, P, A>;
     int grid = blocks_of(a, slice_columns(VEC, P));
     if (A <= 2 && grid > 128) {
-      static const int resident = resident_blocks(kernel, kRowThreads, 0);
+      static ByDevice known;
+      const int resident = resident_blocks(kernel, kRowThreads, 0, known);
       if (grid > resident) grid = resident;
     }
     return launch_after(kernel, grid, dim3(kRowThreads), 0, st, a);
@@ -497,15 +498,13 @@ struct CombineGrad {
 }  // namespace
 
 // Prepares the sort on the current device: the most CTAs of a cluster there, 16 (more than every device promises a cluster)
-// or 8.  0 on an error.
-static int prepare_sort() {
+// or 8.
+static cudaError_t prepare_sort(int* ranks) {
   constexpr size_t most = (size_t)(kSortWarps + 2) * kMaxSortExperts * 4;  // (parts: 1024 sums at most)
-  if (cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
-    return 0;
-  if (cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();
-    return 8;
-  }
+  *ranks = 8;
+  cudaError_t err = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (err == cudaSuccess) err = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(kSortCluster);
   c.blockDim = dim3(kSortThreads);
@@ -517,21 +516,14 @@ static int prepare_sort() {
   c.attrs = &at;
   c.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, sort_tokens_kernel, &c) != cudaSuccess) cudaGetLastError();
-  return n > 0 ? kSortCluster : 8;
+  err = cudaOccupancyMaxActiveClusters(&n, sort_tokens_kernel, &c);
+  if (err == cudaSuccess && n > 0) *ranks = kSortCluster;
+  return err;
 }
 
 cudaError_t launch_sort_tokens(const SortArgs& a, cudaStream_t st) {
-  static std::atomic<int> prepared[64];  // by device: prepare_sort()'s answer, 0 before
-  int dev = 0;
-  const cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  int most_ranks = dev < 64 ? prepared[dev].load(std::memory_order_acquire) : 0;
-  if (!most_ranks) {
-    most_ranks = prepare_sort();
-    if (!most_ranks) return cudaGetLastError();
-    if (dev < 64) prepared[dev].store(most_ranks, std::memory_order_release);
-  }
+  static ByDevice prepared;
+  const int most_ranks = once_per_device(prepared, prepare_sort);
   const size_t smem = (size_t)(kSortWarps + 1) * a.E * 4 + 1024 * 4;
   int ranks = 1;
   while (ranks < most_ranks && ranks * 2 * kSortThreads <= a.picks) ranks *= 2;

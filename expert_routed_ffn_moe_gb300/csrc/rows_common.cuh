@@ -2,8 +2,6 @@
 // sums over its threads, launches that overlap the kernel before.
 #pragma once
 
-#include <atomic>
-
 #include "ffn_internal.h"
 
 namespace moe {
@@ -172,14 +170,26 @@ MOE_DEV void copies_wait() {  // all but the last N groups of this thread
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Blocks that walk the rows: as many as are resident on the device's SMs.
+// Blocks that walk the rows: as many as are resident on the device's SMs (one on each where the device does not say).
+template <typename K>
+cudaError_t ask_resident(K kernel, int block, size_t smem, int* n) {
+  int dev = 0, sms = 8, per = 0;  // (a multiple of 8: every walk takes it)
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, smem);
+  *n = sms * (err == cudaSuccess && per > 0 ? per : 1);
+  return err;
+}
 template <typename K>
 int resident_blocks(K kernel, int block, size_t smem) {
-  int dev = 0, sms = 1, per = 1;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, block, smem) != cudaSuccess || per < 1) per = 1;
-  return sms * per;
+  int n = 0;
+  if (ask_resident(kernel, block, smem, &n) != cudaSuccess) cudaGetLastError();
+  return n;
+}
+// The same, asked once for each device; `known` is one for each kernel, block and smem.
+template <typename K>
+int resident_blocks(K kernel, int block, size_t smem, ByDevice& known) {
+  return once_per_device(known, [&](int* n) { return ask_resident(kernel, block, smem, n); });
 }
 
 // Sets a kernel's limit on shared memory once for each device (`done`: the devices that have it).
