@@ -466,9 +466,10 @@ int moe_sort_tokens(const int32_t* idx, int T, int top_k, int n_experts, int32_t
  * slot [T, top_k] int32 as moe_sort_tokens leaves it.  Here and below a slot
  * outside 0 .. n_rows - 1 stands for a dropped pick, rows that no slot names are
  * left as they were, no two picks may have the same slot, and dtypes are MOE_F32
- * or MOE_BF16, of tokens and rows each their own.  Any d; top_k is at most 32, T *
- * top_k and T * ceil(d / 256) at most 2^30 (MOE_ERR_UNSUPPORTED beyond).  The
- * gradient with respect to x is moe_combine of the rows' gradients without w. */
+ * or MOE_BF16, of tokens and rows each their own.  d is any width up to 2^24,
+ * top_k at most 32, T * top_k and T * ceil(d / 256) at most 2^30
+ * (MOE_ERR_UNSUPPORTED beyond).  The gradient with respect to x is moe_combine of
+ * the rows' gradients without w. */
 int moe_dispatch(const void* x, int x_dtype, const int32_t* slot, int T, int top_k, int d, void* rows, int rows_dtype,
                  int n_rows, void* stream);
 
@@ -489,16 +490,17 @@ int moe_combine_backward(const void* dy, int y_dtype, const void* rows, int rows
                          const float* w, int T, int top_k, int d, void* drows, float* dw, void* stream);
 
 typedef struct moe_linear_config {
-  int in_features;     /* columns of x and of the weight; a multiple of 8 */
-  int out_features;    /* rows of the weight, columns of y; a multiple of 8 */
-  int max_tokens;      /* largest T a call will use (the workspace is sized for it) */
+  int in_features;     /* columns of x and of the weight; a multiple of 8, at most 2^24 */
+  int out_features;    /* rows of the weight, columns of y; a multiple of 8, at most 2^24 */
+  int max_tokens;      /* largest T a call will use (the workspace is sized for it), at most 2^28 */
   int activation;      /* MOE_ACT_*, MOE_ACT_NONE among them */
   int training;        /* 1: calls of moe_linear_backward are allowed; 0: forward only */
 } moe_linear_config;
 
 typedef struct moe_linear moe_linear;
 
-/* As moe_ffn_init, for a moe_linear context. */
+/* As moe_ffn_init, for a moe_linear context; MOE_ERR_UNSUPPORTED for sizes past
+ * these limits. */
 int moe_linear_init(const moe_linear_config* cfg, moe_linear** out);
 
 /* pre = x weight^T + bias, y = act(pre) + residual.  x [T, in], weight [out, in]
