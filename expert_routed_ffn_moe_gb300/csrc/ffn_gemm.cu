@@ -642,7 +642,9 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
     if constexpr (kStaged && EPI == kEpiStore) {
       // 64 columns at a time go through the warp's place, as bf16, to leave as 128 bytes of a row.  Against 32 bytes of
       // each of a warp's rows, a backward call (us): 41 tokens, 1256 to 11376 28.6 for 31.8; T = 387, 1976 to 7472 49 for
-      // 53; T = 512, 4096 to 4096 33.9 for 35.5; T = 4096, 4096 to 16384 (long reductions) 640-665 for 640-650.
+      // 53; T = 512, 4096 to 4096 33.9 for 35.5; T = 4096, 4096 to 16384 (long reductions) 640-665 for 640-650.  The gated block's
+      // products: d = 4096, I = 16384, backward T = 16 147 for 174, T = 501 295 for 307, T = 4096 2050 for 2100, forward T = 512
+      // 131 for 139; d = I = 2048, backward T = 501 39.7 for 42.3.
       uint4* const place = reinterpret_cast<uint4*>(scales + ew * kPlaceBytes);
       const int to = lane * 8 + (lane & 7);  // piece e of row `lane` at to ^ e
       const int r0 = lane >> 3, from = r0 * 8 + ((lane & 7) ^ r0);  // a thread's rows are r0 + 4 i: from + 32 i, odd i's ^ 4
@@ -892,7 +894,7 @@ __global__ void __launch_bounds__(threads_of(EPI, MX, SPLIT), 1)
       }
     } else {
       // This warp's share of a pair's columns: W from a0 and W from b0 (gate/up: gate and up columns of W neurons).
-      // (SPLIT == 3, linear only: the 16 chunks of 16 columns go two or three to each of the six.)
+      // (SPLIT == 3, of linear and its gradients: the 16 chunks of 16 columns go two or three to each of the six.)
       constexpr int W = SPLIT == 3 ? 24 : kBN / 4 / SPLIT, kSendBytes = 2 * W * 32 * 4;
       static_assert(SPLIT != 3 || EPI != kEpiGateUp, "columns of one range per warp");
       auto chunk0 = [](int o) { return o * 16 / 6; };

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemv_kernel(const __grid_c
   bool ok = true;
   if (a.ctl.stall) ok = mbar_wait(&never, 0, a.ctl);  // test hook: nothing arrives there
 
-  // The copies of the next step: eight rows' 256 columns, as far as there are any.
+  // The copies of the next step: eight rows' 512 columns, as far as there are any.
   int ahead_chunk = 0, ahead_seg = 0, ahead_slot = 0, issued = 0;
   auto issue = [&]() {
     if (ahead_chunk >= chunks) return;

@@ -3,12 +3,17 @@
 //   dpre = dy act'(pre), rounded to bf16 for the products;  dbias = the sum of
 //   its rows, before that rounding
 //
+// The rounding is the products' price: the tensor cores take both operands in bf16, and
+// dpre in two parts would double them.  It is off by 2^-8 of a term at most, each term's
+// by itself: dx and dweight come to 0.0023 of their size (root mean square) from the
+// definition, where their own rounding alone leaves 0.0017.
+//
 // Bound by memory where there is no activation; its derivative takes as long (two
 // special functions and a dozen operations a value, done for two values at once where
 // there is an instruction for that).  dy and pre are read once, dpre written once.  A
-// cluster of up to 8 CTAs has 64 columns (a row of 128 bytes of bf16), its CTAs' threads every
-// 256th row; the sums meet in shared memory and then in the cluster's first CTA,
-// in a fixed order.
+// cluster of up to 8 CTAs has 64 columns (a row of 128 bytes of bf16), a thread of it one
+// of each 32 rows per CTA (with 8 CTAs every 256th row, with one every 32nd); the sums meet
+// in shared memory and then in the cluster's first CTA, in a fixed order.
 #include "ops_internal.h"
 #include "rows_common.cuh"
 

@@ -10,8 +10,9 @@
 //              rows[slot[t, j]]
 //
 // All but the sort are bound by memory.  Each works from the tokens' side: a token's
-// row is read or written once, its k sorted rows once each, and a sum over the picks
-// runs in their order, with no atomics.  A slot outside 0 .. n_rows - 1 is taken as
+// row is read or written once (dy of backward once for every 2, 4 or 8 picks, from L2 but
+// for the first time), its k sorted rows once each, and a sum over the picks runs in
+// their order, with no atomics.  A slot outside 0 .. n_rows - 1 is taken as
 // dropped, so no access leaves the rows.
 #include "ops_internal.h"
 #include "rows_common.cuh"

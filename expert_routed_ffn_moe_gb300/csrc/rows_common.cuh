@@ -117,6 +117,8 @@ MOE_DEV float2 act_exponent2(float2 g, float2 g2) {
 // reciprocal for both values, 1 / (a b) times b and a, as the special functions are what a tile's epilogue takes longest for.
 // A value's last places thus follow its neighbour, and where 2^e vanishes the result is 1 to 2^-22, not exactly: one minus
 // it is `rest`, 2^e / (1 + 2^e), which is 0 there, and never a difference (a gradient multiplies it by g).
+// (The form for one value, logistic(), which few tokens' kernels use, ends at e^-80: act(g) for silu below -42 or gelu
+// below -7.5, at most 4e-17 in size, is 0 or not by the number of tokens.)
 MOE_DEV float2 logistic2(float2 e, float2& rest) {
   constexpr float kFar = 60.f;
   const float2 t = make_float2(exp2_fast(fminf(e.x, kFar)), exp2_fast(fminf(e.y, kFar))), d = add2(t, both(1.f));
